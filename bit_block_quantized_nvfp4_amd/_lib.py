@@ -25,6 +25,12 @@ MOE_OP_EXPERT_FFN = 2
 MOE_OP_EXPERT_FFN_COMBINE = 3
 MOE_OP_LAYER = 4
 MOE_NOALLOC_WS_BYTES = 32 << 20
+MOE_DT_BF16 = 0
+MOE_DT_F16 = 1
+MOE_DT_F32 = 2
+MOE_GATE_NONE = 0
+MOE_GATE_TOKEN = 1
+MOE_GATE_ELEMENT = 2
 
 
 class MoeNvfp4Weights(ctypes.Structure):
@@ -52,6 +58,28 @@ class MoeNvfp4Router(ctypes.Structure):
     ]
 
 
+class MoeFp8Matrix(ctypes.Structure):
+    _fields_ = [
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("N", ctypes.c_int32),
+        ("K", ctypes.c_int32),
+    ]
+
+
+class MoeFp8Weights(ctypes.Structure):
+    _fields_ = [
+        ("gu_codes", ctypes.c_void_p),
+        ("gu_scales", ctypes.c_void_p),
+        ("dn_codes", ctypes.c_void_p),
+        ("dn_scales", ctypes.c_void_p),
+        ("E", ctypes.c_int32),
+        ("H", ctypes.c_int32),
+        ("I", ctypes.c_int32),
+        ("has_shared", ctypes.c_int32),
+    ]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"moe_nvfp4 status {status}: {msg}")
@@ -63,6 +91,7 @@ _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_F = ctypes.c_float
 
 _SIGS = {
     "moe_init": (_I, []),
@@ -81,6 +110,21 @@ _SIGS = {
     "moe_layer": (_I, [ctypes.POINTER(MoeNvfp4Weights), _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P,
                        _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_router_topk": (_I, [ctypes.POINTER(MoeNvfp4Router), _P, _I, _I, _P, _P, _P, _P, _P]),
+    "moe_dispatch": (_I, [_P, _P, _I, _I, _I, _I, _I, _P, _P]),
+    "moe_dispatch_grad": (_I, [_P, _P, _I, _I, _I, _I, _I, _P, _P]),
+    "moe_combine_typed": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P]),
+    "moe_combine_grad": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P]),
+    "moe_route_topk_grad": (_I, [_P, _P, _P, _I, _I, _I, _P, _P]),
+    "moe_block_norm": (_I, [_P, _P, _P, _I, _P, _P, _F, _F, _F, _I, _I, _I, _P, _P, _P, _P, _P]),
+    "moe_block_norm_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "moe_block_norm_grad": (_I, [_P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _F, _F, _I, _I, _I, _P,
+                                 _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_fp8_quant": (_I, [_P, _I, _I, _I, _P, _P, _P]),
+    "moe_fp8_linear_workspace_bytes": (_SZ, [_I, _I]),
+    "moe_fp8_linear": (_I, [ctypes.POINTER(MoeFp8Matrix), _P, _I, _I, _P, _P, _SZ, _P]),
+    "moe_fp8_expert_ffn_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "moe_fp8_expert_ffn": (_I, [ctypes.POINTER(MoeFp8Weights), _P, _I, _I, _P, _P, _P, _P, _P,
+                                _SZ, _P]),
     "moe_timing_enable": (_I, [_I]),
     "moe_timing_reset": (_I, []),
     "moe_timing_read": (_I, [ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(_I),

@@ -88,6 +88,10 @@ int ensure_init() {
   moe::register_permute_kernels(ks);
   moe::register_combine_kernels(ks);
   moe::register_ffn_kernels(ks);
+  moe::register_sort_kernels(ks);
+  moe::register_block_norm_kernels(ks);
+  moe::register_fp8_stream_kernels(ks);
+  moe::register_fp8_tile_kernels(ks);
   for (const void* k : ks) {
     hipFuncAttributes attr;
     e = hipFuncGetAttributes(&attr, k);
@@ -118,6 +122,26 @@ bool sizes_ok_common(int T, int E, int K) {
   return T >= 1 && E >= 1 && E <= 1024 && K >= 1 && K <= 32 && K <= E &&
          (long long)T * K <= (1LL << 30) && (long long)T * E <= (1LL << 40);
 }
+
+bool dtype_ok(int dt) { return dt >= MOE_DT_BF16 && dt <= MOE_DT_F32; }
+
+template <typename... P>
+bool aligned16(const P*... p) {
+  return ((((uintptr_t)p) & 15) | ...) == 0;
+}
+
+// Sizes of the sort entry points (each block of a grid covers 4 KB of a row
+// at most, so T * H bounds the grid).
+int sort_sizes(const char* who, int T, int K, int H, int has_shared, int dtype) {
+  if (!dtype_ok(dtype)) return fail(MOE_EUNSUPPORTED, "%s: unknown dtype %d", who, dtype);
+  if (T < 1 || K < 1 || K > 32 || H < 8 || H > 65536 || H % 8 != 0 ||
+      (has_shared != 0 && has_shared != 1) || (long long)T * K > (1LL << 30) ||
+      (long long)T * H > (1LL << 40))
+    return fail(MOE_EINVAL, "%s: need T >= 1, 1 <= K <= 32, H a multiple of 8 in [8, 65536], has_shared in {0,1} (T=%d K=%d H=%d)", who, T, K, H);
+  return MOE_OK;
+}
+
+int launched(hipError_t e, const char* what) { return e == hipSuccess ? ok() : hip_fail(e, what); }
 
 }  // namespace
 
@@ -381,6 +405,238 @@ int moe_router_topk(const moe_nvfp4_router* R, const uint16_t* x, int T, int K, 
   hipError_t e = moe::launch_router_topk(*R, x, T, K, ids, w, logits, R->has_gate ? gate : nullptr,
                                          (hipStream_t)stream);
   return e == hipSuccess ? ok() : hip_fail(e, "moe_router_topk launch");
+}
+
+int moe_dispatch(const void* x, const int32_t* slot_pos, int T, int K, int H, int has_shared,
+                 int dtype, void* xs, void* stream) {
+  if (!x || !slot_pos || !xs) return fail(MOE_EINVAL, "moe_dispatch: null pointer");
+  int rc = sort_sizes("moe_dispatch", T, K, H, has_shared, dtype);
+  if (rc != MOE_OK) return rc;
+  if (!aligned16((const char*)x, (const char*)xs))
+    return fail(MOE_EINVAL, "moe_dispatch: rows must be aligned to 16 bytes");
+  rc = ensure_init();
+  if (rc != MOE_OK) return rc;
+  return launched(moe::launch_dispatch(x, slot_pos, T, K, H, has_shared, dtype, xs, (hipStream_t)stream),
+                  "moe_dispatch launch");
+}
+
+int moe_dispatch_grad(const void* dxs, const int32_t* slot_pos, int T, int K, int H,
+                      int has_shared, int dtype, void* dx, void* stream) {
+  if (!dxs || !slot_pos || !dx) return fail(MOE_EINVAL, "moe_dispatch_grad: null pointer");
+  int rc = sort_sizes("moe_dispatch_grad", T, K, H, has_shared, dtype);
+  if (rc != MOE_OK) return rc;
+  if (!aligned16((const char*)dxs, (const char*)dx))
+    return fail(MOE_EINVAL, "moe_dispatch_grad: rows must be aligned to 16 bytes");
+  rc = ensure_init();
+  if (rc != MOE_OK) return rc;
+  return launched(moe::launch_slot_sum(dxs, nullptr, slot_pos, nullptr, T, K, H, has_shared, dtype,
+                                       dx, (hipStream_t)stream),
+                  "moe_dispatch_grad launch");
+}
+
+int moe_combine_typed(const void* y_slots, const float* w, const int32_t* slot_pos,
+                      const float* gate, int T, int K, int H, int has_shared, int dtype, void* out,
+                      void* stream) {
+  if (!y_slots || !w || !slot_pos || !out) return fail(MOE_EINVAL, "moe_combine_typed: null pointer");
+  int rc = sort_sizes("moe_combine_typed", T, K, H, has_shared, dtype);
+  if (rc != MOE_OK) return rc;
+  if (gate && !has_shared)
+    return fail(MOE_EINVAL, "moe_combine_typed: a shared-expert gate needs has_shared");
+  if (!aligned16((const char*)y_slots, (const char*)out))
+    return fail(MOE_EINVAL, "moe_combine_typed: rows must be aligned to 16 bytes");
+  rc = ensure_init();
+  if (rc != MOE_OK) return rc;
+  hipStream_t s = (hipStream_t)stream;
+  return launched(dtype == MOE_DT_BF16
+                      ? moe::launch_combine((const uint16_t*)y_slots, w, slot_pos, gate, T, K, H,
+                                            has_shared, (uint16_t*)out, s)
+                      : moe::launch_slot_sum(y_slots, w, slot_pos, gate, T, K, H, has_shared,
+                                             dtype, out, s),
+                  "moe_combine_typed launch");
+}
+
+int moe_combine_grad(const void* dout, const void* y_slots, const float* w,
+                     const int32_t* slot_pos, const float* gate, int T, int K, int H,
+                     int has_shared, int dtype, void* dy_slots, float* dw, float* dgate,
+                     void* stream) {
+  if (!dout || !y_slots || !w || !slot_pos || !dy_slots || !dw)
+    return fail(MOE_EINVAL, "moe_combine_grad: null pointer");
+  int rc = sort_sizes("moe_combine_grad", T, K, H, has_shared, dtype);
+  if (rc != MOE_OK) return rc;
+  if (gate && !has_shared)
+    return fail(MOE_EINVAL, "moe_combine_grad: a shared-expert gate needs has_shared");
+  if ((gate != nullptr) != (dgate != nullptr))
+    return fail(MOE_EINVAL, "moe_combine_grad: gate and dgate are given together");
+  if (!aligned16((const char*)dout, (const char*)y_slots, (const char*)dy_slots))
+    return fail(MOE_EINVAL, "moe_combine_grad: rows must be aligned to 16 bytes");
+  rc = ensure_init();
+  if (rc != MOE_OK) return rc;
+  return launched(moe::launch_combine_grad(dout, y_slots, w, slot_pos, gate, T, K, H, has_shared,
+                                           dtype, dy_slots, dw, dgate, (hipStream_t)stream),
+                  "moe_combine_grad launch");
+}
+
+int moe_route_topk_grad(const int32_t* ids, const float* w, const float* dw, int T, int E, int K,
+                        float* dlogits, void* stream) {
+  if (!ids || !w || !dw || !dlogits) return fail(MOE_EINVAL, "moe_route_topk_grad: null pointer");
+  if (!sizes_ok_common(T, E, K))
+    return fail(MOE_EINVAL, "moe_route_topk_grad: need T >= 1, 1 <= K <= min(E, 32), E <= 1024 (T=%d E=%d K=%d)", T, E, K);
+  int rc = ensure_init();
+  if (rc != MOE_OK) return rc;
+  return launched(moe::launch_topk_grad(ids, w, dw, T, E, K, dlogits, (hipStream_t)stream),
+                  "moe_route_topk_grad launch");
+}
+
+static int norm_sizes(const char* who, int T, int H, int dtype, int gate_kind) {
+  if (!dtype_ok(dtype)) return fail(MOE_EUNSUPPORTED, "%s: unknown dtype %d", who, dtype);
+  if (gate_kind < MOE_GATE_NONE || gate_kind > MOE_GATE_ELEMENT)
+    return fail(MOE_EUNSUPPORTED, "%s: unknown gate_kind %d", who, gate_kind);
+  if (T < 1 || T > (1 << 30) || H < 8 || H > 8192 || H % 8 != 0)
+    return fail(MOE_EINVAL, "%s: need 1 <= T <= 2^30 and H a multiple of 8 in [8, 8192] (T=%d H=%d)", who, T, H);
+  return MOE_OK;
+}
+
+int moe_block_norm(const void* residual, const void* y, const void* gate, int gate_kind,
+                   const float* w_post, const float* w_pre, float res_scale, float out_scale,
+                   float eps, int T, int H, int dtype, void* r_out, void* n_out, float* rstd_post,
+                   float* rstd_pre, void* stream) {
+  if (!residual) return fail(MOE_EINVAL, "moe_block_norm: null pointer");
+  int rc = norm_sizes("moe_block_norm", T, H, dtype, gate_kind);
+  if (rc != MOE_OK) return rc;
+  if ((gate_kind == MOE_GATE_NONE) != (gate == nullptr))
+    return fail(MOE_EINVAL, "moe_block_norm: gate and gate_kind do not agree");
+  if (!y && (gate || w_post || r_out || !w_pre))
+    return fail(MOE_EINVAL, "moe_block_norm: without y only w_pre and n_out are given");
+  if (y && !r_out) return fail(MOE_EINVAL, "moe_block_norm: r_out is missing");
+  if ((w_pre != nullptr) != (n_out != nullptr))
+    return fail(MOE_EINVAL, "moe_block_norm: w_pre and n_out are given together");
+  if ((rstd_post && !w_post) || (rstd_pre && !w_pre))
+    return fail(MOE_EINVAL, "moe_block_norm: statistics of a norm that is not computed");
+  if (!(eps >= 0.f)) return fail(MOE_EINVAL, "moe_block_norm: eps must be >= 0");
+  if (!aligned16((const char*)residual, (const char*)y, (const char*)w_post, (const char*)w_pre,
+                 (const char*)r_out, (const char*)n_out) ||
+      (gate_kind == MOE_GATE_ELEMENT && !aligned16((const char*)gate)))
+    return fail(MOE_EINVAL, "moe_block_norm: rows and weights must be aligned to 16 bytes");
+  rc = ensure_init();
+  if (rc != MOE_OK) return rc;
+  return launched(moe::launch_block_norm(residual, y, gate, gate_kind, w_post, w_pre, res_scale,
+                                         out_scale, eps, T, H, dtype, r_out, n_out, rstd_post,
+                                         rstd_pre, (hipStream_t)stream),
+                  "moe_block_norm launch");
+}
+
+size_t moe_block_norm_workspace_bytes(int T, int H, int dtype) {
+  if (!dtype_ok(dtype) || T < 1 || T > (1 << 30) || H < 8 || H > 8192 || H % 8 != 0) return 0;
+  return moe::block_norm_workspace_bytes(T, H, dtype);
+}
+
+int moe_block_norm_grad(const void* dr, const void* dn, const void* r_out, const void* y,
+                        const void* gate, int gate_kind, const float* w_post, const float* w_pre,
+                        const float* rstd_post, const float* rstd_pre, float res_scale,
+                        float out_scale, int T, int H, int dtype, void* dres, void* dy,
+                        void* dgate, float* dw_post, float* dw_pre, void* ws, size_t ws_bytes,
+                        void* stream) {
+  if (!dres || (!dr && !dn)) return fail(MOE_EINVAL, "moe_block_norm_grad: null pointer");
+  int rc = norm_sizes("moe_block_norm_grad", T, H, dtype, gate_kind);
+  if (rc != MOE_OK) return rc;
+  if ((gate_kind == MOE_GATE_NONE) != (gate == nullptr) || (gate != nullptr) != (dgate != nullptr))
+    return fail(MOE_EINVAL, "moe_block_norm_grad: gate, gate_kind and dgate do not agree");
+  if (!y && (gate || w_post || dy))
+    return fail(MOE_EINVAL, "moe_block_norm_grad: without y there is no gate, w_post or dy");
+  if (y && !dy) return fail(MOE_EINVAL, "moe_block_norm_grad: dy is missing");
+  if (w_pre ? !(dn && r_out && rstd_pre && dw_pre) : (dn || dw_pre))
+    return fail(MOE_EINVAL, "moe_block_norm_grad: w_pre, dn, r_out, rstd_pre and dw_pre are given together");
+  if (w_post ? !(rstd_post && dw_post) : dw_post != nullptr)
+    return fail(MOE_EINVAL, "moe_block_norm_grad: w_post, rstd_post and dw_post are given together");
+  if (!aligned16((const char*)dr, (const char*)dn, (const char*)r_out, (const char*)y,
+                 (const char*)w_post, (const char*)w_pre, (const char*)dres, (const char*)dy,
+                 (const char*)ws) ||
+      (gate_kind == MOE_GATE_ELEMENT && !aligned16((const char*)gate, (const char*)dgate)))
+    return fail(MOE_EINVAL, "moe_block_norm_grad: rows, weights and workspace must be aligned to 16 bytes");
+  const size_t need = moe::block_norm_workspace_bytes(T, H, dtype);
+  if (!ws || ws_bytes < need)
+    return fail(MOE_EWORKSPACE, "moe_block_norm_grad: workspace of %zu bytes needed, %zu given", need, ws_bytes);
+  rc = ensure_init();
+  if (rc != MOE_OK) return rc;
+  return launched(moe::launch_block_norm_grad(dr, dn, r_out, y, gate, gate_kind, w_post, w_pre,
+                                              rstd_post, rstd_pre, res_scale, out_scale, T, H,
+                                              dtype, dres, dy, dgate, dw_post, dw_pre, ws,
+                                              (hipStream_t)stream),
+                  "moe_block_norm_grad launch");
+}
+
+static bool fp8_k_ok(int T, int K) {
+  return T >= 1 && T <= (1 << 30) && K >= 16 && K <= 65536 && K % 16 == 0;
+}
+
+int moe_fp8_quant(const void* x, int T, int K, int dtype, uint8_t* codes, float* scales,
+                  void* stream) {
+  if (!x || !codes || !scales) return fail(MOE_EINVAL, "moe_fp8_quant: null pointer");
+  if (!dtype_ok(dtype)) return fail(MOE_EUNSUPPORTED, "moe_fp8_quant: unknown dtype %d", dtype);
+  if (!fp8_k_ok(T, K))
+    return fail(MOE_EINVAL, "moe_fp8_quant: need 1 <= T <= 2^30 and K a multiple of 16 in [16, 65536] (T=%d K=%d)", T, K);
+  if (!aligned16((const char*)x, codes))
+    return fail(MOE_EINVAL, "moe_fp8_quant: rows must be aligned to 16 bytes");
+  int rc = ensure_init();
+  if (rc != MOE_OK) return rc;
+  return launched(moe::launch_fp8_quant(x, T, K, dtype, K, codes, scales, (hipStream_t)stream),
+                  "moe_fp8_quant launch");
+}
+
+size_t moe_fp8_linear_workspace_bytes(int T, int K) {
+  return fp8_k_ok(T, K) ? moe::fp8_linear_workspace_bytes(T, K) : 0;
+}
+
+int moe_fp8_linear(const moe_fp8_matrix* M, const void* x, int T, int dtype, void* out, void* ws,
+                   size_t ws_bytes, void* stream) {
+  if (!M || !x || !out) return fail(MOE_EINVAL, "moe_fp8_linear: null pointer");
+  if (!M->codes || !M->scales) return fail(MOE_EINVAL, "moe_fp8_linear: null weight pointer");
+  if (!dtype_ok(dtype)) return fail(MOE_EUNSUPPORTED, "moe_fp8_linear: unknown dtype %d", dtype);
+  if (!fp8_k_ok(T, M->K) || M->N < 8 || M->N > 65536 || M->N % 8 != 0)
+    return fail(MOE_EINVAL, "moe_fp8_linear: need 1 <= T <= 2^30, K a multiple of 16 in [16, 65536] and N a multiple of 8 in [8, 65536] (T=%d N=%d K=%d)", T, M->N, M->K);
+  if (!aligned16((const char*)x, (const char*)out, M->codes, (const char*)ws))
+    return fail(MOE_EINVAL, "moe_fp8_linear: codes, rows and workspace must be aligned to 16 bytes");
+  const size_t need = moe::fp8_linear_workspace_bytes(T, M->K);
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(MOE_EWORKSPACE, "moe_fp8_linear: workspace of %zu bytes needed, %zu given", need, ws_bytes);
+  int rc = ensure_init();
+  if (rc != MOE_OK) return rc;
+  return launched(moe::launch_fp8_linear(*M, x, T, dtype, out, ws, (hipStream_t)stream),
+                  "moe_fp8_linear launch");
+}
+
+static bool fp8_bank_ok(int H, int I) {
+  return H >= 128 && H <= 8192 && H % 128 == 0 && I >= 128 && I <= 8192 && I % 128 == 0;
+}
+
+size_t moe_fp8_expert_ffn_workspace_bytes(int T, int K, int H, int I, int has_shared) {
+  if (T < 1 || K < 1 || K > 32 || (long long)T * K > (1LL << 30) || !fp8_bank_ok(H, I) ||
+      (has_shared != 0 && has_shared != 1))
+    return 0;
+  return moe::fp8_expert_ffn_workspace_bytes(T, K, H, I, has_shared);
+}
+
+int moe_fp8_expert_ffn(const moe_fp8_weights* W, const uint16_t* x, int T, int K,
+                       const int32_t* offsets, const int32_t* sorted_slot, const int32_t* groups,
+                       uint16_t* y_slots, void* ws, size_t ws_bytes, void* stream) {
+  if (!W || !x || !offsets || !sorted_slot || !groups || !y_slots)
+    return fail(MOE_EINVAL, "moe_fp8_expert_ffn: null pointer");
+  if (!W->gu_codes || !W->gu_scales || !W->dn_codes || !W->dn_scales)
+    return fail(MOE_EINVAL, "moe_fp8_expert_ffn: null weight pointer");
+  if (!sizes_ok_common(T, W->E, K) || (W->has_shared != 0 && W->has_shared != 1))
+    return fail(MOE_EINVAL, "moe_fp8_expert_ffn: need T >= 1, 1 <= K <= min(E, 32), E <= 1024, has_shared in {0,1}");
+  if (!fp8_bank_ok(W->H, W->I))
+    return fail(MOE_EINVAL, "moe_fp8_expert_ffn: need H and I multiples of 128 in [128, 8192] (H=%d I=%d)", W->H, W->I);
+  if (!aligned16((const char*)x, (const char*)y_slots, W->gu_codes, W->dn_codes, (const char*)ws))
+    return fail(MOE_EINVAL, "moe_fp8_expert_ffn: codes, rows and workspace must be aligned to 16 bytes");
+  const size_t need = moe::fp8_expert_ffn_workspace_bytes(T, K, W->H, W->I, W->has_shared);
+  if (!ws || ws_bytes < need)
+    return fail(MOE_EWORKSPACE, "moe_fp8_expert_ffn: workspace of %zu bytes needed, %zu given", need, ws_bytes);
+  int rc = ensure_init();
+  if (rc != MOE_OK) return rc;
+  return launched(moe::launch_fp8_expert_ffn(*W, x, T, K, offsets, sorted_slot, groups, y_slots, ws,
+                                             (hipStream_t)stream),
+                  "moe_fp8_expert_ffn launch");
 }
 
 int moe_timing_enable(int on) {

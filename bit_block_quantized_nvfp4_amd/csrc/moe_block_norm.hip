@@ -1,0 +1,476 @@
+// The norms before and after a block, fused with the block's gate and the
+// residual scale, and the gradients.  Per row t, with c = 1, sigmoid(g_t) or
+// sigmoid(g_th), rms statistics in f32:
+//
+//   u  = y rstd(y) w_post          (u = y without w_post)
+//   r' = a r + b c u               rounded to the rows' type: what is stored
+//   n  = r' rstd(r') w_pre         of the stored r'
+//
+// and backward, with xh = r' rstd(r'), yh = y rstd(y), mean over the H columns:
+//
+//   D  = dr' + rstd(r') (dn w_pre - xh mean(dn w_pre xh))
+//   dr = a D,  du = b c D
+//   dg = b c (1 - c) D u           (summed over the row for a token's gate)
+//   dy = rstd(y) (du w_post - yh mean(du w_post yh))
+//   dw_pre = sum_t dn xh,  dw_post = sum_t du yh
+//
+// Bound by memory: each row of each tensor is read and written once, a row's
+// values stay in registers between the statistics and their use.
+#include <math.h>
+
+#include "moe_internal.hpp"
+#include "moe_vec.hpp"
+
+namespace moe {
+
+// Sum over the threads of a row: one wave, or the W waves of the block (the
+// waves' sums join in wave order).  slot: LDS of this reduction alone.
+template <int W>
+__device__ __forceinline__ float row_sum(float v, float* slot) {
+  v = wave_sum_dpp(v);
+  if (W == 1) return v;
+  if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float r = 0.f;
+#pragma unroll
+  for (int i = 0; i < W; ++i) r += slot[i];
+  return r;
+}
+
+// N f32 weights at column c * N.
+template <int N>
+__device__ __forceinline__ void load_w(const float* __restrict__ w, int c, float (&f)[N]) {
+  const f32x4* p = (const f32x4*)w + (size_t)c * (N / 4);
+#pragma unroll
+  for (int q = 0; q < N / 4; ++q) {
+    const f32x4 v = p[q];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[4 * q + j] = v[j];
+  }
+}
+
+__device__ __forceinline__ float sigmoid_f32(float g) { return 1.0f / (1.0f + expf(-g)); }
+
+struct NormFwd {
+  const u32x4* res;
+  const u32x4* y;       // NULL: r' = res, not written
+  const void* gate;     // NULL, f32 [T], or rows of the element type
+  const float* w_post;  // NULL: no norm after
+  const float* w_pre;   // NULL: no norm before the next block
+  u32x4* r_out;
+  u32x4* n_out;
+  float* rstd_post;
+  float* rstd_pre;
+  float res_scale, out_scale, eps;
+  int T, H, cpr, gate_kind;
+};
+
+// W == 1: a wave per row, four rows to a block; else the block's W waves share
+// one row.
+template <int DT, int NC, int W>
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_block_norm(NormFwd a) {
+  constexpr int N = Chunk<DT>::N;
+  constexpr int TPR = 64 * W;
+  __shared__ float red[2][W];
+  const int lane = W == 1 ? (threadIdx.x & 63) : threadIdx.x;
+  const int t = W == 1 ? blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6)
+                       : blockIdx.x;
+  if (t >= a.T) return;
+  const size_t base = (size_t)t * a.cpr;
+  float v[NC][N];
+  u32x4 rr[NC], yy[NC], gg[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = lane + TPR * i;
+    rr[i] = yy[i] = gg[i] = u32x4{0u, 0u, 0u, 0u};
+    if (c < a.cpr) {
+      if (a.y) yy[i] = a.y[base + c];
+      rr[i] = a.res[base + c];
+      if (a.gate_kind == MOE_GATE_ELEMENT) gg[i] = ((const u32x4*)a.gate)[base + c];
+    }
+  }
+  const float inv_h = 1.0f / (float)a.H;
+  if (a.y) {
+    float rstd = 1.f;
+    if (a.w_post) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        Chunk<DT>::unpack(yy[i], v[i]);
+#pragma unroll
+        for (int j = 0; j < N; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+      }
+      rstd = 1.0f / sqrtf(row_sum<W>(ss, red[0]) * inv_h + a.eps);
+      if (a.rstd_post && lane == 0) a.rstd_post[t] = rstd;
+    }
+    float scale = a.out_scale;
+    if (a.gate_kind == MOE_GATE_TOKEN) scale *= sigmoid_f32(((const float*)a.gate)[t]);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = lane + TPR * i;
+      if (c < a.cpr) {
+        float r[N], g[N], wp[N];
+        Chunk<DT>::unpack(yy[i], v[i]);
+        Chunk<DT>::unpack(rr[i], r);
+        if (a.w_post) {
+          load_w<N>(a.w_post, c, wp);
+#pragma unroll
+          for (int j = 0; j < N; ++j) v[i][j] = v[i][j] * rstd * wp[j];
+        }
+        if (a.gate_kind == MOE_GATE_ELEMENT) {
+          Chunk<DT>::unpack(gg[i], g);
+#pragma unroll
+          for (int j = 0; j < N; ++j) v[i][j] *= sigmoid_f32(g[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[i][j] = fmaf(scale, v[i][j], a.res_scale * r[j]);
+        rr[i] = Chunk<DT>::pack(v[i]);
+        a.r_out[base + c] = rr[i];
+      }
+    }
+  }
+  if (!a.w_pre) return;
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    Chunk<DT>::unpack(rr[i], v[i]);  // as stored
+#pragma unroll
+    for (int j = 0; j < N; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+  }
+  const float rstd = 1.0f / sqrtf(row_sum<W>(ss, red[1]) * inv_h + a.eps);
+  if (a.rstd_pre && lane == 0) a.rstd_pre[t] = rstd;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = lane + TPR * i;
+    if (c < a.cpr) {
+      float wp[N];
+      load_w<N>(a.w_pre, c, wp);
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[i][j] = v[i][j] * rstd * wp[j];
+      a.n_out[base + c] = Chunk<DT>::pack(v[i]);
+    }
+  }
+}
+
+struct NormBwd {
+  const u32x4* dr;      // NULL: zero
+  const u32x4* dn;      // NULL iff no w_pre
+  const u32x4* r_out;
+  const u32x4* y;       // NULL: r' = res
+  const void* gate;
+  const float* w_post;
+  const float* w_pre;
+  const float* rstd_post;
+  const float* rstd_pre;
+  u32x4* dres;
+  u32x4* dy;
+  void* dgate;
+  float* part;          // [gridDim.x][2][H] partial sums of dw_post, dw_pre
+  float res_scale, out_scale;
+  int T, H, cpr, gate_kind;
+};
+
+// As the forward kernel, but each wave (or block) takes every P-th row and
+// keeps its share of the weight gradients in registers; at the end the block
+// writes one partial row of each.
+template <int DT, int NC, int W>
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_block_norm_grad(NormBwd a) {
+  constexpr int N = Chunk<DT>::N;
+  constexpr int TPR = 64 * W;
+  constexpr int RPB = W == 1 ? 4 : 1;  // rows in flight per block
+  __shared__ float red[2][W];
+  __shared__ f32x4 join[W == 1 ? 3 * 64 * NC * (N / 4) : 1];
+  const int lane = W == 1 ? (threadIdx.x & 63) : threadIdx.x;
+  const int wv = W == 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) : 0;
+  const float inv_h = 1.0f / (float)a.H;
+  float gw_post[NC][N], gw_pre[NC][N];
+#pragma unroll
+  for (int i = 0; i < NC; ++i)
+#pragma unroll
+    for (int j = 0; j < N; ++j) gw_post[i][j] = gw_pre[i][j] = 0.f;
+
+  for (long t = (long)blockIdx.x * RPB + wv; t < a.T; t += (long)gridDim.x * RPB) {
+    const size_t base = (size_t)t * a.cpr;
+    float D[NC][N];
+    u32x4 vr[NC], vn[NC], vx[NC], vy[NC], vg[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = lane + TPR * i;
+      vr[i] = vn[i] = vx[i] = vy[i] = vg[i] = u32x4{0u, 0u, 0u, 0u};
+      if (c < a.cpr) {
+        if (a.dr) vr[i] = a.dr[base + c];
+        if (a.w_pre) {
+          vn[i] = a.dn[base + c];
+          vx[i] = a.r_out[base + c];
+        }
+        if (a.y) vy[i] = a.y[base + c];
+        if (a.gate_kind == MOE_GATE_ELEMENT) vg[i] = ((const u32x4*)a.gate)[base + c];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) Chunk<DT>::unpack(vr[i], D[i]);
+    if (a.w_pre) {
+      const float rstd = a.rstd_pre[t];
+      float g[NC][N], xh[NC][N], s = 0.f;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int c = lane + TPR * i;
+        float wp[N];
+        Chunk<DT>::unpack(vn[i], g[i]);
+        Chunk<DT>::unpack(vx[i], xh[i]);
+        if (c < a.cpr) {
+          load_w<N>(a.w_pre, c, wp);
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            xh[i][j] *= rstd;
+            gw_pre[i][j] = fmaf(g[i][j], xh[i][j], gw_pre[i][j]);
+            g[i][j] *= wp[j];
+            s = fmaf(g[i][j], xh[i][j], s);
+          }
+        }
+      }
+      const float m = row_sum<W>(s, red[0]) * inv_h;
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int j = 0; j < N; ++j) D[i][j] = fmaf(rstd, g[i][j] - xh[i][j] * m, D[i][j]);
+    }
+    // without y the rows passed through: dr = D
+    const float rs = a.y ? a.res_scale : 1.f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = lane + TPR * i;
+      if (c < a.cpr) {
+        float o[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) o[j] = rs * D[i][j];
+        a.dres[base + c] = Chunk<DT>::pack(o);
+      }
+    }
+    if (!a.y) {
+      if (W > 1) __syncthreads();  // red[] is free again
+      continue;
+    }
+    const float rstd = a.w_post ? a.rstd_post[t] : 1.f;
+    float sg = 1.f;
+    if (a.gate_kind == MOE_GATE_TOKEN) sg = sigmoid_f32(((const float*)a.gate)[t]);
+    // D becomes b D, then du w_post = b c D w_post; s sums that times yh,
+    // which is <b c D, u>, also the token gate's gradient up to (1 - c)
+    float s = 0.f;
+    float yh[NC][N];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = lane + TPR * i;
+      Chunk<DT>::unpack(vy[i], yh[i]);
+      float wp[N], gt[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) wp[j] = 1.f;
+      if (c < a.cpr) {
+        if (a.w_post) load_w<N>(a.w_post, c, wp);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          yh[i][j] *= rstd;
+          D[i][j] *= a.out_scale;
+        }
+        if (a.gate_kind == MOE_GATE_ELEMENT) {
+          Chunk<DT>::unpack(vg[i], gt);
+          float o[N];
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            const float c1 = sigmoid_f32(gt[j]);
+            D[i][j] *= c1;
+            o[j] = D[i][j] * yh[i][j] * wp[j] * (1.f - c1);
+          }
+          ((u32x4*)a.dgate)[base + c] = Chunk<DT>::pack(o);
+        } else {
+#pragma unroll
+          for (int j = 0; j < N; ++j) D[i][j] *= sg;
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          gw_post[i][j] = fmaf(D[i][j], yh[i][j], gw_post[i][j]);
+          D[i][j] *= wp[j];
+          s = fmaf(D[i][j], yh[i][j], s);
+        }
+      }
+    }
+    float m = 0.f;
+    if (a.w_post || a.gate_kind == MOE_GATE_TOKEN) {
+      s = row_sum<W>(s, red[1]);
+      if (a.gate_kind == MOE_GATE_TOKEN && lane == 0) ((float*)a.dgate)[t] = (1.f - sg) * s;
+      if (a.w_post) m = s * inv_h;
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = lane + TPR * i;
+      if (c < a.cpr) {
+        float o[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) o[j] = rstd * (D[i][j] - yh[i][j] * m);
+        a.dy[base + c] = Chunk<DT>::pack(o);
+      }
+    }
+    if (W > 1) __syncthreads();  // red[] is free again
+  }
+
+  // the block's partial sums: the four waves of W == 1 join in wave order
+  auto put = [&](float (&gw)[NC][N], int which) {
+    constexpr int Q = N / 4;
+    if (W == 1) {
+      __syncthreads();
+      if (wv > 0) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+          for (int q = 0; q < Q; ++q)
+            join[((wv - 1) * NC * Q + i * Q + q) * 64 + lane] =
+                f32x4{gw[i][4 * q], gw[i][4 * q + 1], gw[i][4 * q + 2], gw[i][4 * q + 3]};
+      }
+      __syncthreads();
+      if (wv > 0) return;
+      for (int w2 = 0; w2 < 3; ++w2)
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            const f32x4 v = join[(w2 * NC * Q + i * Q + q) * 64 + lane];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) gw[i][4 * q + j] += v[j];
+          }
+    }
+    f32x4* dst = (f32x4*)(a.part + ((size_t)blockIdx.x * 2 + which) * a.H);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = lane + TPR * i;
+      if (c < a.cpr) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+          dst[c * Q + q] =
+              f32x4{gw[i][4 * q], gw[i][4 * q + 1], gw[i][4 * q + 2], gw[i][4 * q + 3]};
+      }
+    }
+  };
+  if (a.w_post) put(gw_post, 0);
+  if (a.w_pre) put(gw_pre, 1);
+}
+
+// dw[which][h] = sum over the P partial rows, in row order within 16 strided
+// shares, then over the shares: 16 columns x 16 shares to a block.
+__global__ __launch_bounds__(256) void k_norm_dw(const float* __restrict__ part, int P, int H,
+                                                 int first, float* __restrict__ dw_post,
+                                                 float* __restrict__ dw_pre) {
+  __shared__ float sh[16][17];
+  const int which = first + (int)blockIdx.y;
+  const int col = blockIdx.x * 16 + (threadIdx.x & 15), share = threadIdx.x >> 4;
+  float s = 0.f;
+  if (col < H)
+    for (int p = share; p < P; p += 16) s += part[((size_t)p * 2 + which) * H + col];
+  sh[share][threadIdx.x & 15] = s;
+  __syncthreads();
+  if (share == 0 && col < H) {
+    for (int q = 1; q < 16; ++q) s += sh[q][threadIdx.x];
+    (which ? dw_pre : dw_post)[col] = s;
+  }
+}
+
+// Waves to a row: one wave holds up to 256 chunks, four up to 1024, eight up
+// to 2048.  Few rows are spread over four waves each from 65 chunks on, since
+// the latency of a row counts then.
+static int norm_waves(int T, int cpr) {
+  if (cpr > 1024) return 8;
+  if (cpr > 256) return 4;
+  return (cpr > 64 && T <= 512) ? 4 : 1;
+}
+
+template <int DT, typename F>
+static void by_shape(int T, int cpr, F&& f) {
+  const int W = norm_waves(T, cpr);
+  if (W == 8) f(IntC<4>{}, IntC<8>{});
+  else if (W == 4 && cpr <= 256) f(IntC<1>{}, IntC<4>{});
+  else if (W == 4) f(IntC<4>{}, IntC<4>{});
+  else if (cpr <= 64) f(IntC<1>{}, IntC<1>{});
+  else f(IntC<4>{}, IntC<1>{});
+}
+
+void register_block_norm_kernels(std::vector<const void*>& k) {
+  auto add = [&](auto D) {
+    constexpr int DT = decltype(D)::value;
+    auto one = [&](auto NC, auto W) {
+      k.push_back((const void*)&k_block_norm<DT, decltype(NC)::value, decltype(W)::value>);
+      k.push_back((const void*)&k_block_norm_grad<DT, decltype(NC)::value, decltype(W)::value>);
+    };
+    one(IntC<1>{}, IntC<1>{});
+    one(IntC<4>{}, IntC<1>{});
+    one(IntC<1>{}, IntC<4>{});
+    one(IntC<4>{}, IntC<4>{});
+    one(IntC<4>{}, IntC<8>{});
+  };
+  for (int dt = MOE_DT_BF16; dt <= MOE_DT_F32; ++dt) by_dtype(dt, add);
+  k.push_back((const void*)&k_norm_dw);
+}
+
+hipError_t launch_block_norm(const void* res, const void* y, const void* gate, int gate_kind,
+                             const float* w_post, const float* w_pre, float res_scale,
+                             float out_scale, float eps, int T, int H, int dtype, void* r_out,
+                             void* n_out, float* rstd_post, float* rstd_pre, hipStream_t s) {
+  const int cpr = H * dtype_bytes(dtype) / 16;
+  const NormFwd a{(const u32x4*)res, (const u32x4*)y, gate,      w_post,    w_pre,
+                  (u32x4*)r_out,     (u32x4*)n_out,   rstd_post, rstd_pre,  res_scale,
+                  out_scale,         eps,             T,         H,         cpr,
+                  gate_kind};
+  by_dtype(dtype, [&](auto D) {
+    constexpr int DT = decltype(D)::value;
+    by_shape<DT>(T, cpr, [&](auto NC, auto W) {
+      constexpr int w = decltype(W)::value;
+      MOE_LAUNCH("block_norm", s, (k_block_norm<DT, decltype(NC)::value, w>),
+                 dim3(w == 1 ? (T + 3) / 4 : T), dim3(w == 1 ? 256 : 64 * w), 0, s, a);
+    });
+  });
+  return hipGetLastError();
+}
+
+// Blocks of the backward kernel, each with a partial row of the weight
+// gradients: enough to fill the chip, few enough that the partials stay small
+// beside the rows.  A function of the sizes alone, so results do not depend on
+// the device's state.
+static int norm_parts(int T, int H, int dtype) {
+  const int cpr = H * dtype_bytes(dtype) / 16;
+  const int rows = norm_waves(T, cpr) == 1 ? 4 : 1;
+  const int P = (T + rows - 1) / rows;
+  return P < 512 ? P : 512;
+}
+
+size_t block_norm_workspace_bytes(int T, int H, int dtype) {
+  return (size_t)norm_parts(T, H, dtype) * 2 * H * sizeof(float);
+}
+
+hipError_t launch_block_norm_grad(const void* dr, const void* dn, const void* r_out, const void* y,
+                                  const void* gate, int gate_kind, const float* w_post,
+                                  const float* w_pre, const float* rstd_post,
+                                  const float* rstd_pre, float res_scale, float out_scale, int T,
+                                  int H, int dtype, void* dres, void* dy, void* dgate,
+                                  float* dw_post, float* dw_pre, void* ws, hipStream_t s) {
+  const int cpr = H * dtype_bytes(dtype) / 16;
+  const int P = norm_parts(T, H, dtype);
+  const NormBwd a{(const u32x4*)dr, (const u32x4*)dn, (const u32x4*)r_out, (const u32x4*)y,
+                  gate,             w_post,           w_pre,               rstd_post,
+                  rstd_pre,         (u32x4*)dres,     (u32x4*)dy,          dgate,
+                  (float*)ws,       res_scale,        out_scale,           T,
+                  H,                cpr,              gate_kind};
+  by_dtype(dtype, [&](auto D) {
+    constexpr int DT = decltype(D)::value;
+    by_shape<DT>(T, cpr, [&](auto NC, auto W) {
+      constexpr int w = decltype(W)::value;
+      MOE_LAUNCH("block_norm_grad", s, (k_block_norm_grad<DT, decltype(NC)::value, w>), dim3(P),
+                 dim3(w == 1 ? 256 : 64 * w), 0, s, a);
+    });
+  });
+  hipError_t e = hipGetLastError();
+  const int n = (w_post ? 1 : 0) + (w_pre ? 1 : 0);
+  if (e != hipSuccess || n == 0) return e;
+  MOE_LAUNCH("block_norm_dw", s, k_norm_dw, dim3((H + 15) / 16, n), dim3(256), 0, s,
+             (const float*)ws, P, H, w_post ? 0 : 1, dw_post, dw_pre);
+  return hipGetLastError();
+}
+
+}  // namespace moe

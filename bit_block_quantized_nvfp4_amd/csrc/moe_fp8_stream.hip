@@ -1,0 +1,262 @@
+// e4m3 products of few rows (up to 16): the weights stream once from memory to
+// registers, the rows are quantised on the way, in the same launch.
+//
+//   z[r][n] = sum_b s[r][b] S[n / 128][b] sum_{k in block b} q[r][k] W[n][k]
+//
+// Bound by the weight bytes.  A wave owns RT tiles of 16 weight rows and every
+// KW-th block of 128 along K; the KW waves of a tile join through LDS in wave
+// order.  16 rows are one MFMA operand whatever their number, so one row costs
+// the same instructions as sixteen; the rows' own reads are masked off past
+// the last.  Each wave quantises the blocks it needs by itself (32 values a
+// lane): repeated per tile, but it saves a launch and its wait.
+#include <math.h>
+
+#include "moe_ffn_common.hpp"
+#include "moe_fp8.hpp"
+#include "moe_internal.hpp"
+
+namespace moe {
+
+enum { kStreamLinear = 0, kStreamGateUp = 1, kStreamDown = 2 };
+
+struct StreamArgs {
+  const uint8_t* codes;    // [N][K] (of group 0)
+  const float* scales;     // [ceil(N/128)][ceil(K/128)]
+  const void* x;           // rows of K values
+  void* out;
+  const int32_t* offsets;  // grouped modes
+  const int32_t* sorted_slot;
+  const int32_t* groups;
+  int R;                   // rows (linear)
+  int N, K, T, topk, has_shared;
+  int tiles;               // blocks along N
+};
+
+// 32 consecutive values of a row from position k0 on, zero from K on.
+template <int DT>
+__device__ __forceinline__ void load32(const void* __restrict__ row, int k0, int K,
+                                       float (&f)[32]) {
+  constexpr int N = Chunk<DT>::N;
+  const u32x4* p = (const u32x4*)row;
+  u32x4 v[32 / N];
+#pragma unroll
+  for (int i = 0; i < 32 / N; ++i) {
+    v[i] = u32x4{0u, 0u, 0u, 0u};
+    if (k0 + i * N < K) v[i] = p[k0 / N + i];
+  }
+#pragma unroll
+  for (int i = 0; i < 32 / N; ++i) {
+    float c[N];
+    Chunk<DT>::unpack(v[i], c);
+#pragma unroll
+    for (int j = 0; j < N; ++j) f[i * N + j] = c[j];
+  }
+}
+
+template <int DT, int MODE, int RT, int KW>
+__global__ __launch_bounds__(512) void k_fp8_stream(StreamArgs a) {
+  constexpr int RW = 8 / KW;            // tile groups of the block
+  constexpr bool EX = MODE == kStreamLinear && DT == MOE_DT_F32;
+  constexpr int kPad = 1;
+  __shared__ f32x4 red[8][RT][64 + kPad];
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int kw = wv % KW, rw = wv / KW;
+  const int tile = blockIdx.x % a.tiles;
+
+  const uint8_t* codes = a.codes;
+  const float* scales = a.scales;
+  const int nb = (a.K + kQB - 1) / kQB;
+  int p0 = 0, rows = a.R;
+  if (MODE != kStreamLinear) {
+    const int gi = blockIdx.x / a.tiles;
+    if (gi >= a.groups[0]) return;
+    const int g = a.groups[1 + gi];
+    p0 = a.offsets[g];
+    rows = a.offsets[g + 1] - p0;
+    const int nr = MODE == kStreamGateUp ? 2 * a.N : a.N;  // weight rows of a group
+    codes += (size_t)g * nr * a.K;
+    scales += (size_t)g * (nr / kQB) * nb;
+  }
+  // first weight row of each of the wave's tiles; tile i of gate_up is the
+  // gate (i = 0) or the up (i = 1) row block of the same columns
+  int n0[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+    n0[i] = MODE == kStreamGateUp ? (tile * RW + rw) * 16 + i * a.N
+                                  : ((tile * RW + rw) * RT + i) * 16;
+  const int nlim = MODE == kStreamGateUp ? 2 * a.N : a.N;
+  const int q = lane >> 4;
+  const uint8_t* wrow[RT];
+  const float* srow[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    wrow[i] = codes + (size_t)min(n0[i] + (lane & 15), nlim - 1) * a.K;
+    srow[i] = scales + (size_t)(min(n0[i], nlim - 1) / kQB) * nb;
+  }
+  // 16 rows at a time: a group has more than 16 only if a caller's ids name an
+  // expert twice for one token
+  for (int r0 = 0; r0 < rows; r0 += 16) {
+    if (r0) __syncthreads();  // red[] is free again
+    const int pos = p0 + r0 + (lane & 15);  // this lane's input row
+    bool on = r0 + (lane & 15) < rows;
+    const char* xrow = nullptr;
+    if (on) {
+      int from = pos;
+      if (MODE != kStreamLinear) {
+        const int tok = slot_token(a.sorted_slot[pos], a.T, a.topk, a.has_shared);
+        on = tok >= 0;
+        if (MODE == kStreamGateUp) from = tok;
+      }
+      if (on) xrow = (const char*)a.x + (size_t)from * a.K * (DT == MOE_DT_F32 ? 4 : 2);
+    }
+    f32x4 acc[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int b = kw; b < nb; b += KW) {
+      const int k0 = b * kQB + 32 * q;
+      Frag<EX> w[RT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        // chunks past the row's end are read from its start instead: their
+        // counterparts in the token rows are zeros
+        const u32x4 lo = *(const u32x4*)(wrow[i] + (k0 < a.K ? k0 : 0));
+        const u32x4 hi = *(const u32x4*)(wrow[i] + (k0 + 16 < a.K ? k0 + 16 : 0));
+        w[i].set(join8(lo, hi));
+      }
+      float f[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) f[j] = 0.f;
+      if (on) load32<DT>(xrow, k0, a.K, f);
+      float am = 0.f;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) am = fmaxf(am, fabsf(f[j]));
+      am = fmaxf(am, __shfl_xor(am, 16));
+      am = fmaxf(am, __shfl_xor(am, 32));
+      am = q_floor(am);
+      const float m = 448.0f / am, sx = am / 448.0f;
+      i32x8 xq;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        xq[j] = (int)fp8x4(f[4 * j] * m, f[4 * j + 1] * m, f[4 * j + 2] * m, f[4 * j + 3] * m);
+      Frag<EX> xf;
+      xf.set(xq);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const f32x4 p = mfma128(w[i], xf);
+        const float s = sx * srow[i][b];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(s, p[j], acc[i][j]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) red[wv][i][lane] = acc[i];
+    __syncthreads();
+    // wave rw * KW joins its tile group's KW partial sums, in wave order
+    if (kw != 0) continue;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int w2 = 1; w2 < KW; ++w2) acc[i] += red[wv + w2][i][lane];
+    if (!on) continue;
+    if (MODE == kStreamGateUp) {
+      const int n = n0[0] + 4 * q;
+      f32x4 h;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = silu_f32(acc[0][j]) * acc[RT - 1][j];
+      *(f32x4*)((float*)a.out + (size_t)pos * a.N + n) = h;
+    } else {
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const int n = n0[i] + 4 * q;
+        if (n >= a.N) continue;
+        constexpr int ODT = MODE == kStreamDown ? MOE_DT_BF16 : DT;
+        const size_t at = (size_t)pos * a.N + n;
+        if (ODT == MOE_DT_F32) {
+          *(f32x4*)((float*)a.out + at) = acc[i];
+        } else if (ODT == MOE_DT_BF16) {
+          *(u32x2*)((uint16_t*)a.out + at) =
+              u32x2{pack_bf16x2(acc[i][0], acc[i][1]), pack_bf16x2(acc[i][2], acc[i][3])};
+        } else {
+          *(u32x2*)((uint16_t*)a.out + at) =
+              u32x2{pack_f16x2(acc[i][0], acc[i][1]), pack_f16x2(acc[i][2], acc[i][3])};
+        }
+      }
+    }
+  }
+}
+
+template <int DT>
+static void reg(std::vector<const void*>& k) {
+  k.push_back((const void*)&k_fp8_stream<DT, kStreamLinear, 1, 8>);
+  k.push_back((const void*)&k_fp8_stream<DT, kStreamLinear, 2, 8>);
+}
+void register_fp8_stream_kernels(std::vector<const void*>& k) {
+  reg<MOE_DT_BF16>(k);
+  reg<MOE_DT_F16>(k);
+  reg<MOE_DT_F32>(k);
+  k.push_back((const void*)&k_fp8_stream<MOE_DT_BF16, kStreamGateUp, 2, 8>);
+  k.push_back((const void*)&k_fp8_stream<MOE_DT_F32, kStreamDown, 2, 4>);
+}
+
+hipError_t launch_fp8_stream_linear(const moe_fp8_matrix& M, const void* x, int T, int dtype,
+                                    void* out, hipStream_t s) {
+  StreamArgs a{};
+  a.codes = M.codes;
+  a.scales = M.scales;
+  a.x = x;
+  a.out = out;
+  a.R = T;
+  a.N = M.N;
+  a.K = M.K;
+  const int RT = M.N >= 8192 ? 2 : 1;
+  a.tiles = (M.N + 16 * RT - 1) / (16 * RT);
+  by_dtype(dtype, [&](auto D) {
+    constexpr int DT = decltype(D)::value;
+    if (RT == 1)
+      MOE_LAUNCH("fp8_stream", s, (k_fp8_stream<DT, kStreamLinear, 1, 8>), dim3(a.tiles),
+                 dim3(512), 0, s, a);
+    else
+      MOE_LAUNCH("fp8_stream", s, (k_fp8_stream<DT, kStreamLinear, 2, 8>), dim3(a.tiles),
+                 dim3(512), 0, s, a);
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_fp8_stream_experts(const moe_fp8_weights& W, const uint16_t* x, int T, int K,
+                                     const int32_t* offsets, const int32_t* sorted_slot,
+                                     const int32_t* groups, float* h, uint16_t* y,
+                                     hipStream_t s) {
+  const long most = (long)T * K < W.E ? (long)T * K : W.E;
+  const int G = (int)most + W.has_shared;  // groups that can be active
+  StreamArgs a{};
+  a.codes = W.gu_codes;
+  a.scales = W.gu_scales;
+  a.x = x;
+  a.out = h;
+  a.offsets = offsets;
+  a.sorted_slot = sorted_slot;
+  a.groups = groups;
+  a.N = W.I;
+  a.K = W.H;
+  a.T = T;
+  a.topk = K;
+  a.has_shared = W.has_shared;
+  a.tiles = W.I / 16;
+  MOE_LAUNCH("fp8_stream_gate_up", s, (k_fp8_stream<MOE_DT_BF16, kStreamGateUp, 2, 8>),
+             dim3((unsigned)G * a.tiles), dim3(512), 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  a.codes = W.dn_codes;
+  a.scales = W.dn_scales;
+  a.x = h;
+  a.out = y;
+  a.N = W.H;
+  a.K = W.I;
+  a.tiles = W.H / 64;
+  MOE_LAUNCH("fp8_stream_down", s, (k_fp8_stream<MOE_DT_F32, kStreamDown, 2, 4>),
+             dim3((unsigned)G * a.tiles), dim3(512), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace moe

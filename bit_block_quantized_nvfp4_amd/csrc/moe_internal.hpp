@@ -136,4 +136,54 @@ hipError_t launch_decode_ffn(const moe_nvfp4_weights& W, const uint16_t* x, int 
                              const int32_t* groups, int act_mode, uint16_t* hbuf, uint8_t* xq,
                              float* xs, uint16_t* y, hipStream_t s);
 
+// Token sort and its gradients (moe_sort.hip).
+void register_sort_kernels(std::vector<const void*>& k);
+hipError_t launch_dispatch(const void* x, const int32_t* slot_pos, int T, int K, int H,
+                           int has_shared, int dtype, void* xs, hipStream_t s);
+// w == nullptr: plain sum of the slots' rows.
+hipError_t launch_slot_sum(const void* y, const float* w, const int32_t* slot_pos,
+                           const float* gate, int T, int K, int H, int has_shared, int dtype,
+                           void* out, hipStream_t s);
+hipError_t launch_combine_grad(const void* dout, const void* y, const float* w,
+                               const int32_t* slot_pos, const float* gate, int T, int K, int H,
+                               int has_shared, int dtype, void* dy, float* dw, float* dgate,
+                               hipStream_t s);
+hipError_t launch_topk_grad(const int32_t* ids, const float* w, const float* dw, int T, int E,
+                            int K, float* dlogits, hipStream_t s);
+
+// Norms around a block (moe_block_norm.hip).
+void register_block_norm_kernels(std::vector<const void*>& k);
+hipError_t launch_block_norm(const void* res, const void* y, const void* gate, int gate_kind,
+                             const float* w_post, const float* w_pre, float res_scale,
+                             float out_scale, float eps, int T, int H, int dtype, void* r_out,
+                             void* n_out, float* rstd_post, float* rstd_pre, hipStream_t s);
+size_t block_norm_workspace_bytes(int T, int H, int dtype);
+hipError_t launch_block_norm_grad(const void* dr, const void* dn, const void* r_out, const void* y,
+                                  const void* gate, int gate_kind, const float* w_post,
+                                  const float* w_pre, const float* rstd_post,
+                                  const float* rstd_pre, float res_scale, float out_scale, int T,
+                                  int H, int dtype, void* dres, void* dy, void* dgate,
+                                  float* dw_post, float* dw_pre, void* ws, hipStream_t s);
+
+// e4m3 products with a scale per block of 128 (moe_fp8_stream.hip: up to
+// kFp8StreamMaxT rows, one MFMA operand; moe_fp8_tile.hip: more).
+constexpr int kFp8StreamMaxT = 16;
+void register_fp8_stream_kernels(std::vector<const void*>& k);
+void register_fp8_tile_kernels(std::vector<const void*>& k);
+hipError_t launch_fp8_quant(const void* x, int T, int K, int dtype, int ldq, uint8_t* codes,
+                            float* scales, hipStream_t s);
+size_t fp8_linear_workspace_bytes(int T, int K);
+hipError_t launch_fp8_linear(const moe_fp8_matrix& M, const void* x, int T, int dtype, void* out,
+                             void* ws, hipStream_t s);
+hipError_t launch_fp8_stream_linear(const moe_fp8_matrix& M, const void* x, int T, int dtype,
+                                    void* out, hipStream_t s);
+size_t fp8_expert_ffn_workspace_bytes(int T, int K, int H, int I, int has_shared);
+hipError_t launch_fp8_expert_ffn(const moe_fp8_weights& W, const uint16_t* x, int T, int K,
+                                 const int32_t* offsets, const int32_t* sorted_slot,
+                                 const int32_t* groups, uint16_t* y, void* ws, hipStream_t s);
+hipError_t launch_fp8_stream_experts(const moe_fp8_weights& W, const uint16_t* x, int T, int K,
+                                     const int32_t* offsets, const int32_t* sorted_slot,
+                                     const int32_t* groups, float* h, uint16_t* y,
+                                     hipStream_t s);
+
 }  // namespace moe

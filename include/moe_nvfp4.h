@@ -12,6 +12,11 @@
  *                                      expert group (routed + shared)
  *   moe_combine     -> out             fixed-order fp32 weighted sum
  *
+ * Around and beside the layer: the token sort by itself with its gradients
+ * (moe_dispatch, moe_combine_grad, ...), the norms before and after a block
+ * (moe_block_norm), and products in e4m3 with a scale per block of 128
+ * (moe_fp8_linear, moe_fp8_expert_ffn).
+ *
  * Sources.  The operations are the ones listed as the prefill ops of a MoE
  * layer that can change the logits (router GEMM + top-k, shared expert, routed
  * experts, combine/unpermute) in the issue "[job] Qwen3.8-Flash-Next:
@@ -64,6 +69,16 @@ extern "C" {
 #define MOE_ACT_FP8_ROW 1     /* gate_up reads per-token-row e4m3 activations      */
 #define MOE_ACT_FP8_ROUTED 2  /* routed experts e4m3, the shared expert bf16       */
 #define MOE_ACT_FP8_SHARED 3  /* routed experts bf16, the shared expert e4m3       */
+
+/* Element types of the rows that the sort, norm and e4m3 entry points take. */
+#define MOE_DT_BF16 0
+#define MOE_DT_F16 1
+#define MOE_DT_F32 2
+
+/* Gates of moe_block_norm. */
+#define MOE_GATE_NONE 0
+#define MOE_GATE_TOKEN 1      /* one f32 logit per token                           */
+#define MOE_GATE_ELEMENT 2    /* a logit per element, in the rows' type            */
 
 /* Operation ids of moe_workspace_bytes. */
 #define MOE_OP_PERMUTE 1
@@ -366,6 +381,171 @@ int moe_combine(const uint16_t* y_slots, const float* w, const int32_t* slot_pos
  */
 int moe_combine_gated(const uint16_t* y_slots, const float* w, const int32_t* slot_pos,
                       const float* gate, int T, int K, int H, uint16_t* out, void* stream);
+
+/*
+ * The token sort by itself, its gradients, and the gradient of the routing
+ * weights: what training the router and the experts needs around products of
+ * its own.  Rows are bf16, f16 or f32 (dtype, MOE_DT_*); slot_pos is
+ * moe_permute's, [T*K + T*has_shared]; sums are f32 in slot order, then the
+ * shared expert, with one rounding to nearest even at the end.
+ *
+ *   moe_dispatch       xs[slot_pos[s]] = x[token of s] for every slot s
+ *   moe_dispatch_grad  dx[t] = sum over the slots s of t of dxs[slot_pos[s]]
+ *   moe_combine_typed  moe_combine (gate NULL) or moe_combine_gated (gate given,
+ *                      which needs has_shared) for rows of any dtype
+ *   moe_combine_grad   of moe_combine / moe_combine_gated:
+ *                        dy_slots[slot_pos[tK+k]] = w[t][k] dout[t]
+ *                        dw[t][k] = <dout[t], y_slots[slot_pos[tK+k]]>
+ *                        dy_slots[slot_pos[TK+t]] = c dout[t]
+ *                        dgate[t] = c (1 - c) <dout[t], y_slots[slot_pos[TK+t]]>
+ *                      with c = sigmoid(gate[t]), or 1 without a gate
+ *   moe_route_topk_grad  dlogits[t][ids[t][k]] = w_k (dw_k - sum_j w_j dw_j),
+ *                      zero for the experts not chosen; an expert named twice
+ *                      in a row gets both terms, an id outside [0, E) none
+ *
+ *   x, dx, out, dout [T][H]; xs, dxs, y_slots, dy_slots [T*K + T*has_shared][H]
+ *   w, dw [T][K], gate, dgate [T], dlogits [T][E]: float32
+ *
+ * A routed slot whose slot_pos lies outside [0, T*K), or a shared one outside
+ * [0, T*K + T), is skipped: it adds nothing, its dw is 0 and its dgate 0, and
+ * rows of xs and dy_slots that no slot points at are left as they were.
+ * Limits: 1 <= K <= 32, H a multiple of 8 in [8, 65536], row pointers aligned
+ * to 16 bytes.  The outputs may not overlap the inputs.
+ */
+int moe_dispatch(const void* x, const int32_t* slot_pos, int T, int K, int H, int has_shared,
+                 int dtype, void* xs, void* stream);
+int moe_dispatch_grad(const void* dxs, const int32_t* slot_pos, int T, int K, int H,
+                      int has_shared, int dtype, void* dx, void* stream);
+int moe_combine_typed(const void* y_slots, const float* w, const int32_t* slot_pos,
+                      const float* gate, int T, int K, int H, int has_shared, int dtype, void* out,
+                      void* stream);
+int moe_combine_grad(const void* dout, const void* y_slots, const float* w,
+                     const int32_t* slot_pos, const float* gate, int T, int K, int H,
+                     int has_shared, int dtype, void* dy_slots, float* dw, float* dgate,
+                     void* stream);
+int moe_route_topk_grad(const int32_t* ids, const float* w, const float* dw, int T, int E, int K,
+                        float* dlogits, void* stream);
+
+/*
+ * The norms before and after a block (such as this layer), fused with the
+ * block's gate and the residual scale.  For each row t of H values, with
+ * rstd(v) = 1 / sqrt(mean(v^2) + eps) in f32:
+ *
+ *   u  = y rstd(y) w_post            norm after (w_post NULL: u = y)
+ *   r' = res_scale r + out_scale c u the residual stream, rounded to dtype
+ *   n  = r' rstd(r') w_pre           norm before the next block, of the rounded
+ *                                    r' (w_pre NULL: not computed)
+ *
+ * c = 1 (gate_kind MOE_GATE_NONE), sigmoid(gate[t]) (MOE_GATE_TOKEN, float32
+ * [T]) or sigmoid(gate[t][h]) (MOE_GATE_ELEMENT, rows of dtype).  Without y
+ * (NULL) only n = r rstd(r) w_pre is computed: a first block's norm; w_post,
+ * gate and r_out are then NULL.
+ *
+ *   residual, y, r_out, n_out [T][H] of dtype; r_out may be residual itself
+ *   w_post, w_pre [H] float32; rstd_post, rstd_pre [T] float32 (out, or NULL)
+ *
+ * moe_block_norm_grad returns the gradients of all of it from dr (gradient of
+ * r_out, or NULL for zero) and dn (gradient of n_out; NULL exactly when w_pre
+ * is), with r_out (the residual itself where y is NULL), y, gate and the
+ * statistics of the forward call:
+ *
+ *   dres [T][H], dy [T][H] (NULL without y), dgate as gate (NULL without one),
+ *   dw_post, dw_pre [H] float32 (NULL without the weight)
+ *   ws  at least moe_block_norm_workspace_bytes(T, H, dtype) bytes
+ *
+ * The sums over the tokens of dw_post and dw_pre are f32, split and joined in
+ * an order that T and H alone determine.  Limits: H a multiple of 8 in
+ * [8, 8192], all row and weight pointers aligned to 16 bytes, eps >= 0.
+ * Except r_out on residual, outputs may not overlap inputs.
+ */
+int moe_block_norm(const void* residual, const void* y, const void* gate, int gate_kind,
+                   const float* w_post, const float* w_pre, float res_scale, float out_scale,
+                   float eps, int T, int H, int dtype, void* r_out, void* n_out, float* rstd_post,
+                   float* rstd_pre, void* stream);
+size_t moe_block_norm_workspace_bytes(int T, int H, int dtype);
+int moe_block_norm_grad(const void* dr, const void* dn, const void* r_out, const void* y,
+                        const void* gate, int gate_kind, const float* w_post, const float* w_pre,
+                        const float* rstd_post, const float* rstd_pre, float res_scale,
+                        float out_scale, int T, int H, int dtype, void* dres, void* dy,
+                        void* dgate, float* dw_post, float* dw_pre, void* ws, size_t ws_bytes,
+                        void* stream);
+
+/*
+ * Products in e4m3 (OCP "fn") with a scale for each block of 128.  A weight
+ * matrix W[n][k] = codes[n][k] * scales[n / 128][k / 128], a row x is quantised
+ * in blocks of 128 along K: a = max(absmax, 2^-100) of the block, scale
+ * s = a / 448, code = e4m3(x * (448 / a)), each operation rounded to f32.
+ *
+ *   codes [N][K] e4m3, scales [ceil(N/128)][ceil(K/128)] float32
+ *
+ * moe_fp8_quant writes the codes [T][K] and scales [T][ceil(K/128)] of rows x.
+ *
+ * moe_fp8_linear: out[t][n] = sum_b s[t][b] scales[n/128][b] sum_{k in b}
+ * code_x[t][k] codes[n][k], f32 sums, one rounding to dtype.  Up to 16 rows
+ * run as one launch that streams the weights once; more run as the
+ * quantisation and a tiled product.  The gradient by x is the same call with
+ * the transposed matrix (codes^T, scales^T: blocks of 128 x 128 stay blocks,
+ * so it is exact and is laid out once) on the gradient of out.
+ *
+ *   x [T][K], out [T][N] of dtype
+ *   ws  at least moe_fp8_linear_workspace_bytes(T, K) bytes (0 up to 16 rows)
+ *
+ * A NaN or an infinity in a row makes that row's outputs NaN and no others.
+ * Limits: K a multiple of 16, N a multiple of 8, both in [16, 65536] and
+ * [8, 65536]; pointers of codes, x and out aligned to 16 bytes.
+ */
+typedef struct moe_fp8_matrix {
+  const uint8_t* codes;
+  const float* scales;
+  int32_t N;
+  int32_t K;
+} moe_fp8_matrix;
+
+int moe_fp8_quant(const void* x, int T, int K, int dtype, uint8_t* codes, float* scales,
+                  void* stream);
+size_t moe_fp8_linear_workspace_bytes(int T, int K);
+int moe_fp8_linear(const moe_fp8_matrix* M, const void* x, int T, int dtype, void* out, void* ws,
+                   size_t ws_bytes, void* stream);
+
+/*
+ * A bank of experts in that format, laid out like moe_nvfp4_weights
+ * (E' = E + has_shared groups, the shared expert at index E):
+ *
+ *   gu_codes [E'][2I][H], gu_scales [E'][2I/128][H/128]   rows 0..I-1 gate, I..2I-1 up
+ *   dn_codes [E'][H][I],  dn_scales [E'][H/128][I/128]
+ *
+ * moe_fp8_expert_ffn is moe_expert_ffn for such a bank: for the row of sorted
+ * position p in group e (token t)
+ *
+ *   g = xq[t] . W_gate,e^T, u = xq[t] . W_up,e^T,  h = silu(g) * u   (f32)
+ *   y_slots[p] = bf16( hq . W_down,e^T )
+ *
+ * with xq, hq the rows quantised as above (x [T][H] bf16, h not rounded in
+ * between).  offsets, sorted_slot and groups are moe_permute's; y_slots goes to
+ * moe_combine.  Up to 16 tokens the active experts' weights stream once, in
+ * two launches; more run as the quantisation and two grouped products.
+ *
+ *   ws  at least moe_fp8_expert_ffn_workspace_bytes(T, K, H, I, has_shared)
+ *
+ * Rows whose sorted_slot entry is out of range are skipped.  Limits: those of
+ * the permutation; H and I multiples of 128 in [128, 8192]; pointers of
+ * codes, x and y_slots aligned to 16 bytes.
+ */
+typedef struct moe_fp8_weights {
+  const uint8_t* gu_codes;
+  const float* gu_scales;
+  const uint8_t* dn_codes;
+  const float* dn_scales;
+  int32_t E;
+  int32_t H;
+  int32_t I;
+  int32_t has_shared;
+} moe_fp8_weights;
+
+size_t moe_fp8_expert_ffn_workspace_bytes(int T, int K, int H, int I, int has_shared);
+int moe_fp8_expert_ffn(const moe_fp8_weights* W, const uint16_t* x, int T, int K,
+                       const int32_t* offsets, const int32_t* sorted_slot, const int32_t* groups,
+                       uint16_t* y_slots, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Per-kernel timing, for measurement only.  While enabled, every kernel the
