@@ -625,8 +625,8 @@ int moe_fp8_expert_ffn(const moe_fp8_weights* W, const uint16_t* x, int T, int K
     return fail(MOE_EINVAL, "moe_fp8_expert_ffn: null weight pointer");
   if (!sizes_ok_common(T, W->E, K) || (W->has_shared != 0 && W->has_shared != 1))
     return fail(MOE_EINVAL, "moe_fp8_expert_ffn: need T >= 1, 1 <= K <= min(E, 32), E <= 1024, has_shared in {0,1}");
-  if (!fp8_bank_ok(W->H, W->I))
-    return fail(MOE_EINVAL, "moe_fp8_expert_ffn: need H and I multiples of 128 in [128, 8192] (H=%d I=%d)", W->H, W->I);
+  if (!fp8_bank_ok(W->H, W->I) || (long long)T * W->H >= (1LL << 32))
+    return fail(MOE_EINVAL, "moe_fp8_expert_ffn: need H and I multiples of 128 in [128, 8192] and T*H < 2^32 (T=%d H=%d I=%d)", T, W->H, W->I);
   if (!aligned16((const char*)x, (const char*)y_slots, W->gu_codes, W->dn_codes, (const char*)ws))
     return fail(MOE_EINVAL, "moe_fp8_expert_ffn: codes, rows and workspace must be aligned to 16 bytes");
   const size_t need = moe::fp8_expert_ffn_workspace_bytes(T, K, W->H, W->I, W->has_shared);

@@ -79,39 +79,78 @@ struct TileArgs {
   int nt;                  // tiles along N
 };
 
-__device__ __forceinline__ void wait_dma() {
-  __builtin_amdgcn_s_waitcnt(0 | (7 << 4) | (15 << 8));  // vmcnt(0) only
+// Buffer descriptor of `bytes` bytes at p (both wave-uniform): loads past the
+// end return zeros.
+__device__ __forceinline__ u32x4 buf_of(const void* p, uint32_t bytes) {
+  const uint64_t a = (uint64_t)(uintptr_t)p;
+  return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+               (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)) & 0xFFFFu,
+               (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00027000u};
+}
+// Memory to LDS, 16 (4) bytes a lane: lane l's bytes at voff + soff land at
+// lds + 16 l (4 l).  No register is written.  In asm because the compiler
+// would wait for every such load before the next LDS read of any buffer; the
+// kernel's own waits below order them.  m0 is reserved: the compiler keeps
+// nothing in it, and nothing else here uses it.
+__device__ __forceinline__ void dma_b128(u32x4 buf, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds),
+               "v"(voff), "s"(buf), "s"(soff)
+               : "memory");
+}
+__device__ __forceinline__ void dma_b32(u32x4 buf, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds),
+               "v"(voff), "s"(buf), "s"(soff)
+               : "memory");
+}
+// All but the wave's last N memory operations are done, and all its LDS reads;
+// then the block's waves meet.
+template <int N>
+__device__ __forceinline__ void wait_step() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-template <int MODE, int DT, int BN, int BM, int WN, int WM>
+// NBUF buffers of one K step each: step b is computed while steps up to b +
+// NBUF - 1 are on their way.
+template <int MODE, int DT, int BN, int BM, int WN, int WM, int NBUF>
 __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
-  constexpr int NT = 64 * WN * WM;
+  constexpr int NW = WN * WM, NT = 64 * NW;
   constexpr int TN = BN / WN, TM = BM / WM;    // a wave's part of the tile
   constexpr int FN = TN / 16, FM = TM / 16;
-  constexpr int ROWS = BN + BM;
-  constexpr int DMA = ROWS * 8 / NT;           // 16-byte chunks per thread and step
+  constexpr int DW = BN * 8 / NT, DX = BM * 8 / NT;  // 16-byte chunks per thread and step
+  constexpr int D = DW + DX + 1;               // memory operations per wave and step
+  constexpr int kTok = BN * kQB, kScale = kTok + BM * kQB;  // LDS offsets in a buffer
+  constexpr int kBuf = kScale + BM * 4;
   constexpr bool EX = DT == MOE_DT_F32;
-  static_assert(ROWS * 8 % NT == 0 && TN % 16 == 0 && TM % 16 == 0, "tile shape");
-  __shared__ __align__(1024) uint8_t lds[2][ROWS * kQB];
+  static_assert(BN * 8 % NT == 0 && BM * 8 % NT == 0 && TN % 16 == 0 && TM % 16 == 0 &&
+                    BM % 64 == 0 && BM / 64 <= NW && (NBUF - 2) * D < 64,
+                "tile shape");
+  constexpr int kMaxNB = (MODE == kTileLinear ? 65536 : 8192) / kQB;
+  constexpr int NS = (BN + kQB - 1) / kQB;     // weight scales of a step
+  __shared__ __align__(1024) uint8_t lds[NBUF * kBuf];
+  __shared__ float wsc[NS][kMaxNB];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wn = wv % WN, wm = wv / WN;        // waves of one SIMD share wn
+  const int wn = wv % WN, wm = wv / WN;
   const int nb = (a.K + kQB - 1) / kQB;
 
   const uint8_t* codes = a.codes;
   const float* scales = a.scales;
   int m0, rows, n0;                            // first token row, rows left, first column
   if (MODE == kTileLinear) {
-    const int mt = (a.R + BM - 1) / BM;
-    // 8 XCDs take the blocks in turn: give each a run of token tiles of one
-    // weight tile
+    // Blocks are dealt to the 8 XCDs in turn: give each XCD a run of tiles, and
+    // let a run go 8 token tiles deep before its next weight tile, so that the
+    // blocks that run together on one XCD share rows of both operands in its L2
+    const int mt = (a.R + BM - 1) / BM, nblk = gridDim.x, per = nblk / 8;
     const int b = blockIdx.x;
-    n0 = (b / mt) * BN;
-    m0 = (b % mt) * BM;
+    const int lin = b < per * 8 ? (b % 8) * per + b / 8 : b;
+    const int deep = 8 * a.nt, grp = lin / deep, in = lin % deep;
+    const int gm = min(8, mt - grp * 8);
+    m0 = (grp * 8 + in % gm) * BM;
+    n0 = (in / gm) * BN;
     rows = a.R - m0;
   } else {
     __shared__ unsigned long long base[kPMaxG];
-    __shared__ unsigned long long wsum[NT / 64];
+    __shared__ unsigned long long wsum[NW];
     PfTile ti;
     if (!pf_find_tile<NT>(a.offsets, a.G, a.nt, base, wsum, &ti)) return;
     const int nr = MODE == kTileGateUp ? 2 * a.N : a.N;
@@ -121,42 +160,63 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
     rows = ti.rows;
     n0 = ti.nt * (MODE == kTileGateUp ? BN / 2 : BN);
   }
-  if (rows > BM) rows = BM;
+  m0 = __builtin_amdgcn_readfirstlane(m0);
+  n0 = __builtin_amdgcn_readfirstlane(n0);
+  rows = __builtin_amdgcn_readfirstlane(min(rows, BM));
 
-  // Weight row of LDS row lr.  gate_up: each wave's TN rows are TN / 2 gate
-  // rows and the up rows of the same columns.
+  // Weight row (from the buffer's base) of LDS row lr.  gate_up: each wave's TN
+  // rows are TN / 2 gate rows and the up rows of the same columns.
   auto wrow_of = [&](int lr) {
     if (MODE == kTileGateUp) {
       const int w = lr / TN, q = lr % TN;
       return n0 + w * (TN / 2) + q % (TN / 2) + (q < TN / 2 ? 0 : a.N);
     }
-    return min(n0 + lr, a.N - 1);
+    return min(lr, a.N - 1 - n0);
   };
-  const uint8_t* src[DMA];
-  int kbase[DMA];                              // position of the chunk in the block
+  // Row of the token buffer of the tile's row r.
+  auto xrow_of = [&](int r) {
+    r = min(r, rows - 1);
+    if (MODE == kTileGateUp)
+      return max(slot_token(a.sorted_slot[m0 + r], a.T, a.topk, a.has_shared), 0);
+    return r;
+  };
+  const uint32_t ldx = (uint32_t)nb * kQB;
+  u32x4 wbuf = MODE == kTileGateUp
+                         ? buf_of(codes, (uint32_t)(2 * a.N) * (uint32_t)a.K)
+                         : buf_of(codes + (size_t)n0 * a.K,
+                                  (uint32_t)min(BN, a.N - n0) * (uint32_t)a.K);
+  u32x4 xbuf = MODE == kTileGateUp ? buf_of(a.xq, (uint32_t)a.T * ldx)
+                                         : buf_of(a.xq + (size_t)m0 * ldx, (uint32_t)rows * ldx);
+  u32x4 sbuf = MODE == kTileGateUp
+                         ? buf_of(a.xs, (uint32_t)a.T * (uint32_t)nb * 4u)
+                         : buf_of(a.xs + (size_t)m0 * nb, (uint32_t)rows * (uint32_t)nb * 4u);
+  // a memory instruction may read scalar registers that a vector instruction
+  // wrote (the descriptors') only 5 states later; in asm that is for us to keep
+  asm volatile("s_nop 4" : "+s"(wbuf), "+s"(xbuf), "+s"(sbuf));
+  // Chunk i of this thread: LDS row lr, place tid % 8; rows of one thread are
+  // NT / 8 apart, a multiple of 8, so its chunk of the row is always the same.
+  const int chunk = 16 * ((tid & 7) ^ ((tid >> 3) & 7));
+  uint32_t woff[DW], xoff[DX];
 #pragma unroll
-  for (int i = 0; i < DMA; ++i) {
-    const int at = i * NT + tid;               // chunk: LDS row at / 8, place at % 8
-    const int lr = at >> 3, c = (at & 7) ^ (lr & 7);
-    kbase[i] = 16 * c;
-    if (lr < BN) {
-      src[i] = codes + (size_t)wrow_of(lr) * a.K;
-    } else {
-      const int r = min(lr - BN, rows - 1);
-      int from = m0 + r;
-      if (MODE == kTileGateUp) from = max(slot_token(a.sorted_slot[from], a.T, a.topk, a.has_shared), 0);
-      src[i] = a.xq + (size_t)from * nb * kQB;
-    }
-  }
-  auto dma = [&](int b, int buf) {
+  for (int i = 0; i < DW; ++i)
+    woff[i] = (uint32_t)wrow_of((i * NT + tid) >> 3) * (uint32_t)a.K + chunk;
 #pragma unroll
-    for (int i = 0; i < DMA; ++i) {
-      // past the end of a weight row its first chunk is read instead: the
-      // tokens' codes there are zeros
-      int k = b * kQB + kbase[i];
-      if (i * NT < BN * 8 && k >= a.K && (i * NT + tid) < BN * 8) k = 0;
-      dma16(src[i] + k, &lds[buf][(i * NT + wv * 64) * 16]);
-    }
+  for (int i = 0; i < DX; ++i) xoff[i] = (uint32_t)xrow_of((i * NT + tid) >> 3) * ldx + chunk;
+  const int srow = 64 * (wv % (BM / 64)) + lane;  // every wave brings 64 token scales
+  const uint32_t soff = (uint32_t)xrow_of(srow) * (uint32_t)nb * 4u;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+  const uint32_t ldsw = lds0 + wv * 1024;
+
+  auto dma = [&](int b) {
+    const uint32_t at = (uint32_t)(b % NBUF) * kBuf, k = (uint32_t)b * kQB;
+    // a chunk past the end of a weight row is read from the start of the block
+    // instead: the tokens' codes there are zeros
+    const uint32_t back = (int)k + chunk >= a.K ? (uint32_t)chunk : 0u;
+#pragma unroll
+    for (int i = 0; i < DW; ++i) dma_b128(wbuf, woff[i] - back, k, ldsw + at + i * NT * 16);
+#pragma unroll
+    for (int i = 0; i < DX; ++i) dma_b128(xbuf, xoff[i], k, ldsw + at + kTok + i * NT * 16);
+    dma_b32(sbuf, soff, (uint32_t)b * 4u, lds0 + at + kScale + 256 * (wv % (BM / 64)));
   };
 
   f32x4 acc[FN][FM];
@@ -165,55 +225,48 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
 #pragma unroll
     for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // this lane's token of each tile column, for its scales
-  const float* xs[FM];
-  int live = 0;                                // columns of the wave with rows in them
+  // columns of 16 tokens of this wave with rows in them
+  const int live = min(FM, max(0, (rows - wm * TM + 15) / 16));
 #pragma unroll
-  for (int j = 0; j < FM; ++j) {
-    const int r = wm * TM + 16 * j + (lane & 15);
-    if (wm * TM + 16 * j < rows) live = j + 1;
-    int from = m0 + min(r, rows - 1);
-    if (MODE == kTileGateUp) from = max(slot_token(a.sorted_slot[from], a.T, a.topk, a.has_shared), 0);
-    xs[j] = a.xs + (size_t)from * nb;
+  for (int b = 0; b < NBUF - 1; ++b)
+    if (b < nb) dma(b);
+  // The weight scales of all steps, one per 128 rows of the tile: in LDS, since
+  // a load of one in the loop would wait for the DMA under way.  gate_up: the
+  // gate's, then the up's.
+  for (int i = tid; i < NS * nb; i += NT) {
+    const int h = i / nb, b = i % nb;
+    const int row = MODE == kTileGateUp ? n0 + h * a.N : min(n0 + h * kQB, a.N - 1);
+    wsc[h][b] = scales[(size_t)(row / kQB) * nb + b];
   }
-  // weight scales of the wave's rows: constant over each 128 rows
-  const float* ws[2];
-  if (MODE == kTileGateUp) {
-    ws[0] = scales + (size_t)(n0 / kQB) * nb;
-    ws[1] = scales + (size_t)((n0 + a.N) / kQB) * nb;
-  } else {
-    ws[0] = ws[1] = scales + (size_t)(min(n0 + wn * TN, a.N - 1) / kQB) * nb;
-  }
+  const int hs = MODE == kTileGateUp ? 0 : wn * TN / kQB;
 
-  // LDS address of this lane's two chunks of row 16 i + lane % 16
+  // this lane's two chunks of row 16 i + lane % 16
   const int fr = lane & 15, fq = lane >> 4;
+  const uint32_t c0 = (uint32_t)(fr * kQB + ((fq ^ (fr & 7)) << 4));
+  const uint32_t c1 = (uint32_t)(fr * kQB + (((fq + 4) ^ (fr & 7)) << 4));
   auto frag = [&](const uint8_t* p, int row16) {
-    const uint8_t* r = p + (row16 + fr) * kQB;
-    return join8(*(const u32x4*)(r + ((fq ^ (fr & 7)) << 4)),
-                 *(const u32x4*)(r + (((fq + 4) ^ (fr & 7)) << 4)));
+    return join8(*(const u32x4*)(p + row16 * kQB + c0), *(const u32x4*)(p + row16 * kQB + c1));
   };
 
-  dma(0, 0);
-  float sx[FM];
-#pragma unroll
-  for (int j = 0; j < FM; ++j) sx[j] = xs[j][0];
-  wait_dma();
-  __syncthreads();
   for (int b = 0; b < nb; ++b) {
-    const int buf = b & 1;
-    float sn[FM];
-    if (b + 1 < nb) {
-      dma(b + 1, buf ^ 1);
-#pragma unroll
-      for (int j = 0; j < FM; ++j) sn[j] = xs[j][b + 1];
-    }
-    const uint8_t* pw = &lds[buf][wn * TN * kQB];
-    const uint8_t* pt = &lds[buf][(BN + wm * TM) * kQB];
-    Frag<EX> tf[FM];
+    // step b has landed when only the steps after it are under way
+    if (nb - 1 - b >= NBUF - 2) wait_step<(NBUF - 2) * D>();
+    else wait_step<0>();
+    // the buffer of step b + NBUF - 1 was read in step b - 1
+    if (b + NBUF - 1 < nb) dma(b + NBUF - 1);
+    const uint8_t* buf = lds + (b % NBUF) * kBuf;
+    const uint8_t* pw = buf + wn * TN * kQB;
+    const uint8_t* pt = buf + kTok + wm * TM * kQB;
+    const float* ps = (const float*)(buf + kScale) + wm * TM + fr;
     if (live > 0) {
+      Frag<EX> tf[FM];
+      float sx[FM];
 #pragma unroll
-      for (int j = 0; j < FM; ++j) tf[j].set(frag(pt, 16 * j));
-      const float w0 = ws[0][b], w1 = ws[1][b];
+      for (int j = 0; j < FM; ++j) {
+        tf[j].set(frag(pt, 16 * j));
+        sx[j] = ps[16 * j];
+      }
+      const float w0 = wsc[hs][b], w1 = wsc[MODE == kTileGateUp ? 1 : hs][b];
 #pragma unroll
       for (int i = 0; i < FN; ++i) {
         Frag<EX> wf;
@@ -230,10 +283,6 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
         }
       }
     }
-#pragma unroll
-    for (int j = 0; j < FM; ++j) sx[j] = sn[j];
-    wait_dma();
-    __syncthreads();
   }
 
   if (MODE == kTileGateUp) {
@@ -241,7 +290,8 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
     // scale of h), then its codes
     constexpr int HN = FN / 2;
     static_assert(MODE != kTileGateUp || BN == 256, "a tile holds one scale of h");
-    float* amax = (float*)&lds[0][0];          // [WN][BM]
+    float* amax = (float*)lds;                 // [WN][BM]
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
       float am = 0.f;
@@ -306,14 +356,14 @@ void register_fp8_tile_kernels(std::vector<const void*>& k) {
     constexpr int DT = decltype(D)::value;
     k.push_back((const void*)&k_fp8_quant<DT>);
     if constexpr (DT != MOE_DT_F32)
-      k.push_back((const void*)&k_fp8_tile<kTileLinear, DT, 256, 256, 2, 4>);
+      k.push_back((const void*)&k_fp8_tile<kTileLinear, DT, 256, 256, 2, 4, 2>);
     else
-      k.push_back((const void*)&k_fp8_tile<kTileLinear, DT, 128, 128, 2, 2>);
-    k.push_back((const void*)&k_fp8_tile<kTileLinear, DT, 128, 64, 4, 1>);
+      k.push_back((const void*)&k_fp8_tile<kTileLinear, DT, 128, 128, 2, 2, 3>);
+    k.push_back((const void*)&k_fp8_tile<kTileLinear, DT, 128, 64, 4, 1, 3>);
   };
   for (int dt = MOE_DT_BF16; dt <= MOE_DT_F32; ++dt) by_dtype(dt, add);
-  k.push_back((const void*)&k_fp8_tile<kTileGateUp, MOE_DT_BF16, 256, 128, 4, 2>);
-  k.push_back((const void*)&k_fp8_tile<kTileDown, MOE_DT_BF16, 256, 128, 4, 2>);
+  k.push_back((const void*)&k_fp8_tile<kTileGateUp, MOE_DT_BF16, 256, 128, 4, 2, 3>);
+  k.push_back((const void*)&k_fp8_tile<kTileDown, MOE_DT_BF16, 256, 128, 4, 2, 3>);
 }
 
 hipError_t launch_fp8_quant(const void* x, int T, int K, int dtype, int ldq, uint8_t* codes,
@@ -356,17 +406,20 @@ hipError_t launch_fp8_linear(const moe_fp8_matrix& M, const void* x, int T, int 
     constexpr int DT = decltype(D)::value;
     if (big >= 192) {
       if constexpr (DT != MOE_DT_F32) {
-        MOE_LAUNCH("fp8_tile_256", s, (k_fp8_tile<kTileLinear, DT, 256, 256, 2, 4>),
+        a.nt = (M.N + 255) / 256;
+        MOE_LAUNCH("fp8_tile_256", s, (k_fp8_tile<kTileLinear, DT, 256, 256, 2, 4, 2>),
                    dim3((unsigned)big), dim3(512), 0, s, a);
       } else {
         // f16 operands take twice the registers
-        const unsigned n = (unsigned)((M.N + 127) / 128) * (unsigned)((T + 127) / 128);
-        MOE_LAUNCH("fp8_tile_128", s, (k_fp8_tile<kTileLinear, DT, 128, 128, 2, 2>), dim3(n),
+        a.nt = (M.N + 127) / 128;
+        const unsigned n = (unsigned)a.nt * (unsigned)((T + 127) / 128);
+        MOE_LAUNCH("fp8_tile_128", s, (k_fp8_tile<kTileLinear, DT, 128, 128, 2, 2, 3>), dim3(n),
                    dim3(256), 0, s, a);
       }
     } else {
-      const unsigned n = (unsigned)((M.N + 127) / 128) * (unsigned)((T + 63) / 64);
-      MOE_LAUNCH("fp8_tile_128", s, (k_fp8_tile<kTileLinear, DT, 128, 64, 4, 1>), dim3(n),
+      a.nt = (M.N + 127) / 128;
+      const unsigned n = (unsigned)a.nt * (unsigned)((T + 63) / 64);
+      MOE_LAUNCH("fp8_tile_128", s, (k_fp8_tile<kTileLinear, DT, 128, 64, 4, 1, 3>), dim3(n),
                  dim3(256), 0, s, a);
     }
   });
@@ -410,7 +463,7 @@ hipError_t launch_fp8_expert_ffn(const moe_fp8_weights& W, const uint16_t* x, in
   a.N = W.I;
   a.K = W.H;
   a.nt = W.I / 128;
-  MOE_LAUNCH("fp8_tile_gate_up", s, (k_fp8_tile<kTileGateUp, MOE_DT_BF16, 256, 128, 4, 2>),
+  MOE_LAUNCH("fp8_tile_gate_up", s, (k_fp8_tile<kTileGateUp, MOE_DT_BF16, 256, 128, 4, 2, 3>),
              dim3(mt * a.nt), dim3(512), 0, s, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -423,7 +476,7 @@ hipError_t launch_fp8_expert_ffn(const moe_fp8_weights& W, const uint16_t* x, in
   a.N = W.H;
   a.K = W.I;
   a.nt = (W.H + 255) / 256;
-  MOE_LAUNCH("fp8_tile_down", s, (k_fp8_tile<kTileDown, MOE_DT_BF16, 256, 128, 4, 2>),
+  MOE_LAUNCH("fp8_tile_down", s, (k_fp8_tile<kTileDown, MOE_DT_BF16, 256, 128, 4, 2, 3>),
              dim3(mt * a.nt), dim3(512), 0, s, a);
   return hipGetLastError();
 }

@@ -34,7 +34,9 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # the handle itself: torch.cuda.current_stream() builds a Stream object around
+    # it, 3 us where this takes 0.2
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _need(t: torch.Tensor, dtype, shape=None, name="tensor"):
@@ -395,24 +397,33 @@ def _dev(t: torch.Tensor, name: str) -> torch.device:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     d = t.device
-    if d.index != torch.cuda.current_device():
+    if d.index != torch._C._cuda_getDevice():
         raise ValueError(f"{name} is on {d}, not on the current device")
     return d
 
 
-def _want(t: torch.Tensor, dtype, shape, dev, name: str) -> torch.Tensor:
-    """t itself, checked against dtype, shape, device and contiguity."""
-    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+def _want(t: torch.Tensor, dtype, shape, dev, name: str) -> int:
+    """t's pointer, after checks of dtype, shape, device and contiguity."""
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
         if t.device != dev:
             raise ValueError(f"{name} must be on {dev}, got {t.device}")
         _need(t, dtype, shape, name)
-    return t
+    return t.data_ptr()
 
 
 def _out(t: Optional[torch.Tensor], dtype, shape, dev, name: str) -> torch.Tensor:
     if t is None:
         return torch.empty(shape, dtype=dtype, device=dev)
-    return _want(t, dtype, shape, dev, name)
+    _want(t, dtype, shape, dev, name)
+    return t
+
+
+def _like(t: Optional[torch.Tensor], ref: torch.Tensor, dev, name: str) -> torch.Tensor:
+    """Output of ref's type and shape: a new one, or t checked against them."""
+    if t is None:
+        return torch.empty_like(ref)
+    _want(t, ref.dtype, ref.shape, dev, name)
+    return t
 
 
 def _slots(slot_pos: torch.Tensor, K: int, has_shared: bool) -> int:
@@ -503,11 +514,11 @@ def moe_combine_grad(dout: torch.Tensor, y_slots: torch.Tensor, w: torch.Tensor,
     _want(slot_pos, torch.int32, (S,), dev, "slot_pos")
     if gate is not None:
         _want(gate, torch.float32, (T,), dev, "gate")
-        dgate = _out(dgate, torch.float32, (T,), dev, "dgate")
+        dgate = _like(dgate, gate, dev, "dgate")
     elif dgate is not None:
         raise ValueError("dgate is given without a gate")
-    dy_slots = _out(dy_slots, dout.dtype, (S, H), dev, "dy_slots")
-    dw = _out(dw, torch.float32, (T, K), dev, "dw")
+    dy_slots = _like(dy_slots, y_slots, dev, "dy_slots")
+    dw = _like(dw, w, dev, "dw")
     check(_lib.lib().moe_combine_grad(dout.data_ptr(), y_slots.data_ptr(), w.data_ptr(),
                                       slot_pos.data_ptr(), _ptr(gate), T, K, H, int(has_shared),
                                       dt, dy_slots.data_ptr(), dw.data_ptr(), _ptr(dgate),
@@ -569,7 +580,7 @@ def moe_block_norm(residual: torch.Tensor, y: Optional[torch.Tensor] = None,
     kind = _gate_kind(gate, residual, dev)
     if y is not None:
         _want(y, residual.dtype, shape, dev, "y")
-        r_out = _out(r_out, residual.dtype, shape, dev, "r_out")
+        r_out = _like(r_out, residual, dev, "r_out")
     if w_post is not None:
         _want(w_post, torch.float32, (H,), dev, "w_post")
         rstd_post = _out(rstd_post, torch.float32, (T,), dev, "rstd_post")
@@ -577,7 +588,7 @@ def moe_block_norm(residual: torch.Tensor, y: Optional[torch.Tensor] = None,
         raise ValueError("rstd_post is given without w_post")
     if w_pre is not None:
         _want(w_pre, torch.float32, (H,), dev, "w_pre")
-        n_out = _out(n_out, residual.dtype, shape, dev, "n_out")
+        n_out = _like(n_out, residual, dev, "n_out")
         rstd_pre = _out(rstd_pre, torch.float32, (T,), dev, "rstd_pre")
     elif n_out is not None or rstd_pre is not None:
         raise ValueError("n_out or rstd_pre is given without w_pre")
@@ -620,19 +631,19 @@ def moe_block_norm_grad(dr: Optional[torch.Tensor], dn: Optional[torch.Tensor], 
         if rstd_pre is None:
             raise ValueError("w_pre needs rstd_pre")
         _want(rstd_pre, f32, (T,), dev, "rstd_pre")
-        dw_pre = torch.empty(H, dtype=f32, device=dev)
+        dw_pre = torch.empty_like(w_pre)
     if y is not None:
         _want(y, r.dtype, shape, dev, "y")
-        dy = torch.empty(shape, dtype=r.dtype, device=dev)
+        dy = torch.empty_like(r)
         if gate is not None:
-            dgate = torch.empty(gate.shape, dtype=gate.dtype, device=dev)
+            dgate = torch.empty_like(gate)
     if w_post is not None:
         _want(w_post, f32, (H,), dev, "w_post")
         if rstd_post is None:
             raise ValueError("w_post needs rstd_post")
         _want(rstd_post, f32, (T,), dev, "rstd_post")
-        dw_post = torch.empty(H, dtype=f32, device=dev)
-    dres = torch.empty(shape, dtype=r.dtype, device=dev)
+        dw_post = torch.empty_like(w_post)
+    dres = torch.empty_like(r)
     L = _lib.lib()
     nb = L.moe_block_norm_workspace_bytes(T, H, dt)
     ws = _scratch(ws, nb, dev)

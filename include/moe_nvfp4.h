@@ -528,8 +528,8 @@ int moe_fp8_linear(const moe_fp8_matrix* M, const void* x, int T, int dtype, voi
  *   ws  at least moe_fp8_expert_ffn_workspace_bytes(T, K, H, I, has_shared)
  *
  * Rows whose sorted_slot entry is out of range are skipped.  Limits: those of
- * the permutation; H and I multiples of 128 in [128, 8192]; pointers of
- * codes, x and y_slots aligned to 16 bytes.
+ * the permutation; H and I multiples of 128 in [128, 8192], T*H < 2^32;
+ * pointers of codes, x and y_slots aligned to 16 bytes.
  */
 typedef struct moe_fp8_weights {
   const uint8_t* gu_codes;
