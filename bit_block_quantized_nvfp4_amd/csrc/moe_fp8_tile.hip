@@ -109,25 +109,26 @@ __device__ __forceinline__ void wait_step() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// NBUF buffers of one K step each: step b is computed while steps up to b +
-// NBUF - 1 are on their way.
-template <int MODE, int DT, int BN, int BM, int WN, int WM, int NBUF>
+// NBUF buffers of one K step each: while step b is computed, the steps up to b +
+// NBUF - 1 (at its end b + NBUF) are on their way.
+template <int MODE, int DT, int BN, int BM, int WN, int WM, int NBUF, int PF>
 __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
   constexpr int NW = WN * WM, NT = 64 * NW;
   constexpr int TN = BN / WN, TM = BM / WM;    // a wave's part of the tile
   constexpr int FN = TN / 16, FM = TM / 16;
   constexpr int DW = BN * 8 / NT, DX = BM * 8 / NT;  // 16-byte chunks per thread and step
-  constexpr int D = DW + DX + 1;               // memory operations per wave and step
+  constexpr int D = DW + DX + 1 + (PF > 0);    // memory operations per wave and step
   constexpr int kTok = BN * kQB, kScale = kTok + BM * kQB;  // LDS offsets in a buffer
   constexpr int kBuf = kScale + BM * 4;
   constexpr bool EX = DT == MOE_DT_F32;
   static_assert(BN * 8 % NT == 0 && BM * 8 % NT == 0 && TN % 16 == 0 && TM % 16 == 0 &&
-                    BM % 64 == 0 && BM / 64 <= NW && (NBUF - 2) * D < 64,
+                    BM % 64 == 0 && BM / 64 <= NW && (NBUF - 1) * D < 64 && FN >= 2,
                 "tile shape");
   constexpr int kMaxNB = (MODE == kTileLinear ? 65536 : 8192) / kQB;
   constexpr int NS = (BN + kQB - 1) / kQB;     // weight scales of a step
   __shared__ __align__(1024) uint8_t lds[NBUF * kBuf];
   __shared__ float wsc[NS][kMaxNB];
+  __shared__ uint32_t touched[PF > 0 ? NT : 1];  // where the L2 prefetch puts its words
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wv % WN, wm = wv / WN;
@@ -204,19 +205,37 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
   for (int i = 0; i < DX; ++i) xoff[i] = (uint32_t)xrow_of((i * NT + tid) >> 3) * ldx + chunk;
   const int srow = 64 * (wv % (BM / 64)) + lane;  // every wave brings 64 token scales
   const uint32_t soff = (uint32_t)xrow_of(srow) * (uint32_t)nb * 4u;
+  // L2 prefetch: one word of each row's block, a row per lane
+  const int prow = (64 * wv) % (BN + BM);
+  const uint32_t poff = prow < BN ? (uint32_t)wrow_of(prow + lane) * (uint32_t)a.K
+                                  : (uint32_t)xrow_of(prow - BN + lane) * ldx;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
   const uint32_t ldsw = lds0 + wv * 1024;
 
+  // Step b to its buffer.  Past the last step the buffers are empty ones (zeros
+  // come, to where nobody reads): every wave then has the same number of
+  // operations under way at every wait, and the loop has no branch, behind
+  // which the compiler would move the sums of half a step and spill.
   auto dma = [&](int b) {
     const uint32_t at = (uint32_t)(b % NBUF) * kBuf, k = (uint32_t)b * kQB;
+    u32x4 wb = wbuf, xb = xbuf, sb = sbuf;
+    wb.z = b < nb ? wb.z : 0u;
+    xb.z = b < nb ? xb.z : 0u;
+    sb.z = b < nb ? sb.z : 0u;
     // a chunk past the end of a weight row is read from the start of the block
     // instead: the tokens' codes there are zeros
     const uint32_t back = (int)k + chunk >= a.K ? (uint32_t)chunk : 0u;
 #pragma unroll
-    for (int i = 0; i < DW; ++i) dma_b128(wbuf, woff[i] - back, k, ldsw + at + i * NT * 16);
+    for (int i = 0; i < DW; ++i) dma_b128(wb, woff[i] - back, k, ldsw + at + i * NT * 16);
 #pragma unroll
-    for (int i = 0; i < DX; ++i) dma_b128(xbuf, xoff[i], k, ldsw + at + kTok + i * NT * 16);
-    dma_b32(sbuf, soff, (uint32_t)b * 4u, lds0 + at + kScale + 256 * (wv % (BM / 64)));
+    for (int i = 0; i < DX; ++i) dma_b128(xb, xoff[i], k, ldsw + at + kTok + i * NT * 16);
+    dma_b32(sb, soff, (uint32_t)b * 4u, lds0 + at + kScale + 256 * (wv % (BM / 64)));
+    if (PF > 0) {
+      u32x4 pb = prow < BN ? wbuf : xbuf;
+      pb.z = b + PF < nb ? pb.z : 0u;
+      dma_b32(pb, poff, k + PF * kQB,
+              (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint32_t*)touched + 256 * wv);
+    }
   };
 
   f32x4 acc[FN][FM];
@@ -228,8 +247,7 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
   // columns of 16 tokens of this wave with rows in them
   const int live = min(FM, max(0, (rows - wm * TM + 15) / 16));
 #pragma unroll
-  for (int b = 0; b < NBUF - 1; ++b)
-    if (b < nb) dma(b);
+  for (int b = 0; b < NBUF; ++b) dma(b);
   // The weight scales of all steps, one per 128 rows of the tile: in LDS, since
   // a load of one in the loop would wait for the DMA under way.  gate_up: the
   // gate's, then the up's.
@@ -247,43 +265,82 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
   auto frag = [&](const uint8_t* p, int row16) {
     return join8(*(const u32x4*)(p + row16 * kQB + c0), *(const u32x4*)(p + row16 * kQB + c1));
   };
-
-  for (int b = 0; b < nb; ++b) {
-    // step b has landed when only the steps after it are under way
-    if (nb - 1 - b >= NBUF - 2) wait_step<(NBUF - 2) * D>();
-    else wait_step<0>();
-    // the buffer of step b + NBUF - 1 was read in step b - 1
-    if (b + NBUF - 1 < nb) dma(b + NBUF - 1);
-    const uint8_t* buf = lds + (b % NBUF) * kBuf;
+  auto buf_at = [&](int b) { return lds + (b % NBUF) * kBuf; };
+  // The next step's first operands, read before its barrier-free part begins:
+  // all token fragments, or two of them where the registers end.
+  constexpr int PRE = FN * FM * 4 + FM * 16 > 160 ? 0 : FM;
+  i32x8 tn[PRE > 0 ? PRE : 1], wnx;
+  auto first = [&](int b) {
+    const uint8_t* buf = buf_at(b);
+    if (PRE > 0) wnx = frag(buf + wn * TN * kQB, 0);
+#pragma unroll
+    for (int j = 0; j < PRE; ++j) tn[j] = frag(buf + kTok + wm * TM * kQB, 16 * j);
+  };
+  auto step = [&](int b, auto last) {
+    const uint8_t* buf = buf_at(b);
     const uint8_t* pw = buf + wn * TN * kQB;
-    const uint8_t* pt = buf + kTok + wm * TM * kQB;
     const float* ps = (const float*)(buf + kScale) + wm * TM + fr;
-    if (live > 0) {
-      Frag<EX> tf[FM];
-      float sx[FM];
+    Frag<EX> tf[FM];
+    float sx[FM];
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      tf[j].set(j < PRE ? tn[j < PRE ? j : 0] : frag(buf + kTok + wm * TM * kQB, 16 * j));
+      sx[j] = ps[16 * j];
+    }
+    i32x8 wc = PRE > 0 ? wnx : frag(pw, 0);
+    const float w0 = wsc[hs][b], w1 = wsc[MODE == kTileGateUp ? 1 : hs][b];
+    float s0[FM], s1[FM];
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      s0[j] = sx[j] * w0;
+      s1[j] = MODE == kTileGateUp ? sx[j] * w1 : s0[j];
+    }
+    // row i's products run while row i - 1's are scaled into the sums
+    f32x4 p[2][FM];
+    auto add = [&](int i) {
 #pragma unroll
       for (int j = 0; j < FM; ++j) {
-        tf[j].set(frag(pt, 16 * j));
-        sx[j] = ps[16 * j];
-      }
-      const float w0 = wsc[hs][b], w1 = wsc[MODE == kTileGateUp ? 1 : hs][b];
+        if (MODE != kTileLinear && j >= live) continue;
+        const float s = (MODE == kTileGateUp && i >= FN / 2) ? s1[j] : s0[j];
 #pragma unroll
-      for (int i = 0; i < FN; ++i) {
-        Frag<EX> wf;
-        wf.set(frag(pw, 16 * i));
-        const float sw = (MODE == kTileGateUp && i >= FN / 2) ? w1 : w0;
+        for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(s, p[i & 1][j][q], acc[i][j][q]);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+      Frag<EX> wf;
+      wf.set(wc);
+      if (i + 1 < FN) wc = frag(pw, 16 * (i + 1));
+      if (i == FN - 2 && !decltype(last)::value) {
+        wait_step<(NBUF - 2) * D + (PF > 0)>();
+        dma(b + NBUF);
+        first(b + 1);
+      }
+#pragma unroll
+      for (int j = 0; j < FM; ++j)
+        if (MODE == kTileLinear || j < live) p[i & 1][j] = mfma128(wf, tf[j]);
+      if (i > 0) add(i - 1);
+      if (MODE == kTileLinear && !EX) {
 #pragma unroll
         for (int j = 0; j < FM; ++j) {
-          if (MODE == kTileLinear || j < live) {
-            const f32x4 p = mfma128(wf, tf[j]);
-            const float s = sx[j] * sw;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(s, p[q], acc[i][j][q]);
-          }
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // one MFMA
+          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);  // four vector operations
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
-  }
+    add(FN - 1);
+  };
+
+  // One barrier a step, before its last two rows of products: the wave has
+  // read the last of buffer b then, so behind it the DMA of step b + NBUF may
+  // go there, and step b + 1 has landed, so its first operands are read while
+  // those products run.
+  wait_step<(NBUF - 1) * D + (PF > 0)>();
+  first(0);
+  for (int b = 0; b + 1 < nb; ++b) step(b, std::false_type{});
+  step(nb - 1, std::true_type{});
+  wait_step<0>();  // nothing is under way to LDS any more
 
   if (MODE == kTileGateUp) {
     // h = silu(gate) up in f32, its absmax over the block's 128 columns (one
@@ -291,7 +348,6 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
     constexpr int HN = FN / 2;
     static_assert(MODE != kTileGateUp || BN == 256, "a tile holds one scale of h");
     float* amax = (float*)lds;                 // [WN][BM]
-    __syncthreads();
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
       float am = 0.f;
@@ -327,25 +383,42 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
       }
     }
   } else {
+    // The wave's part of the output, rounded, through LDS: a lane has 4 columns
+    // of a token, the stores are whole rows of the part (16 bytes a lane).  The
+    // 16-byte chunk c of a row stands at c ^ (row % chunks), for the banks.
+    constexpr int ES = DT == MOE_DT_F32 ? 4 : 2;
+    constexpr int CR = TN * ES / 16;
+    static_assert(TM * TN * ES * NW <= NBUF * kBuf && 64 % CR == 0, "the output's part fits");
+    uint8_t* mine = lds + wv * (TM * TN * ES);
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
-      const int r = wm * TM + 16 * j + fr;
-      bool on = r < rows;
-      if (MODE == kTileDown && on)
-        on = slot_token(a.sorted_slot[m0 + r], a.T, a.topk, a.has_shared) >= 0;
-      if (!on) continue;
+      const int r = 16 * j + fr;
 #pragma unroll
       for (int i = 0; i < FN; ++i) {
-        const int n = n0 + wn * TN + 16 * i + 4 * fq;
-        if (n >= a.N) continue;
-        const size_t at = (size_t)(m0 + r) * a.N + n;
+        const int at = (16 * i + 4 * fq) * ES, c = at / 16;
+        uint8_t* dst = mine + r * (TN * ES) + ((c ^ (r & (CR - 1))) << 4) + (at & 15);
         const f32x4 v = acc[i][j];
         if (DT == MOE_DT_F32)
-          *(f32x4*)((float*)a.out + at) = v;
+          *(f32x4*)dst = v;
         else if (DT == MOE_DT_BF16)
-          *(u32x2*)((uint16_t*)a.out + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+          *(u32x2*)dst = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
         else
-          *(u32x2*)((uint16_t*)a.out + at) = u32x2{pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3])};
+          *(u32x2*)dst = u32x2{pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3])};
+      }
+    }
+    // the wave reads only what it wrote itself
+    __builtin_amdgcn_wave_barrier();
+    const int c = lane % CR, n = n0 + wn * TN + c * (16 / ES);
+    if (n < a.N) {
+#pragma unroll 4
+      for (int r0 = 0; r0 < TM; r0 += 64 / CR) {
+        const int r = r0 + lane / CR, row = wm * TM + r;
+        bool on = row < rows;
+        if (MODE == kTileDown && on)
+          on = slot_token(a.sorted_slot[m0 + row], a.T, a.topk, a.has_shared) >= 0;
+        if (on)
+          *(u32x4*)((uint8_t*)a.out + ((size_t)(m0 + row) * a.N + n) * ES) =
+              *(const u32x4*)(mine + r * (TN * ES) + ((c ^ (r & (CR - 1))) << 4));
       }
     }
   }
@@ -356,14 +429,14 @@ void register_fp8_tile_kernels(std::vector<const void*>& k) {
     constexpr int DT = decltype(D)::value;
     k.push_back((const void*)&k_fp8_quant<DT>);
     if constexpr (DT != MOE_DT_F32)
-      k.push_back((const void*)&k_fp8_tile<kTileLinear, DT, 256, 256, 2, 4, 2>);
+      k.push_back((const void*)&k_fp8_tile<kTileLinear, DT, 256, 256, 2, 4, 2, 0>);
     else
-      k.push_back((const void*)&k_fp8_tile<kTileLinear, DT, 128, 128, 2, 2, 3>);
-    k.push_back((const void*)&k_fp8_tile<kTileLinear, DT, 128, 64, 4, 1, 3>);
+      k.push_back((const void*)&k_fp8_tile<kTileLinear, DT, 128, 128, 2, 2, 3, 0>);
+    k.push_back((const void*)&k_fp8_tile<kTileLinear, DT, 128, 64, 4, 1, 3, 0>);
   };
   for (int dt = MOE_DT_BF16; dt <= MOE_DT_F32; ++dt) by_dtype(dt, add);
-  k.push_back((const void*)&k_fp8_tile<kTileGateUp, MOE_DT_BF16, 256, 128, 4, 2, 3>);
-  k.push_back((const void*)&k_fp8_tile<kTileDown, MOE_DT_BF16, 256, 128, 4, 2, 3>);
+  k.push_back((const void*)&k_fp8_tile<kTileGateUp, MOE_DT_BF16, 256, 128, 4, 2, 3, 0>);
+  k.push_back((const void*)&k_fp8_tile<kTileDown, MOE_DT_BF16, 256, 128, 4, 2, 3, 0>);
 }
 
 hipError_t launch_fp8_quant(const void* x, int T, int K, int dtype, int ldq, uint8_t* codes,
@@ -407,19 +480,19 @@ hipError_t launch_fp8_linear(const moe_fp8_matrix& M, const void* x, int T, int 
     if (big >= 192) {
       if constexpr (DT != MOE_DT_F32) {
         a.nt = (M.N + 255) / 256;
-        MOE_LAUNCH("fp8_tile_256", s, (k_fp8_tile<kTileLinear, DT, 256, 256, 2, 4, 2>),
+        MOE_LAUNCH("fp8_tile_256", s, (k_fp8_tile<kTileLinear, DT, 256, 256, 2, 4, 2, 0>),
                    dim3((unsigned)big), dim3(512), 0, s, a);
       } else {
         // f16 operands take twice the registers
         a.nt = (M.N + 127) / 128;
         const unsigned n = (unsigned)a.nt * (unsigned)((T + 127) / 128);
-        MOE_LAUNCH("fp8_tile_128", s, (k_fp8_tile<kTileLinear, DT, 128, 128, 2, 2, 3>), dim3(n),
+        MOE_LAUNCH("fp8_tile_128", s, (k_fp8_tile<kTileLinear, DT, 128, 128, 2, 2, 3, 0>), dim3(n),
                    dim3(256), 0, s, a);
       }
     } else {
       a.nt = (M.N + 127) / 128;
       const unsigned n = (unsigned)a.nt * (unsigned)((T + 63) / 64);
-      MOE_LAUNCH("fp8_tile_128", s, (k_fp8_tile<kTileLinear, DT, 128, 64, 4, 1, 3>), dim3(n),
+      MOE_LAUNCH("fp8_tile_128", s, (k_fp8_tile<kTileLinear, DT, 128, 64, 4, 1, 3, 0>), dim3(n),
                  dim3(256), 0, s, a);
     }
   });
@@ -463,7 +536,7 @@ hipError_t launch_fp8_expert_ffn(const moe_fp8_weights& W, const uint16_t* x, in
   a.N = W.I;
   a.K = W.H;
   a.nt = W.I / 128;
-  MOE_LAUNCH("fp8_tile_gate_up", s, (k_fp8_tile<kTileGateUp, MOE_DT_BF16, 256, 128, 4, 2, 3>),
+  MOE_LAUNCH("fp8_tile_gate_up", s, (k_fp8_tile<kTileGateUp, MOE_DT_BF16, 256, 128, 4, 2, 3, 0>),
              dim3(mt * a.nt), dim3(512), 0, s, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -476,7 +549,7 @@ hipError_t launch_fp8_expert_ffn(const moe_fp8_weights& W, const uint16_t* x, in
   a.N = W.H;
   a.K = W.I;
   a.nt = (W.H + 255) / 256;
-  MOE_LAUNCH("fp8_tile_down", s, (k_fp8_tile<kTileDown, MOE_DT_BF16, 256, 128, 4, 2, 3>),
+  MOE_LAUNCH("fp8_tile_down", s, (k_fp8_tile<kTileDown, MOE_DT_BF16, 256, 128, 4, 2, 3, 0>),
              dim3(mt * a.nt), dim3(512), 0, s, a);
   return hipGetLastError();
 }
