@@ -109,15 +109,20 @@ __device__ __forceinline__ void wait_step() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// The block's waves meet, each with its LDS reads done.
+__device__ __forceinline__ void meet() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 // NBUF buffers of one K step each: while step b is computed, the steps up to b +
 // NBUF - 1 (at its end b + NBUF) are on their way.
-template <int MODE, int DT, int BN, int BM, int WN, int WM, int NBUF, int PF>
+template <int MODE, int DT, int BN, int BM, int WN, int WM, int NBUF>
 __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
   constexpr int NW = WN * WM, NT = 64 * NW;
   constexpr int TN = BN / WN, TM = BM / WM;    // a wave's part of the tile
   constexpr int FN = TN / 16, FM = TM / 16;
   constexpr int DW = BN * 8 / NT, DX = BM * 8 / NT;  // 16-byte chunks per thread and step
-  constexpr int D = DW + DX + 1 + (PF > 0);    // memory operations per wave and step
+  constexpr int D = DW + DX + 1;               // memory operations per wave and step
   constexpr int kTok = BN * kQB, kScale = kTok + BM * kQB;  // LDS offsets in a buffer
   constexpr int kBuf = kScale + BM * 4;
   constexpr bool EX = DT == MOE_DT_F32;
@@ -128,7 +133,6 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
   constexpr int NS = (BN + kQB - 1) / kQB;     // weight scales of a step
   __shared__ __align__(1024) uint8_t lds[NBUF * kBuf];
   __shared__ float wsc[NS][kMaxNB];
-  __shared__ uint32_t touched[PF > 0 ? NT : 1];  // where the L2 prefetch puts its words
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wv % WN, wm = wv / WN;
@@ -205,37 +209,32 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
   for (int i = 0; i < DX; ++i) xoff[i] = (uint32_t)xrow_of((i * NT + tid) >> 3) * ldx + chunk;
   const int srow = 64 * (wv % (BM / 64)) + lane;  // every wave brings 64 token scales
   const uint32_t soff = (uint32_t)xrow_of(srow) * (uint32_t)nb * 4u;
-  // L2 prefetch: one word of each row's block, a row per lane
-  const int prow = (64 * wv) % (BN + BM);
-  const uint32_t poff = prow < BN ? (uint32_t)wrow_of(prow + lane) * (uint32_t)a.K
-                                  : (uint32_t)xrow_of(prow - BN + lane) * ldx;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
   const uint32_t ldsw = lds0 + wv * 1024;
 
-  // Step b to its buffer.  Past the last step the buffers are empty ones (zeros
-  // come, to where nobody reads): every wave then has the same number of
-  // operations under way at every wait, and the loop has no branch, behind
-  // which the compiler would move the sums of half a step and spill.
-  auto dma = [&](int b) {
+  // Step b's tokens (and their scales), and its weights, to its buffer.  Past
+  // the last step the buffers are empty ones (zeros come, to where nobody
+  // reads): every wave then has the same number of operations under way at
+  // every wait, and the loop has no branch, behind which the compiler would
+  // move the sums of half a step and spill.
+  auto dma_tokens = [&](int b) {
     const uint32_t at = (uint32_t)(b % NBUF) * kBuf, k = (uint32_t)b * kQB;
-    u32x4 wb = wbuf, xb = xbuf, sb = sbuf;
-    wb.z = b < nb ? wb.z : 0u;
+    u32x4 xb = xbuf, sb = sbuf;
     xb.z = b < nb ? xb.z : 0u;
     sb.z = b < nb ? sb.z : 0u;
+#pragma unroll
+    for (int i = 0; i < DX; ++i) dma_b128(xb, xoff[i], k, ldsw + at + kTok + i * NT * 16);
+    dma_b32(sb, soff, (uint32_t)b * 4u, lds0 + at + kScale + 256 * (wv % (BM / 64)));
+  };
+  auto dma_weights = [&](int b) {
+    const uint32_t at = (uint32_t)(b % NBUF) * kBuf, k = (uint32_t)b * kQB;
+    u32x4 wb = wbuf;
+    wb.z = b < nb ? wb.z : 0u;
     // a chunk past the end of a weight row is read from the start of the block
     // instead: the tokens' codes there are zeros
     const uint32_t back = (int)k + chunk >= a.K ? (uint32_t)chunk : 0u;
 #pragma unroll
     for (int i = 0; i < DW; ++i) dma_b128(wb, woff[i] - back, k, ldsw + at + i * NT * 16);
-#pragma unroll
-    for (int i = 0; i < DX; ++i) dma_b128(xb, xoff[i], k, ldsw + at + kTok + i * NT * 16);
-    dma_b32(sb, soff, (uint32_t)b * 4u, lds0 + at + kScale + 256 * (wv % (BM / 64)));
-    if (PF > 0) {
-      u32x4 pb = prow < BN ? wbuf : xbuf;
-      pb.z = b + PF < nb ? pb.z : 0u;
-      dma_b32(pb, poff, k + PF * kQB,
-              (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint32_t*)touched + 256 * wv);
-    }
   };
 
   f32x4 acc[FN][FM];
@@ -247,7 +246,10 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
   // columns of 16 tokens of this wave with rows in them
   const int live = min(FM, max(0, (rows - wm * TM + 15) / 16));
 #pragma unroll
-  for (int b = 0; b < NBUF; ++b) dma(b);
+  for (int b = 0; b < NBUF; ++b) {
+    dma_tokens(b);
+    dma_weights(b);
+  }
   // The weight scales of all steps, one per 128 rows of the tile: in LDS, since
   // a load of one in the loop would wait for the DMA under way.  gate_up: the
   // gate's, then the up's.
@@ -312,14 +314,18 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
       wf.set(wc);
       if (i + 1 < FN) wc = frag(pw, 16 * (i + 1));
       if (i == FN - 2 && !decltype(last)::value) {
-        wait_step<(NBUF - 2) * D + (PF > 0)>();
-        dma(b + NBUF);
+        wait_step<(NBUF - 2) * D + DX + 1>();
+        dma_weights(b + NBUF);
         first(b + 1);
       }
 #pragma unroll
       for (int j = 0; j < FM; ++j)
         if (MODE == kTileLinear || j < live) p[i & 1][j] = mfma128(wf, tf[j]);
       if (i > 0) add(i - 1);
+      if (i == 0 && !decltype(last)::value) {
+        meet();
+        dma_tokens(b + NBUF);
+      }
       if (MODE == kTileLinear && !EX) {
 #pragma unroll
         for (int j = 0; j < FM; ++j) {
@@ -332,11 +338,12 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
     add(FN - 1);
   };
 
-  // One barrier a step, before its last two rows of products: the wave has
-  // read the last of buffer b then, so behind it the DMA of step b + NBUF may
-  // go there, and step b + 1 has landed, so its first operands are read while
-  // those products run.
-  wait_step<(NBUF - 1) * D + (PF > 0)>();
+  // Two barriers a step.  Behind the first product row every wave holds all its
+  // token fragments of the step, so the tokens of step b + NBUF may go to its
+  // buffer; before the last two rows every wave has read the last of the
+  // weights, and the step after has landed (only the tokens just asked for are
+  // under way), so its first operands are read while those products run.
+  wait_step<(NBUF - 1) * D>();
   first(0);
   for (int b = 0; b + 1 < nb; ++b) step(b, std::false_type{});
   step(nb - 1, std::true_type{});
@@ -429,14 +436,14 @@ void register_fp8_tile_kernels(std::vector<const void*>& k) {
     constexpr int DT = decltype(D)::value;
     k.push_back((const void*)&k_fp8_quant<DT>);
     if constexpr (DT != MOE_DT_F32)
-      k.push_back((const void*)&k_fp8_tile<kTileLinear, DT, 256, 256, 2, 4, 2, 0>);
+      k.push_back((const void*)&k_fp8_tile<kTileLinear, DT, 256, 256, 2, 4, 2>);
     else
-      k.push_back((const void*)&k_fp8_tile<kTileLinear, DT, 128, 128, 2, 2, 3, 0>);
-    k.push_back((const void*)&k_fp8_tile<kTileLinear, DT, 128, 64, 4, 1, 3, 0>);
+      k.push_back((const void*)&k_fp8_tile<kTileLinear, DT, 128, 128, 2, 2, 3>);
+    k.push_back((const void*)&k_fp8_tile<kTileLinear, DT, 128, 64, 4, 1, 3>);
   };
   for (int dt = MOE_DT_BF16; dt <= MOE_DT_F32; ++dt) by_dtype(dt, add);
-  k.push_back((const void*)&k_fp8_tile<kTileGateUp, MOE_DT_BF16, 256, 128, 4, 2, 3, 0>);
-  k.push_back((const void*)&k_fp8_tile<kTileDown, MOE_DT_BF16, 256, 128, 4, 2, 3, 0>);
+  k.push_back((const void*)&k_fp8_tile<kTileGateUp, MOE_DT_BF16, 256, 128, 4, 2, 3>);
+  k.push_back((const void*)&k_fp8_tile<kTileDown, MOE_DT_BF16, 256, 128, 4, 2, 3>);
 }
 
 hipError_t launch_fp8_quant(const void* x, int T, int K, int dtype, int ldq, uint8_t* codes,
@@ -480,19 +487,19 @@ hipError_t launch_fp8_linear(const moe_fp8_matrix& M, const void* x, int T, int 
     if (big >= 192) {
       if constexpr (DT != MOE_DT_F32) {
         a.nt = (M.N + 255) / 256;
-        MOE_LAUNCH("fp8_tile_256", s, (k_fp8_tile<kTileLinear, DT, 256, 256, 2, 4, 2, 0>),
+        MOE_LAUNCH("fp8_tile_256", s, (k_fp8_tile<kTileLinear, DT, 256, 256, 2, 4, 2>),
                    dim3((unsigned)big), dim3(512), 0, s, a);
       } else {
         // f16 operands take twice the registers
         a.nt = (M.N + 127) / 128;
         const unsigned n = (unsigned)a.nt * (unsigned)((T + 127) / 128);
-        MOE_LAUNCH("fp8_tile_128", s, (k_fp8_tile<kTileLinear, DT, 128, 128, 2, 2, 3, 0>), dim3(n),
+        MOE_LAUNCH("fp8_tile_128", s, (k_fp8_tile<kTileLinear, DT, 128, 128, 2, 2, 3>), dim3(n),
                    dim3(256), 0, s, a);
       }
     } else {
       a.nt = (M.N + 127) / 128;
       const unsigned n = (unsigned)a.nt * (unsigned)((T + 63) / 64);
-      MOE_LAUNCH("fp8_tile_128", s, (k_fp8_tile<kTileLinear, DT, 128, 64, 4, 1, 3, 0>), dim3(n),
+      MOE_LAUNCH("fp8_tile_128", s, (k_fp8_tile<kTileLinear, DT, 128, 64, 4, 1, 3>), dim3(n),
                  dim3(256), 0, s, a);
     }
   });
@@ -536,7 +543,7 @@ hipError_t launch_fp8_expert_ffn(const moe_fp8_weights& W, const uint16_t* x, in
   a.N = W.I;
   a.K = W.H;
   a.nt = W.I / 128;
-  MOE_LAUNCH("fp8_tile_gate_up", s, (k_fp8_tile<kTileGateUp, MOE_DT_BF16, 256, 128, 4, 2, 3, 0>),
+  MOE_LAUNCH("fp8_tile_gate_up", s, (k_fp8_tile<kTileGateUp, MOE_DT_BF16, 256, 128, 4, 2, 3>),
              dim3(mt * a.nt), dim3(512), 0, s, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -549,7 +556,7 @@ hipError_t launch_fp8_expert_ffn(const moe_fp8_weights& W, const uint16_t* x, in
   a.N = W.H;
   a.K = W.I;
   a.nt = (W.H + 255) / 256;
-  MOE_LAUNCH("fp8_tile_down", s, (k_fp8_tile<kTileDown, MOE_DT_BF16, 256, 128, 4, 2, 3, 0>),
+  MOE_LAUNCH("fp8_tile_down", s, (k_fp8_tile<kTileDown, MOE_DT_BF16, 256, 128, 4, 2, 3>),
              dim3(mt * a.nt), dim3(512), 0, s, a);
   return hipGetLastError();
 }
