@@ -26,14 +26,14 @@ namespace moe {
 // One thread per 8 values, 16 lanes to a block of 128.  ldq: bytes of a code
 // row (K, or K rounded up to 128 with zeros behind).
 template <int DT>
-__global__ __launch_bounds__(256) void k_fp8_quant(const void* __restrict__ x, int T, int K,
-                                                   int ldq, int lg, int cb,
-                                                   uint8_t* __restrict__ codes,
-                                                   float* __restrict__ scales) {
+__device__ __forceinline__ void quant_block(unsigned block, const void* __restrict__ x, int T,
+                                            int K, int ldq, int lg, int cb,
+                                            uint8_t* __restrict__ codes,
+                                            float* __restrict__ scales) {
   constexpr int N = Chunk<DT>::N;
   const int nb = (K + kQB - 1) / kQB;
   int t, c;
-  if (!row_chunk(lg, cb, T, nb * 16, &t, &c)) return;
+  if (!row_chunk(block, lg, cb, T, nb * 16, &t, &c)) return;
   const u32x4* p = (const u32x4*)((const char*)x + (size_t)t * K * (DT == MOE_DT_F32 ? 4 : 2));
   float f[8];
   float am = 0.f;
@@ -63,6 +63,71 @@ __global__ __launch_bounds__(256) void k_fp8_quant(const void* __restrict__ x, i
   if ((c & 15) == 0) scales[(size_t)t * nb + c / 16] = am / 448.0f;
 }
 
+template <int DT>
+__global__ __launch_bounds__(256) void k_fp8_quant(const void* __restrict__ x, int T, int K,
+                                                   int ldq, int lg, int cb,
+                                                   uint8_t* __restrict__ codes,
+                                                   float* __restrict__ scales) {
+  quant_block<DT>(blockIdx.x, x, T, K, ldq, lg, cb, codes, scales);
+}
+
+// The row tiles of the grouped products: items[0] = their number, then from
+// items[4] on {group, first row, rows, 0} of each, in the order of
+// moe_prefill_items.hpp (heaviest first).  One block of 256 threads.
+__device__ __forceinline__ void write_items(const int32_t* __restrict__ offsets, int G,
+                                            int32_t* __restrict__ items) {
+  __shared__ unsigned long long wsum[4];
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int per = (G + 255) / 256;
+  const int lo = min(tid * per, G), hi = min(lo + per, G);
+  auto unit = [](int cnt) {
+    const int rem = cnt % kPM;
+    const int k = (rem > 0 && rem <= 96) ? 4 - (rem + 31) / 32 : 0;
+    return (unsigned long long)(cnt / kPM + (rem > 96 ? 1 : 0)) | (k ? pf_unit(k) : 0ull);
+  };
+  unsigned long long local = 0;
+  for (int g = lo; g < hi; ++g) local += unit(max(offsets[g + 1] - offsets[g], 0));
+  const unsigned long long incl = pf_wave_incl_scan64(local, lane);
+  if (lane == 63) wsum[wv] = incl;
+  __syncthreads();
+  unsigned long long before = 0, total = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    before += (i < wv) ? wsum[i] : 0ull;
+    total += wsum[i];
+  }
+  unsigned long long run = before + incl - local;
+  int first[4], n = 0;
+  for (int k = 0; k < 4; ++k) {
+    first[k] = n;
+    n += pf_field(total, k);
+  }
+  if (tid == 0) items[0] = n;
+  i32x4* list = (i32x4*)(items + 4);
+  for (int g = lo; g < hi; ++g) {
+    const int p0 = offsets[g], cnt = max(offsets[g + 1] - p0, 0);
+    const unsigned long long u = unit(cnt);
+    for (int i = 0, at = first[0] + pf_field(run, 0); i < pf_field(u, 0); ++i)
+      list[at + i] = i32x4{g, p0 + i * kPM, min(kPM, cnt - i * kPM), 0};
+    for (int k = 1; k < 4; ++k)
+      if (pf_field(u, k))
+        list[first[k] + pf_field(run, k)] =
+            i32x4{g, p0 + cnt / kPM * kPM, cnt % kPM, 0};
+    run += u;
+  }
+}
+
+// Quantisation of the experts' token rows (K a multiple of 128) and, in block
+// 0, the list of row tiles.
+__global__ __launch_bounds__(256) void k_fp8_prep(const uint16_t* __restrict__ x, int T, int K,
+                                                  int lg, int cb, uint8_t* __restrict__ codes,
+                                                  float* __restrict__ scales,
+                                                  const int32_t* __restrict__ offsets, int G,
+                                                  int32_t* __restrict__ items) {
+  if (blockIdx.x == 0) write_items(offsets, G, items);
+  else quant_block<MOE_DT_BF16>(blockIdx.x - 1, x, T, K, K, lg, cb, codes, scales);
+}
+
 enum { kTileLinear = 0, kTileGateUp = 1, kTileDown = 2 };
 
 struct TileArgs {
@@ -72,10 +137,10 @@ struct TileArgs {
   const float* xs;         // token scales [rows][nb]
   void* out;
   float* out_scales;       // gate_up: scales of h
-  const int32_t* offsets;  // grouped modes
+  const int32_t* items;    // grouped modes: row tiles (write_items)
   const int32_t* sorted_slot;
   int R;                   // rows (linear)
-  int N, K, T, topk, has_shared, G;
+  int N, K, T, topk, has_shared;
   int nt;                  // tiles along N
 };
 
@@ -131,6 +196,7 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
                 "tile shape");
   constexpr int kMaxNB = (MODE == kTileLinear ? 65536 : 8192) / kQB;
   constexpr int NS = (BN + kQB - 1) / kQB;     // weight scales of a step
+  static_assert(MODE == kTileLinear || BM == kPM, "row tiles of the items");
   __shared__ __align__(1024) uint8_t lds[NBUF * kBuf];
   __shared__ float wsc[NS][kMaxNB];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -154,16 +220,16 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
     n0 = (in / gm) * BN;
     rows = a.R - m0;
   } else {
-    __shared__ unsigned long long base[kPMaxG];
-    __shared__ unsigned long long wsum[NW];
-    PfTile ti;
-    if (!pf_find_tile<NT>(a.offsets, a.G, a.nt, base, wsum, &ti)) return;
+    // the column tiles of one row tile back to back on one XCD
+    const int lin = pf_item_of_block(blockIdx.x, gridDim.x, a.nt), item = lin / a.nt;
+    if (item >= a.items[0]) return;
+    const i32x4 e = ((const i32x4*)(a.items + 4))[item];
     const int nr = MODE == kTileGateUp ? 2 * a.N : a.N;
-    codes += (size_t)ti.g * nr * a.K;
-    scales += (size_t)ti.g * (nr / kQB) * nb;
-    m0 = ti.p0;
-    rows = ti.rows;
-    n0 = ti.nt * (MODE == kTileGateUp ? BN / 2 : BN);
+    codes += (size_t)e.x * nr * a.K;
+    scales += (size_t)e.x * (nr / kQB) * nb;
+    m0 = e.y;
+    rows = e.z;
+    n0 = (lin % a.nt) * (MODE == kTileGateUp ? BN / 2 : BN);
   }
   m0 = __builtin_amdgcn_readfirstlane(m0);
   n0 = __builtin_amdgcn_readfirstlane(n0);
@@ -178,12 +244,12 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
     }
     return min(lr, a.N - 1 - n0);
   };
-  // Row of the token buffer of the tile's row r.
+  // Row of the token buffer of the tile's row r; past the tile's rows one
+  // behind the buffer's end, for which nothing is read.
   auto xrow_of = [&](int r) {
-    r = min(r, rows - 1);
-    if (MODE == kTileGateUp)
-      return max(slot_token(a.sorted_slot[m0 + r], a.T, a.topk, a.has_shared), 0);
-    return r;
+    if (MODE != kTileGateUp) return r;
+    if (r >= rows) return a.T;
+    return max(slot_token(a.sorted_slot[m0 + r], a.T, a.topk, a.has_shared), 0);
   };
   const uint32_t ldx = (uint32_t)nb * kQB;
   u32x4 wbuf = MODE == kTileGateUp
@@ -442,8 +508,9 @@ void register_fp8_tile_kernels(std::vector<const void*>& k) {
     k.push_back((const void*)&k_fp8_tile<kTileLinear, DT, 128, 64, 4, 1, 3>);
   };
   for (int dt = MOE_DT_BF16; dt <= MOE_DT_F32; ++dt) by_dtype(dt, add);
+  k.push_back((const void*)&k_fp8_prep);
   k.push_back((const void*)&k_fp8_tile<kTileGateUp, MOE_DT_BF16, 256, 128, 4, 2, 3>);
-  k.push_back((const void*)&k_fp8_tile<kTileDown, MOE_DT_BF16, 256, 128, 4, 2, 3>);
+  k.push_back((const void*)&k_fp8_tile<kTileDown, MOE_DT_BF16, 128, 128, 2, 2, 2>);
 }
 
 hipError_t launch_fp8_quant(const void* x, int T, int K, int dtype, int ldq, uint8_t* codes,
@@ -506,11 +573,14 @@ hipError_t launch_fp8_linear(const moe_fp8_matrix& M, const void* x, int T, int 
   return hipGetLastError();
 }
 
+// Row tiles of S rows in G groups, at most: the full ones and a partial one per group.
+static size_t max_tiles(size_t S, int G) { return S / kPM + (size_t)G; }
+
 size_t fp8_expert_ffn_workspace_bytes(int T, int K, int H, int I, int has_shared) {
   const size_t S = (size_t)T * K + (has_shared ? T : 0);
   if (T <= kFp8StreamMaxT) return up256(S * I * sizeof(float));
   return up256((size_t)T * H) + up256((size_t)T * (H / kQB) * sizeof(float)) + up256(S * I) +
-         up256(S * (I / kQB) * sizeof(float));
+         up256(S * (I / kQB) * sizeof(float)) + 16 * (max_tiles(S, kPMaxG) + 1);
 }
 
 hipError_t launch_fp8_expert_ffn(const moe_fp8_weights& W, const uint16_t* x, int T, int K,
@@ -523,17 +593,20 @@ hipError_t launch_fp8_expert_ffn(const moe_fp8_weights& W, const uint16_t* x, in
   float* xs = (float*)(xq + up256((size_t)T * W.H));
   uint8_t* hq = (uint8_t*)xs + up256((size_t)T * (W.H / kQB) * sizeof(float));
   float* hs = (float*)(hq + up256(S * W.I));
-  hipError_t e = launch_fp8_quant(x, T, W.H, MOE_DT_BF16, W.H, xq, xs, s);
+  int32_t* items = (int32_t*)((uint8_t*)hs + up256(S * (W.I / kQB) * sizeof(float)));
+  const int G = W.E + W.has_shared;
+  const RowGrid g = row_grid(T, W.H / kQB * 16);
+  MOE_LAUNCH("fp8_prep", s, k_fp8_prep, dim3(g.blocks + 1), dim3(256), 0, s, x, T, W.H, g.lg, g.cb,
+             xq, xs, offsets, G, items);
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   TileArgs a{};
-  a.offsets = offsets;
+  a.items = items;
   a.sorted_slot = sorted_slot;
   a.T = T;
   a.topk = K;
   a.has_shared = W.has_shared;
-  a.G = W.E + W.has_shared;
-  // row tiles: at most one partial tile per group, and the full ones
-  const unsigned mt = (unsigned)(S / kPM + (size_t)a.G);
+  const unsigned mt = (unsigned)max_tiles(S, G);
   a.codes = W.gu_codes;
   a.scales = W.gu_scales;
   a.xq = xq;
@@ -555,9 +628,9 @@ hipError_t launch_fp8_expert_ffn(const moe_fp8_weights& W, const uint16_t* x, in
   a.out_scales = nullptr;
   a.N = W.H;
   a.K = W.I;
-  a.nt = (W.H + 255) / 256;
-  MOE_LAUNCH("fp8_tile_down", s, (k_fp8_tile<kTileDown, MOE_DT_BF16, 256, 128, 4, 2, 3>),
-             dim3(mt * a.nt), dim3(512), 0, s, a);
+  a.nt = W.H / 128;
+  MOE_LAUNCH("fp8_tile_down", s, (k_fp8_tile<kTileDown, MOE_DT_BF16, 128, 128, 2, 2, 2>),
+             dim3(mt * a.nt), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -29,7 +29,7 @@ __global__ __launch_bounds__(256) void k_dispatch(const u32x4* __restrict__ x,
                                                   int K, int cpr, int lg, int cb, int has_shared,
                                                   u32x4* __restrict__ xs) {
   int t, c;
-  if (!row_chunk(lg, cb, T, cpr, &t, &c)) return;
+  if (!row_chunk(blockIdx.x, lg, cb, T, cpr, &t, &c)) return;
   const int TK = T * K;
   const u32x4 v = x[(size_t)t * cpr + c];
   const int32_t* sp = slot_pos + (size_t)t * K;
@@ -54,7 +54,7 @@ __global__ __launch_bounds__(256) void k_slot_sum(const u32x4* __restrict__ y,
                                                   u32x4* __restrict__ out) {
   constexpr int N = Chunk<DT>::N;
   int t, c;
-  if (!row_chunk(lg, cb, T, cpr, &t, &c)) return;
+  if (!row_chunk(blockIdx.x, lg, cb, T, cpr, &t, &c)) return;
   const int TK = T * K;
   float acc[N];
 #pragma unroll

@@ -86,8 +86,8 @@ struct RowGrid {
 };
 
 // This thread's token and chunk; false outside.
-__device__ __forceinline__ bool row_chunk(int lg, int cb, int T, int cpr, int* t, int* c) {
-  const int rb = (int)(blockIdx.x / (unsigned)cb), seg = (int)(blockIdx.x % (unsigned)cb);
+__device__ __forceinline__ bool row_chunk(unsigned block, int lg, int cb, int T, int cpr, int* t, int* c) {
+  const int rb = (int)(block / (unsigned)cb), seg = (int)(block % (unsigned)cb);
   int sub = (int)threadIdx.x >> lg;
   if (lg >= 6) sub = __builtin_amdgcn_readfirstlane(sub);
   *t = (rb << (8 - lg)) + sub;
