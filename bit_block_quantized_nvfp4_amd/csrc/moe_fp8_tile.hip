@@ -338,28 +338,33 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
   // all token fragments, or two of them where the registers end.
   constexpr int PRE = FN * FM * 4 + FM * 16 > 160 ? 0 : FM;
   i32x8 tn[PRE > 0 ? PRE : 1], wnx;
-  auto first = [&](int b) {
+  auto first = [&](int b, auto count) {
+    constexpr int LV = decltype(count)::value;
     const uint8_t* buf = buf_at(b);
-    if (PRE > 0) wnx = frag(buf + wn * TN * kQB, 0);
+    if (PRE > 0 && LV > 0) wnx = frag(buf + wn * TN * kQB, 0);
 #pragma unroll
-    for (int j = 0; j < PRE; ++j) tn[j] = frag(buf + kTok + wm * TM * kQB, 16 * j);
+    for (int j = 0; j < PRE; ++j)
+      if (j < LV) tn[j] = frag(buf + kTok + wm * TM * kQB, 16 * j);
   };
-  auto step = [&](int b, auto last) {
+  auto step = [&](int b, auto last, auto count) {
+    constexpr int LV = decltype(count)::value;
+    constexpr bool kLast = decltype(last)::value;
     const uint8_t* buf = buf_at(b);
     const uint8_t* pw = buf + wn * TN * kQB;
     const float* ps = (const float*)(buf + kScale) + wm * TM + fr;
     Frag<EX> tf[FM];
     float sx[FM];
 #pragma unroll
-    for (int j = 0; j < FM; ++j) {
+    for (int j = 0; j < LV; ++j) {
       tf[j].set(j < PRE ? tn[j < PRE ? j : 0] : frag(buf + kTok + wm * TM * kQB, 16 * j));
       sx[j] = ps[16 * j];
     }
-    i32x8 wc = PRE > 0 ? wnx : frag(pw, 0);
+    i32x8 wc = {};
+    if (LV > 0) wc = PRE > 0 ? wnx : frag(pw, 0);
     const float w0 = wsc[hs][b], w1 = wsc[MODE == kTileGateUp ? 1 : hs][b];
     float s0[FM], s1[FM];
 #pragma unroll
-    for (int j = 0; j < FM; ++j) {
+    for (int j = 0; j < LV; ++j) {
       s0[j] = sx[j] * w0;
       s1[j] = MODE == kTileGateUp ? sx[j] * w1 : s0[j];
     }
@@ -367,8 +372,7 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
     f32x4 p[2][FM];
     auto add = [&](int i) {
 #pragma unroll
-      for (int j = 0; j < FM; ++j) {
-        if (MODE != kTileLinear && j >= live) continue;
+      for (int j = 0; j < LV; ++j) {
         const float s = (MODE == kTileGateUp && i >= FN / 2) ? s1[j] : s0[j];
 #pragma unroll
         for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(s, p[i & 1][j][q], acc[i][j][q]);
@@ -378,23 +382,22 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
     for (int i = 0; i < FN; ++i) {
       Frag<EX> wf;
       wf.set(wc);
-      if (i + 1 < FN) wc = frag(pw, 16 * (i + 1));
-      if (i == FN - 2 && !decltype(last)::value) {
+      if (LV > 0 && i + 1 < FN) wc = frag(pw, 16 * (i + 1));
+      if (i == FN - 2 && !kLast) {
         wait_step<(NBUF - 2) * D + DX + 1>();
         dma_weights(b + NBUF);
-        first(b + 1);
+        first(b + 1, count);
       }
 #pragma unroll
-      for (int j = 0; j < FM; ++j)
-        if (MODE == kTileLinear || j < live) p[i & 1][j] = mfma128(wf, tf[j]);
+      for (int j = 0; j < LV; ++j) p[i & 1][j] = mfma128(wf, tf[j]);
       if (i > 0) add(i - 1);
-      if (i == 0 && !decltype(last)::value) {
+      if (i == 0 && !kLast) {
         meet();
         dma_tokens(b + NBUF);
       }
-      if (MODE == kTileLinear && !EX) {
+      if (!EX) {
 #pragma unroll
-        for (int j = 0; j < FM; ++j) {
+        for (int j = 0; j < LV; ++j) {
           __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // one MFMA
           __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);  // four vector operations
         }
@@ -410,9 +413,24 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
   // weights, and the step after has landed (only the tokens just asked for are
   // under way), so its first operands are read while those products run.
   wait_step<(NBUF - 1) * D>();
-  first(0);
-  for (int b = 0; b + 1 < nb; ++b) step(b, std::false_type{});
-  step(nb - 1, std::true_type{});
+  auto run = [&](auto count) {
+    first(0, count);
+    for (int b = 0; b + 1 < nb; ++b) step(b, std::false_type{}, count);
+    step(nb - 1, std::true_type{}, count);
+  };
+  // A wave computes only its columns of 16 tokens with rows in them, in a loop
+  // made for their number: a test at each product would break up the schedule.
+  // Every such loop has the same barriers.
+  if constexpr (MODE == kTileLinear) {
+    run(IntC<FM>{});
+  } else {
+    static_assert(FM == 4, "the loops below");
+    if (live == 4) run(IntC<4>{});
+    else if (live == 3) run(IntC<3>{});
+    else if (live == 2) run(IntC<2>{});
+    else if (live == 1) run(IntC<1>{});
+    else run(IntC<0>{});
+  }
   wait_step<0>();  // nothing is under way to LDS any more
 
   if (MODE == kTileGateUp) {
