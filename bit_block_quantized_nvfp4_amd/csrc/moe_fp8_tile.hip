@@ -72,19 +72,22 @@ __global__ __launch_bounds__(256) void k_fp8_quant(const void* __restrict__ x, i
 }
 
 // The row tiles of the grouped products: items[0] = their number, then from
-// items[4] on {group, first row, rows, 0} of each, in the order of
-// moe_prefill_items.hpp (heaviest first).  One block of 256 threads.
+// items[4] on {group, first row, rows, 1 if the group has no other tile} of
+// each.  Groups of several tiles come first, a group's tiles one after the
+// other (its weights are then still near when the next tile reads them: T =
+// 16384 gate_up 682 us, 705 us with all full tiles first), then the others by
+// the number of 32-row parts, so that the short ones fill the launch's end.
+// One block of 256 threads.
 __device__ __forceinline__ void write_items(const int32_t* __restrict__ offsets, int G,
                                             int32_t* __restrict__ items) {
   __shared__ unsigned long long wsum[4];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int per = (G + 255) / 256;
   const int lo = min(tid * per, G), hi = min(lo + per, G);
-  auto unit = [](int cnt) {
-    const int rem = cnt % kPM;
-    const int k = (rem > 0 && rem <= 96) ? 4 - (rem + 31) / 32 : 0;
-    return (unsigned long long)(cnt / kPM + (rem > 96 ? 1 : 0)) | (k ? pf_unit(k) : 0ull);
-  };
+  // a group of more than one tile: all of them in class 0
+  auto tiles = [](int cnt) { return (cnt + kPM - 1) / kPM; };
+  auto cls = [](int cnt) { return cnt > kPM ? 0 : 4 - (cnt + 31) / 32; };
+  auto unit = [&](int cnt) { return cnt > 0 ? (unsigned long long)tiles(cnt) * pf_unit(cls(cnt)) : 0ull; };
   unsigned long long local = 0;
   for (int g = lo; g < hi; ++g) local += unit(max(offsets[g + 1] - offsets[g], 0));
   const unsigned long long incl = pf_wave_incl_scan64(local, lane);
@@ -106,14 +109,11 @@ __device__ __forceinline__ void write_items(const int32_t* __restrict__ offsets,
   i32x4* list = (i32x4*)(items + 4);
   for (int g = lo; g < hi; ++g) {
     const int p0 = offsets[g], cnt = max(offsets[g + 1] - p0, 0);
-    const unsigned long long u = unit(cnt);
-    for (int i = 0, at = first[0] + pf_field(run, 0); i < pf_field(u, 0); ++i)
-      list[at + i] = i32x4{g, p0 + i * kPM, min(kPM, cnt - i * kPM), 0};
-    for (int k = 1; k < 4; ++k)
-      if (pf_field(u, k))
-        list[first[k] + pf_field(run, k)] =
-            i32x4{g, p0 + cnt / kPM * kPM, cnt % kPM, 0};
-    run += u;
+    if (cnt == 0) continue;
+    const int k = cls(cnt), at = first[k] + pf_field(run, k);
+    for (int i = 0; i < tiles(cnt); ++i)
+      list[at + i] = i32x4{g, p0 + i * kPM, min(kPM, cnt - i * kPM), cnt <= kPM};
+    run += unit(cnt);
   }
 }
 
@@ -142,7 +142,14 @@ struct TileArgs {
   int R;                   // rows (linear)
   int N, K, T, topk, has_shared;
   int nt;                  // tiles along N
+  int ntb;                 // of them per block (grouped modes), a divisor of nt
 };
+
+// Weight scales of a block's steps in LDS, times the scales of a step: K up to
+// 65536 for one tile, or ntb * K / 128 of a bank's (K up to 8192, ntb up to 8).
+constexpr int kTileScales = 512;
+// Blocks that a grouped launch keeps at least when its blocks take several tiles.
+constexpr size_t kStreamBlocks = 2048;
 
 // Buffer descriptor of `bytes` bytes at p (both wave-uniform): loads past the
 // end return zeros.
@@ -156,15 +163,24 @@ __device__ __forceinline__ u32x4 buf_of(const void* p, uint32_t bytes) {
 // lds + 16 l (4 l).  No register is written.  In asm because the compiler
 // would wait for every such load before the next LDS read of any buffer; the
 // kernel's own waits below order them.  m0 is reserved: the compiler keeps
-// nothing in it, and nothing else here uses it.
+// nothing in it, and nothing else here uses it.  The wait states are those a
+// memory instruction needs after m0, or a scalar register that a vector
+// instruction wrote (the descriptor's), was written.  ONCE: the bytes are not
+// read again (non-temporal).
+template <bool ONCE = false>
 __device__ __forceinline__ void dma_b128(u32x4 buf, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds),
-               "v"(voff), "s"(buf), "s"(soff)
-               : "memory");
+  if (ONCE)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds" ::"s"(lds),
+                 "v"(voff), "s"(buf), "s"(__builtin_amdgcn_readfirstlane((int)soff))
+                 : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds),
+                 "v"(voff), "s"(buf), "s"(__builtin_amdgcn_readfirstlane((int)soff))
+                 : "memory");
 }
 __device__ __forceinline__ void dma_b32(u32x4 buf, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds),
-               "v"(voff), "s"(buf), "s"(soff)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds),
+               "v"(voff), "s"(buf), "s"(__builtin_amdgcn_readfirstlane((int)soff))
                : "memory");
 }
 // All but the wave's last N memory operations are done, and all its LDS reads;
@@ -179,8 +195,11 @@ __device__ __forceinline__ void meet() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// NBUF buffers of one K step each: while step b is computed, the steps up to b +
-// NBUF - 1 (at its end b + NBUF) are on their way.
+// A block computes a.ntb tiles of BN weight rows side by side (grouped modes; one
+// in the linear mode) for one tile of BM tokens: a stream of ntb * nb steps,
+// one block of 128 along K each, through NBUF buffers.  While step s is
+// computed, the steps up to s + NBUF are on their way, across the ends of
+// tiles, so the output of a tile is written while the next one's operands come.
 template <int MODE, int DT, int BN, int BM, int WN, int WM, int NBUF>
 __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
   constexpr int NW = WN * WM, NT = 64 * NW;
@@ -191,22 +210,29 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
   constexpr int kTok = BN * kQB, kScale = kTok + BM * kQB;  // LDS offsets in a buffer
   constexpr int kBuf = kScale + BM * 4;
   constexpr bool EX = DT == MOE_DT_F32;
-  static_assert(BN * 8 % NT == 0 && BM * 8 % NT == 0 && TN % 16 == 0 && TM % 16 == 0 &&
-                    BM % 64 == 0 && BM / 64 <= NW && (NBUF - 1) * D < 64 && FN >= 2,
-                "tile shape");
-  constexpr int kMaxNB = (MODE == kTileLinear ? 65536 : 8192) / kQB;
+  constexpr int ES = DT == MOE_DT_F32 ? 4 : 2;
+  constexpr int CR = TN * ES / 16;             // 16-byte chunks of a row of the wave's output
   constexpr int NS = (BN + kQB - 1) / kQB;     // weight scales of a step
+  constexpr int BC = MODE == kTileGateUp ? BN / 2 : BN;  // columns of a tile
+  static_assert(BN * 8 % NT == 0 && BM * 8 % NT == 0 && TN % 16 == 0 && TM % 16 == 0 &&
+                    BM % 64 == 0 && BM / 64 <= NW && NBUF * D < 64 && FN >= 2 && 64 % CR == 0,
+                "tile shape");
   static_assert(MODE == kTileLinear || BM == kPM, "row tiles of the items");
+  static_assert(MODE != kTileGateUp || BC == kQB, "a tile holds one scale of h");
   __shared__ __align__(1024) uint8_t lds[NBUF * kBuf];
-  __shared__ float wsc[NS][kMaxNB];
+  __shared__ float wsc[NS * kTileScales];
+  __shared__ __align__(16) uint8_t side[MODE == kTileGateUp ? WN * BM * 4
+                                        : MODE == kTileDown ? NW * 16 * TN * ES : 16];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wv % WN, wm = wv / WN;
   const int nb = (a.K + kQB - 1) / kQB;
+  const int ntb = MODE == kTileLinear ? 1 : a.ntb;
 
   const uint8_t* codes = a.codes;
   const float* scales = a.scales;
   int m0, rows, n0;                            // first token row, rows left, first column
+  bool single = false;                         // the group has no other row tile
   if (MODE == kTileLinear) {
     // Blocks are dealt to the 8 XCDs in turn: give each XCD a run of tiles, and
     // let a run go 8 token tiles deep before its next weight tile, so that the
@@ -221,15 +247,18 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
     rows = a.R - m0;
   } else {
     // the column tiles of one row tile back to back on one XCD
-    const int lin = pf_item_of_block(blockIdx.x, gridDim.x, a.nt), item = lin / a.nt;
-    if (item >= a.items[0]) return;
+    const int per = a.nt / ntb;
+    const int lin = pf_item_of_block(blockIdx.x, gridDim.x, per), item = lin / per;
+    const int n = a.items[0];
     const i32x4 e = ((const i32x4*)(a.items + 4))[item];
+    if (item >= n) return;
     const int nr = MODE == kTileGateUp ? 2 * a.N : a.N;
     codes += (size_t)e.x * nr * a.K;
     scales += (size_t)e.x * (nr / kQB) * nb;
     m0 = e.y;
     rows = e.z;
-    n0 = (lin % a.nt) * (MODE == kTileGateUp ? BN / 2 : BN);
+    single = __builtin_amdgcn_readfirstlane(e.w) != 0;
+    n0 = (lin % per) * ntb * BC;
   }
   m0 = __builtin_amdgcn_readfirstlane(m0);
   n0 = __builtin_amdgcn_readfirstlane(n0);
@@ -237,7 +266,7 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
 
   // Weight row (from the buffer's base) of LDS row lr.  gate_up: each wave's TN
   // rows are TN / 2 gate rows and the up rows of the same columns.
-  auto wrow_of = [&](int lr) {
+  auto wrow_of = [&](int lr) __attribute__((always_inline)) {
     if (MODE == kTileGateUp) {
       const int w = lr / TN, q = lr % TN;
       return n0 + w * (TN / 2) + q % (TN / 2) + (q < TN / 2 ? 0 : a.N);
@@ -246,24 +275,21 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
   };
   // Row of the token buffer of the tile's row r; past the tile's rows one
   // behind the buffer's end, for which nothing is read.
-  auto xrow_of = [&](int r) {
+  auto xrow_of = [&](int r) __attribute__((always_inline)) {
     if (MODE != kTileGateUp) return r;
     if (r >= rows) return a.T;
     return max(slot_token(a.sorted_slot[m0 + r], a.T, a.topk, a.has_shared), 0);
   };
   const uint32_t ldx = (uint32_t)nb * kQB;
-  u32x4 wbuf = MODE == kTileGateUp
-                         ? buf_of(codes, (uint32_t)(2 * a.N) * (uint32_t)a.K)
-                         : buf_of(codes + (size_t)n0 * a.K,
-                                  (uint32_t)min(BN, a.N - n0) * (uint32_t)a.K);
-  u32x4 xbuf = MODE == kTileGateUp ? buf_of(a.xq, (uint32_t)a.T * ldx)
-                                         : buf_of(a.xq + (size_t)m0 * ldx, (uint32_t)rows * ldx);
-  u32x4 sbuf = MODE == kTileGateUp
-                         ? buf_of(a.xs, (uint32_t)a.T * (uint32_t)nb * 4u)
-                         : buf_of(a.xs + (size_t)m0 * nb, (uint32_t)rows * (uint32_t)nb * 4u);
-  // a memory instruction may read scalar registers that a vector instruction
-  // wrote (the descriptors') only 5 states later; in asm that is for us to keep
-  asm volatile("s_nop 4" : "+s"(wbuf), "+s"(xbuf), "+s"(sbuf));
+  const u32x4 wbuf = MODE == kTileGateUp
+                   ? buf_of(codes, (uint32_t)(2 * a.N) * (uint32_t)a.K)
+                   : buf_of(codes + (size_t)n0 * a.K,
+                            (uint32_t)min(BN * ntb, a.N - n0) * (uint32_t)a.K);
+  const u32x4 xbuf = MODE == kTileGateUp ? buf_of(a.xq, (uint32_t)a.T * ldx)
+                                   : buf_of(a.xq + (size_t)m0 * ldx, (uint32_t)rows * ldx);
+  const u32x4 sbuf = MODE == kTileGateUp
+                   ? buf_of(a.xs, (uint32_t)a.T * (uint32_t)nb * 4u)
+                   : buf_of(a.xs + (size_t)m0 * nb, (uint32_t)rows * (uint32_t)nb * 4u);
   // Chunk i of this thread: LDS row lr, place tid % 8; rows of one thread are
   // NT / 8 apart, a multiple of 8, so its chunk of the row is always the same.
   const int chunk = 16 * ((tid & 7) ^ ((tid >> 3) & 7));
@@ -278,99 +304,118 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
   const uint32_t ldsw = lds0 + wv * 1024;
 
-  // Step b's tokens (and their scales), and its weights, to its buffer.  Past
-  // the last step the buffers are empty ones (zeros come, to where nobody
-  // reads): every wave then has the same number of operations under way at
-  // every wait, and the loop has no branch, behind which the compiler would
-  // move the sums of half a step and spill.
-  auto dma_tokens = [&](int b) {
-    const uint32_t at = (uint32_t)(b % NBUF) * kBuf, k = (uint32_t)b * kQB;
-    u32x4 xb = xbuf, sb = sbuf;
-    xb.z = b < nb ? xb.z : 0u;
-    sb.z = b < nb ? sb.z : 0u;
+  // The weight scales of all steps, one per 128 weight rows of a tile, in LDS: a
+  // load of one in the loop would wait for the DMA under way.  gate_up: the
+  // gate's, then the up's.
+  for (int i = tid; i < ntb * NS * nb; i += NT) {
+    const int tile = i / (NS * nb), h = i / nb % NS, b = i % nb;
+    const int row = n0 + tile * BC + (MODE == kTileGateUp ? h * a.N : h * kQB);
+    wsc[i] = scales[(size_t)((MODE == kTileGateUp ? row : min(row, a.N - 1)) / kQB) * nb + b];
+  }
+  // rows of this lane's stores that belong to a slot, a bit each
+  uint32_t mine_ok = ~0u;
+  if (MODE == kTileDown) {
+    mine_ok = 0;
 #pragma unroll
-    for (int i = 0; i < DX; ++i) dma_b128(xb, xoff[i], k, ldsw + at + kTok + i * NT * 16);
-    dma_b32(sb, soff, (uint32_t)b * 4u, lds0 + at + kScale + 256 * (wv % (BM / 64)));
+    for (int i = 0; i < TM * CR / 64; ++i) {
+      const int row = wm * TM + i * (64 / CR) + lane / CR;
+      if (row < rows && slot_token(a.sorted_slot[m0 + row], a.T, a.topk, a.has_shared) >= 0)
+        mine_ok |= 1u << i;
+    }
+  }
+
+  // The next step to bring: how many are left, its block along K and buffer.
+  // Tokens (with their scales) and weights of a step are asked for at different
+  // times, tokens first.  Past the last step the buffers are empty ones (zeros
+  // come, to where nobody reads): every wave then has the same number of
+  // operations under way at every wait, and the loop has no branch, behind
+  // which the compiler would move the sums of half a step and spill.
+  int d_left = ntb * nb, d_k = 0, d_at = 0;
+  uint32_t d_col = 0;                          // offset of the tile's weights
+  auto dma_tokens = [&]() __attribute__((always_inline)) {
+    u32x4 xb = xbuf, sb = sbuf;
+    xb.z = d_left > 0 ? xb.z : 0u;
+    sb.z = d_left > 0 ? sb.z : 0u;
+#pragma unroll
+    for (int i = 0; i < DX; ++i)
+      dma_b128(xb, xoff[i], (uint32_t)d_k * kQB, ldsw + d_at + kTok + i * NT * 16);
+    dma_b32(sb, soff, (uint32_t)d_k * 4u, lds0 + d_at + kScale + 256 * (wv % (BM / 64)));
   };
-  auto dma_weights = [&](int b) {
-    const uint32_t at = (uint32_t)(b % NBUF) * kBuf, k = (uint32_t)b * kQB;
+  auto dma_weights = [&](auto once) __attribute__((always_inline)) {
     u32x4 wb = wbuf;
-    wb.z = b < nb ? wb.z : 0u;
+    wb.z = d_left > 0 ? wb.z : 0u;
+    const uint32_t k = (uint32_t)d_k * kQB;
     // a chunk past the end of a weight row is read from the start of the block
     // instead: the tokens' codes there are zeros
-    const uint32_t back = (int)k + chunk >= a.K ? (uint32_t)chunk : 0u;
+    const uint32_t back = MODE == kTileLinear && (int)k + chunk >= a.K ? (uint32_t)chunk : 0u;
+    const uint32_t so = MODE == kTileLinear ? k : k + d_col;
 #pragma unroll
-    for (int i = 0; i < DW; ++i) dma_b128(wb, woff[i] - back, k, ldsw + at + i * NT * 16);
+    for (int i = 0; i < DW; ++i) dma_b128<decltype(once)::value>(wb, woff[i] - back, so, ldsw + d_at + i * NT * 16);
+    --d_left;
+    d_at = d_at == (NBUF - 1) * kBuf ? 0 : d_at + kBuf;
+    ++d_k;
+    if (MODE != kTileLinear) {
+      d_col += d_k == nb ? (uint32_t)BC * (uint32_t)a.K : 0u;
+      d_k = d_k == nb ? 0 : d_k;
+    }
   };
-
-  f32x4 acc[FN][FM];
-#pragma unroll
-  for (int i = 0; i < FN; ++i)
-#pragma unroll
-    for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  // columns of 16 tokens of this wave with rows in them
-  const int live = min(FM, max(0, (rows - wm * TM + 15) / 16));
 #pragma unroll
   for (int b = 0; b < NBUF; ++b) {
-    dma_tokens(b);
-    dma_weights(b);
+    dma_tokens();
+    dma_weights(std::false_type{});
   }
-  // The weight scales of all steps, one per 128 rows of the tile: in LDS, since
-  // a load of one in the loop would wait for the DMA under way.  gate_up: the
-  // gate's, then the up's.
-  for (int i = tid; i < NS * nb; i += NT) {
-    const int h = i / nb, b = i % nb;
-    const int row = MODE == kTileGateUp ? n0 + h * a.N : min(n0 + h * kQB, a.N - 1);
-    wsc[h][b] = scales[(size_t)(row / kQB) * nb + b];
-  }
+
+  f32x4 acc[FN][FM];
+  // columns of 16 tokens of this wave with rows in them
+  const int live = min(FM, max(0, (rows - wm * TM + 15) / 16));
   const int hs = MODE == kTileGateUp ? 0 : wn * TN / kQB;
 
   // this lane's two chunks of row 16 i + lane % 16
   const int fr = lane & 15, fq = lane >> 4;
   const uint32_t c0 = (uint32_t)(fr * kQB + ((fq ^ (fr & 7)) << 4));
   const uint32_t c1 = (uint32_t)(fr * kQB + (((fq + 4) ^ (fr & 7)) << 4));
-  auto frag = [&](const uint8_t* p, int row16) {
+  auto frag = [&](const uint8_t* p, int row16) __attribute__((always_inline)) {
     return join8(*(const u32x4*)(p + row16 * kQB + c0), *(const u32x4*)(p + row16 * kQB + c1));
   };
-  auto buf_at = [&](int b) { return lds + (b % NBUF) * kBuf; };
-  // The next step's first operands, read before its barrier-free part begins:
-  // all token fragments, or two of them where the registers end.
+  // The next step's first operands, read while the last products of a step run
+  // (none where the registers end before).
   constexpr int PRE = FN * FM * 4 + FM * 16 > 160 ? 0 : FM;
   i32x8 tn[PRE > 0 ? PRE : 1], wnx;
-  auto first = [&](int b, auto count) {
+  auto first = [&](int at, auto count) __attribute__((always_inline)) {
     constexpr int LV = decltype(count)::value;
-    const uint8_t* buf = buf_at(b);
-    if (PRE > 0 && LV > 0) wnx = frag(buf + wn * TN * kQB, 0);
+    if (PRE > 0 && LV > 0) wnx = frag(lds + at + wn * TN * kQB, 0);
 #pragma unroll
     for (int j = 0; j < PRE; ++j)
-      if (j < LV) tn[j] = frag(buf + kTok + wm * TM * kQB, 16 * j);
+      if (j < LV) tn[j] = frag(lds + at + kTok + wm * TM * kQB, 16 * j);
   };
-  auto step = [&](int b, auto last, auto count) {
+  // Step at buffer `at`, whose weight scales are sc[0] and (gate_up: the up
+  // rows') sc[nb].  Two barriers: behind the first product row every wave holds
+  // all its token fragments, so the next tokens may go to their buffer; before
+  // the last two rows every wave has read the last of the weights, and the step
+  // after has landed (what was asked for later may be under way), so its first
+  // operands are read while those products run.  Two product rows: one barrier.
+  auto step = [&](int at, const float* sc, auto last, auto count, auto once) __attribute__((always_inline)) {
     constexpr int LV = decltype(count)::value;
     constexpr bool kLast = decltype(last)::value;
-    const uint8_t* buf = buf_at(b);
-    const uint8_t* pw = buf + wn * TN * kQB;
-    const float* ps = (const float*)(buf + kScale) + wm * TM + fr;
+    const uint8_t* pw = lds + at + wn * TN * kQB;
+    const uint8_t* pt = lds + at + kTok + wm * TM * kQB;
+    const float* ps = (const float*)(lds + at + kScale) + wm * TM + fr;
+    const int next = at == (NBUF - 1) * kBuf ? 0 : at + kBuf;
     Frag<EX> tf[FM];
-    float sx[FM];
+    float s0[FM], s1[FM];
+    const float w0 = sc[0], w1 = MODE == kTileGateUp ? sc[nb] : 0.f;
 #pragma unroll
     for (int j = 0; j < LV; ++j) {
-      tf[j].set(j < PRE ? tn[j < PRE ? j : 0] : frag(buf + kTok + wm * TM * kQB, 16 * j));
-      sx[j] = ps[16 * j];
+      tf[j].set(j < PRE ? tn[j < PRE ? j : 0] : frag(pt, 16 * j));
+      const float sx = ps[16 * j];
+      s0[j] = sx * w0;
+      s1[j] = MODE == kTileGateUp ? sx * w1 : s0[j];
     }
     i32x8 wc = {};
     if (LV > 0) wc = PRE > 0 ? wnx : frag(pw, 0);
-    const float w0 = wsc[hs][b], w1 = wsc[MODE == kTileGateUp ? 1 : hs][b];
-    float s0[FM], s1[FM];
-#pragma unroll
-    for (int j = 0; j < LV; ++j) {
-      s0[j] = sx[j] * w0;
-      s1[j] = MODE == kTileGateUp ? sx[j] * w1 : s0[j];
-    }
     // row i's products run while row i - 1's are scaled into the sums
     f32x4 p[2][FM];
-    auto add = [&](int i) {
+    auto add = [&](int i) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < LV; ++j) {
         const float s = (MODE == kTileGateUp && i >= FN / 2) ? s1[j] : s0[j];
@@ -384,16 +429,17 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
       wf.set(wc);
       if (LV > 0 && i + 1 < FN) wc = frag(pw, 16 * (i + 1));
       if (i == FN - 2 && !kLast) {
-        wait_step<(NBUF - 2) * D + DX + 1>();
-        dma_weights(b + NBUF);
-        first(b + 1, count);
+        wait_step<(NBUF - 2) * D + (FN > 2 ? DX + 1 : 0)>();
+        if (FN == 2) dma_tokens();
+        dma_weights(once);
+        first(next, count);
       }
 #pragma unroll
       for (int j = 0; j < LV; ++j) p[i & 1][j] = mfma128(wf, tf[j]);
       if (i > 0) add(i - 1);
-      if (i == 0 && !kLast) {
+      if (FN > 2 && i == 0 && !kLast) {
         meet();
-        dma_tokens(b + NBUF);
+        dma_tokens();
       }
       if (!EX) {
 #pragma unroll
@@ -407,40 +453,14 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
     add(FN - 1);
   };
 
-  // Two barriers a step.  Behind the first product row every wave holds all its
-  // token fragments of the step, so the tokens of step b + NBUF may go to its
-  // buffer; before the last two rows every wave has read the last of the
-  // weights, and the step after has landed (only the tokens just asked for are
-  // under way), so its first operands are read while those products run.
-  wait_step<(NBUF - 1) * D>();
-  auto run = [&](auto count) {
-    first(0, count);
-    for (int b = 0; b + 1 < nb; ++b) step(b, std::false_type{}, count);
-    step(nb - 1, std::true_type{}, count);
-  };
-  // A wave computes only its columns of 16 tokens with rows in them, in a loop
-  // made for their number: a test at each product would break up the schedule.
-  // Every such loop has the same barriers.
-  if constexpr (MODE == kTileLinear) {
-    run(IntC<FM>{});
-  } else {
-    static_assert(FM == 4, "the loops below");
-    if (live == 4) run(IntC<4>{});
-    else if (live == 3) run(IntC<3>{});
-    else if (live == 2) run(IntC<2>{});
-    else if (live == 1) run(IntC<1>{});
-    else run(IntC<0>{});
-  }
-  wait_step<0>();  // nothing is under way to LDS any more
-
-  if (MODE == kTileGateUp) {
-    // h = silu(gate) up in f32, its absmax over the block's 128 columns (one
-    // scale of h), then its codes
+  // gate_up: h = silu(gate) up in f32, its absmax over the tile's 128 columns
+  // (one scale of h), then its codes.  n: the tile's first column.
+  auto put_h = [&](int n, auto count) __attribute__((always_inline)) {
+    constexpr int LV = decltype(count)::value;
     constexpr int HN = FN / 2;
-    static_assert(MODE != kTileGateUp || BN == 256, "a tile holds one scale of h");
-    float* amax = (float*)lds;                 // [WN][BM]
+    float* amax = (float*)side;                // [WN][BM]
 #pragma unroll
-    for (int j = 0; j < FM; ++j) {
+    for (int j = 0; j < LV; ++j) {
       float am = 0.f;
 #pragma unroll
       for (int i = 0; i < HN; ++i)
@@ -454,9 +474,9 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
       am = fmaxf(am, __shfl_xor(am, 32));
       if (fq == 0) amax[wn * BM + wm * TM + 16 * j + fr] = am;
     }
-    __syncthreads();
+    meet();
 #pragma unroll
-    for (int j = 0; j < FM; ++j) {
+    for (int j = 0; j < LV; ++j) {
       const int r = wm * TM + 16 * j + fr;
       float am = amax[r];
 #pragma unroll
@@ -464,30 +484,30 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
       am = q_floor(am);
       const float m = 448.0f / am;
       if (r < rows) {
-        uint8_t* dst = (uint8_t*)a.out + (size_t)(m0 + r) * a.N + n0 + wn * (TN / 2);
+        uint8_t* dst = (uint8_t*)a.out + (size_t)(m0 + r) * a.N + n + wn * (TN / 2);
 #pragma unroll
         for (int i = 0; i < HN; ++i)
           *(uint32_t*)(dst + 16 * i + 4 * fq) = fp8x4(acc[i][j][0] * m, acc[i][j][1] * m,
                                                       acc[i][j][2] * m, acc[i][j][3] * m);
         if (wn == 0 && fq == 0)
-          a.out_scales[(size_t)(m0 + r) * (a.N / kQB) + n0 / kQB] = am / 448.0f;
+          a.out_scales[(size_t)(m0 + r) * (a.N / kQB) + n / kQB] = am / 448.0f;
       }
     }
-  } else {
-    // The wave's part of the output, rounded, through LDS: a lane has 4 columns
-    // of a token, the stores are whole rows of the part (16 bytes a lane).  The
-    // 16-byte chunk c of a row stands at c ^ (row % chunks), for the banks.
-    constexpr int ES = DT == MOE_DT_F32 ? 4 : 2;
-    constexpr int CR = TN * ES / 16;
-    static_assert(TM * TN * ES * NW <= NBUF * kBuf && 64 % CR == 0, "the output's part fits");
-    uint8_t* mine = lds + wv * (TM * TN * ES);
+  };
+  // The wave's part of the output, rounded, 16 tokens at a time through LDS of
+  // its own: a lane has 4 columns of a token, the stores are whole rows of the
+  // part (16 bytes a lane).  The 16-byte chunk c of a row stands at
+  // c ^ (row % chunks), for the banks.  A wave's LDS operations keep their order.
+  auto put_out = [&](int n, auto count) __attribute__((always_inline)) {
+    constexpr int LV = decltype(count)::value;
+    uint8_t* mine = (MODE == kTileDown ? side : lds) + wv * (16 * TN * ES);
+    const int c = lane % CR, nc = n + wn * TN + c * (16 / ES);
 #pragma unroll
-    for (int j = 0; j < FM; ++j) {
-      const int r = 16 * j + fr;
+    for (int j = 0; j < LV; ++j) {
 #pragma unroll
       for (int i = 0; i < FN; ++i) {
-        const int at = (16 * i + 4 * fq) * ES, c = at / 16;
-        uint8_t* dst = mine + r * (TN * ES) + ((c ^ (r & (CR - 1))) << 4) + (at & 15);
+        const int at = (16 * i + 4 * fq) * ES;
+        uint8_t* dst = mine + fr * (TN * ES) + (((at / 16) ^ (fr & (CR - 1))) << 4) + (at & 15);
         const f32x4 v = acc[i][j];
         if (DT == MOE_DT_F32)
           *(f32x4*)dst = v;
@@ -496,22 +516,60 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
         else
           *(u32x2*)dst = u32x2{pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3])};
       }
-    }
-    // the wave reads only what it wrote itself
-    __builtin_amdgcn_wave_barrier();
-    const int c = lane % CR, n = n0 + wn * TN + c * (16 / ES);
-    if (n < a.N) {
-#pragma unroll 4
-      for (int r0 = 0; r0 < TM; r0 += 64 / CR) {
-        const int r = r0 + lane / CR, row = wm * TM + r;
-        bool on = row < rows;
-        if (MODE == kTileDown && on)
-          on = slot_token(a.sorted_slot[m0 + row], a.T, a.topk, a.has_shared) >= 0;
-        if (on)
-          *(u32x4*)((uint8_t*)a.out + ((size_t)(m0 + row) * a.N + n) * ES) =
-              *(const u32x4*)(mine + r * (TN * ES) + ((c ^ (r & (CR - 1))) << 4));
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int r0 = 0; r0 < 16; r0 += 64 / CR) {
+        const int r = r0 + lane / CR, row = wm * TM + 16 * j + r;
+        const bool on = MODE == kTileDown ? (mine_ok >> ((16 * j + r0) * CR / 64) & 1) : row < rows;
+        const u32x4 v = *(const u32x4*)(mine + r * (TN * ES) + ((c ^ (r & (CR - 1))) << 4));
+        if (on && nc < a.N && r < 16)
+          *(u32x4*)((uint8_t*)a.out + ((size_t)(m0 + row) * a.N + nc) * ES) = v;
       }
+      __builtin_amdgcn_wave_barrier();
     }
+  };
+
+  wait_step<(NBUF - 1) * D>();
+  auto run = [&](auto count, auto once) __attribute__((always_inline)) {
+    int at = 0;
+    auto on = [&]() __attribute__((always_inline)) { at = at == (NBUF - 1) * kBuf ? 0 : at + kBuf; };
+    first(0, count);
+    for (int tile = 0; tile < ntb; ++tile) {
+      const float* sc = wsc + tile * NS * nb + hs * nb;
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int b = 0; b + 1 < nb; ++b, on()) step(at, sc + b, std::false_type{}, count, once);
+      if (MODE != kTileLinear && tile + 1 < ntb) {
+        step(at, sc + nb - 1, std::false_type{}, count, once);
+        on();
+      } else {
+        step(at, sc + nb - 1, std::true_type{}, count, once);
+        wait_step<0>();  // nothing is under way to LDS any more
+      }
+      if (MODE == kTileGateUp) put_h(n0 + tile * BC, count);
+      else put_out(n0 + tile * BC, count);
+    }
+  };
+  // A wave computes only its columns of 16 tokens with rows in them, in a loop
+  // made for their number: a test at each product would break up the schedule.
+  // Every such loop has the same barriers.  The weights of a group with one row
+  // tile are read once (gate_up at T = 1024: 176 us, as ordinary loads 190 us;
+  // where a second tile reads them, 294 us instead of 288 us at T = 4096).
+  if constexpr (MODE == kTileLinear) {
+    run(IntC<FM>{}, std::false_type{});
+  } else {
+    static_assert(FM == 4, "the loops below");
+    auto by_live = [&](auto once) __attribute__((always_inline)) {
+      if (live == 4) run(IntC<4>{}, once);
+      else if (live == 3) run(IntC<3>{}, once);
+      else if (live == 2) run(IntC<2>{}, once);
+      else if (live == 1) run(IntC<1>{}, once);
+      else run(IntC<0>{}, once);
+    };
+    if (single) by_live(std::true_type{});
+    else by_live(std::false_type{});
   }
 }
 
@@ -594,6 +652,16 @@ hipError_t launch_fp8_linear(const moe_fp8_matrix& M, const void* x, int T, int 
 // Row tiles of S rows in G groups, at most: the full ones and a partial one per group.
 static size_t max_tiles(size_t S, int G) { return S / kPM + (size_t)G; }
 
+// Column tiles that one block takes in a row: a longer stream hides more of a
+// block's start and of its outputs, as long as there are blocks enough to share
+// the chip out evenly.
+static int tiles_per_block(size_t S, int G, int nt) {
+  const size_t tiles = (S < (size_t)G ? S : (size_t)G) + S / kPM;
+  int n = 1;
+  while (n < 8 && nt % (2 * n) == 0 && tiles * (size_t)(nt / (2 * n)) >= kStreamBlocks) n *= 2;
+  return n;
+}
+
 size_t fp8_expert_ffn_workspace_bytes(int T, int K, int H, int I, int has_shared) {
   const size_t S = (size_t)T * K + (has_shared ? T : 0);
   if (T <= kFp8StreamMaxT) return up256(S * I * sizeof(float));
@@ -634,8 +702,9 @@ hipError_t launch_fp8_expert_ffn(const moe_fp8_weights& W, const uint16_t* x, in
   a.N = W.I;
   a.K = W.H;
   a.nt = W.I / 128;
+  a.ntb = tiles_per_block(S, G, a.nt);
   MOE_LAUNCH("fp8_tile_gate_up", s, (k_fp8_tile<kTileGateUp, MOE_DT_BF16, 256, 128, 4, 2, 3>),
-             dim3(mt * a.nt), dim3(512), 0, s, a);
+             dim3(mt * (a.nt / a.ntb)), dim3(512), 0, s, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   a.codes = W.dn_codes;
@@ -647,8 +716,9 @@ hipError_t launch_fp8_expert_ffn(const moe_fp8_weights& W, const uint16_t* x, in
   a.N = W.H;
   a.K = W.I;
   a.nt = W.H / 128;
+  a.ntb = tiles_per_block(S, G, a.nt);
   MOE_LAUNCH("fp8_tile_down", s, (k_fp8_tile<kTileDown, MOE_DT_BF16, 128, 128, 2, 2, 2>),
-             dim3(mt * a.nt), dim3(256), 0, s, a);
+             dim3(mt * (a.nt / a.ntb)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
