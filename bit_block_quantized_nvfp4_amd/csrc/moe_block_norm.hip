@@ -354,23 +354,30 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_block_norm_grad(NormB
   if (a.w_pre) put(gw_pre, 1);
 }
 
-// dw[which][h] = sum over the P partial rows, in row order within 16 strided
-// shares, then over the shares: 16 columns x 16 shares to a block.
+// dw[which][h] = sum over the P partial rows: a block has 32 columns, 8 lanes of
+// 4 side by side, and 32 strided shares of the rows; the shares join in order.
 __global__ __launch_bounds__(256) void k_norm_dw(const float* __restrict__ part, int P, int H,
                                                  int first, float* __restrict__ dw_post,
                                                  float* __restrict__ dw_pre) {
-  __shared__ float sh[16][17];
+  __shared__ f32x4 sh[32][8];
   const int which = first + (int)blockIdx.y;
-  const int col = blockIdx.x * 16 + (threadIdx.x & 15), share = threadIdx.x >> 4;
-  float s = 0.f;
-  if (col < H)
-    for (int p = share; p < P; p += 16) s += part[((size_t)p * 2 + which) * H + col];
-  sh[share][threadIdx.x & 15] = s;
-  __syncthreads();
-  if (share == 0 && col < H) {
-    for (int q = 1; q < 16; ++q) s += sh[q][threadIdx.x];
-    (which ? dw_pre : dw_post)[col] = s;
+  const int q = threadIdx.x & 7, share = threadIdx.x >> 3;
+  const int col = blockIdx.x * 32 + 4 * q;
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  if (col < H) {
+    const f32x4* src = (const f32x4*)(part + (size_t)which * H + col);
+    const size_t ld = (size_t)2 * H / 4;  // H is a multiple of 8
+#pragma unroll 8
+    for (int p = share; p < P; p += 32) s += src[p * ld];
   }
+  sh[share][q] = s;
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  const int c = threadIdx.x;
+  float r = 0.f;
+  for (int i = 0; i < 32; ++i) r += ((const float*)sh[i])[c];
+  const int h = blockIdx.x * 32 + c;
+  if (h < H) (which ? dw_pre : dw_post)[h] = r;
 }
 
 // Waves to a row: one wave holds up to 256 chunks, four up to 1024, eight up
@@ -468,7 +475,7 @@ hipError_t launch_block_norm_grad(const void* dr, const void* dn, const void* r_
   hipError_t e = hipGetLastError();
   const int n = (w_post ? 1 : 0) + (w_pre ? 1 : 0);
   if (e != hipSuccess || n == 0) return e;
-  MOE_LAUNCH("block_norm_dw", s, k_norm_dw, dim3((H + 15) / 16, n), dim3(256), 0, s,
+  MOE_LAUNCH("block_norm_dw", s, k_norm_dw, dim3((H + 31) / 32, n), dim3(256), 0, s,
              (const float*)ws, P, H, w_post ? 0 : 1, dw_post, dw_pre);
   return hipGetLastError();
 }

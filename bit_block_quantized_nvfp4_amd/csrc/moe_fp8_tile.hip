@@ -163,24 +163,30 @@ __device__ __forceinline__ u32x4 buf_of(const void* p, uint32_t bytes) {
 // lds + 16 l (4 l).  No register is written.  In asm because the compiler
 // would wait for every such load before the next LDS read of any buffer; the
 // kernel's own waits below order them.  m0 is reserved: the compiler keeps
-// nothing in it, and nothing else here uses it.  The wait states are those a
-// memory instruction needs after m0, or a scalar register that a vector
-// instruction wrote (the descriptor's), was written.  ONCE: the bytes are not
+// nothing in it, and nothing else here uses it; a memory instruction may read it
+// one state after it was written.  ONCE: the bytes are not
 // read again (non-temporal).
+// A wave-uniform offset for these, in a scalar register that a memory
+// instruction may read: one that a vector instruction wrote needs 5 states.
+__device__ __forceinline__ uint32_t dma_offset(uint32_t v) {
+  uint32_t s = (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+  asm volatile("s_nop 4" : "+s"(s));
+  return s;
+}
 template <bool ONCE = false>
 __device__ __forceinline__ void dma_b128(u32x4 buf, uint32_t voff, uint32_t soff, uint32_t lds) {
   if (ONCE)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds" ::"s"(lds),
-                 "v"(voff), "s"(buf), "s"(__builtin_amdgcn_readfirstlane((int)soff))
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds" ::"s"(lds),
+                 "v"(voff), "s"(buf), "s"(soff)
                  : "memory");
   else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds),
-                 "v"(voff), "s"(buf), "s"(__builtin_amdgcn_readfirstlane((int)soff))
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds),
+                 "v"(voff), "s"(buf), "s"(soff)
                  : "memory");
 }
 __device__ __forceinline__ void dma_b32(u32x4 buf, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds),
-               "v"(voff), "s"(buf), "s"(__builtin_amdgcn_readfirstlane((int)soff))
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds),
+               "v"(voff), "s"(buf), "s"(soff)
                : "memory");
 }
 // All but the wave's last N memory operations are done, and all its LDS reads;
@@ -336,10 +342,11 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
     u32x4 xb = xbuf, sb = sbuf;
     xb.z = d_left > 0 ? xb.z : 0u;
     sb.z = d_left > 0 ? sb.z : 0u;
+    const uint32_t kb = dma_offset((uint32_t)d_k * 4u);
 #pragma unroll
     for (int i = 0; i < DX; ++i)
-      dma_b128(xb, xoff[i], (uint32_t)d_k * kQB, ldsw + d_at + kTok + i * NT * 16);
-    dma_b32(sb, soff, (uint32_t)d_k * 4u, lds0 + d_at + kScale + 256 * (wv % (BM / 64)));
+      dma_b128(xb, xoff[i], kb * (kQB / 4), ldsw + d_at + kTok + i * NT * 16);
+    dma_b32(sb, soff, kb, lds0 + d_at + kScale + 256 * (wv % (BM / 64)));
   };
   auto dma_weights = [&](auto once) __attribute__((always_inline)) {
     u32x4 wb = wbuf;
@@ -348,7 +355,7 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
     // a chunk past the end of a weight row is read from the start of the block
     // instead: the tokens' codes there are zeros
     const uint32_t back = MODE == kTileLinear && (int)k + chunk >= a.K ? (uint32_t)chunk : 0u;
-    const uint32_t so = MODE == kTileLinear ? k : k + d_col;
+    const uint32_t so = dma_offset(MODE == kTileLinear ? k : k + d_col);
 #pragma unroll
     for (int i = 0; i < DW; ++i) dma_b128<decltype(once)::value>(wb, woff[i] - back, so, ldsw + d_at + i * NT * 16);
     --d_left;
@@ -438,6 +445,7 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
       for (int j = 0; j < LV; ++j) p[i & 1][j] = mfma128(wf, tf[j]);
       if (i > 0) add(i - 1);
       if (FN > 2 && i == 0 && !kLast) {
+        __builtin_amdgcn_sched_barrier(0);
         meet();
         dma_tokens();
       }

@@ -60,8 +60,8 @@ __global__ __launch_bounds__(256) void k_slot_sum(const u32x4* __restrict__ y,
 #pragma unroll
   for (int i = 0; i < N; ++i) acc[i] = 0.f;
   const int ps = has_shared ? slot_pos[(size_t)TK + t] : -1;
-  // batches of 12 slots: positions and weights, then the rows, then the sums
-  // in slot order
+  // batches of 12 slots: positions and weights, then the rows (row 0 for a slot
+  // that is skipped: a load without a branch), then the sums in slot order
   for (int k0 = 0; k0 < K; k0 += 12) {
     int p[12];
     float wt[12];
@@ -74,7 +74,8 @@ __global__ __launch_bounds__(256) void k_slot_sum(const u32x4* __restrict__ y,
     u32x4 v[12];
 #pragma unroll
     for (int j = 0; j < 12; ++j)
-      if (slot_ok(p[j], TK)) v[j] = y[(size_t)p[j] * cpr + c];
+      if (k0 + j < K)
+        v[j] = __builtin_nontemporal_load(y + (size_t)(slot_ok(p[j], TK) ? p[j] : 0) * cpr + c);
 #pragma unroll
     for (int j = 0; j < 12; ++j) {
       if (slot_ok(p[j], TK)) {
@@ -155,15 +156,19 @@ __global__ __launch_bounds__(256) void k_combine_grad(
   }
 }
 
-// One wave per token.  Lanes k < K hold the slots' gradients; every lane then
-// gathers the ones of its experts, in slot order (an expert that a caller
-// names twice gets both).
+// One wave per token.  Lanes k < K hold the slots' gradients; a lane adds up
+// those of the slots that name its expert too (a caller may name one twice), in
+// slot order, and puts the sum into the row of zeros that the wave keeps in LDS
+// and then stores as 16 bytes a lane (VEC: E a multiple of 4) or 4.
+template <bool VEC>
 __global__ __launch_bounds__(256) void k_topk_grad(const int32_t* __restrict__ ids,
                                                    const float* __restrict__ w,
                                                    const float* __restrict__ dw, int T, int E,
                                                    int K, float* __restrict__ dlogits) {
+  __shared__ f32x4 rows[4][256];
   const int lane = threadIdx.x & 63;
-  const long t = (long)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const long t = (long)blockIdx.x * 4 + wv;
   if (t >= T) return;
   int id = -1;
   float wk = 0.f, g = 0.f;
@@ -172,23 +177,31 @@ __global__ __launch_bounds__(256) void k_topk_grad(const int32_t* __restrict__ i
     wk = w[t * K + lane];
     g = dw[t * K + lane];
   }
+  const int nv = (E + 3) / 4;
+  for (int e = lane; e < nv; e += 64) rows[wv][e] = f32x4{0.f, 0.f, 0.f, 0.f};
   const float mean = wave_sum_dpp(wk * g);
   g = wk * (g - mean);
-  float* row = dlogits + t * E;
-  for (int e = lane; e < E; e += 64) {
-    float a = 0.f;
-    for (int k = 0; k < K; ++k) {
-      const int ik = __builtin_amdgcn_readlane(id, k);
-      const float gk = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(g), k));
-      if (ik == e) a += gk;
-    }
-    row[e] = a;
+  float sum = 0.f;
+  for (int k = 0; k < K; ++k) {
+    const int ik = __builtin_amdgcn_readlane(id, k);
+    const float gk = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(g), k));
+    if (ik == id) sum += gk;
   }
+  // a wave's LDS operations keep their order
+  __builtin_amdgcn_wave_barrier();
+  if (id >= 0 && id < E) ((float*)rows[wv])[id] = sum;
+  __builtin_amdgcn_wave_barrier();
+  float* row = dlogits + t * E;
+  if (VEC)
+    for (int e = lane; e < nv; e += 64) ((f32x4*)row)[e] = rows[wv][e];
+  else
+    for (int e = lane; e < E; e += 64) row[e] = ((const float*)rows[wv])[e];
 }
 
 void register_sort_kernels(std::vector<const void*>& k) {
   k.push_back((const void*)&k_dispatch);
-  k.push_back((const void*)&k_topk_grad);
+  k.push_back((const void*)&k_topk_grad<true>);
+  k.push_back((const void*)&k_topk_grad<false>);
   for (int dt = MOE_DT_BF16; dt <= MOE_DT_F32; ++dt)
     by_dtype(dt, [&](auto D) {
       k.push_back((const void*)&k_slot_sum<decltype(D)::value>);
@@ -233,8 +246,10 @@ hipError_t launch_combine_grad(const void* dout, const void* y, const float* w,
 
 hipError_t launch_topk_grad(const int32_t* ids, const float* w, const float* dw, int T, int E,
                             int K, float* dlogits, hipStream_t s) {
-  MOE_LAUNCH("topk_grad", s, k_topk_grad, dim3(blocks(T, 4)), dim3(256), 0, s, ids, w, dw, T, E,
-             K, dlogits);
+  // rows of 16 bytes need E a multiple of 4 and an aligned start
+  const bool vec = E % 4 == 0 && ((uintptr_t)dlogits & 15) == 0;
+  MOE_LAUNCH("topk_grad", s, vec ? k_topk_grad<true> : k_topk_grad<false>, dim3(blocks(T, 4)),
+             dim3(256), 0, s, ids, w, dw, T, E, K, dlogits);
   return hipGetLastError();
 }
 
