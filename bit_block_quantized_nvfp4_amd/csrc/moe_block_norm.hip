@@ -383,22 +383,25 @@ __global__ __launch_bounds__(256) void k_norm_dw(const float* __restrict__ part,
 }
 
 // Waves to a row: one wave holds up to 256 chunks, four up to 1024, eight up
-// to 2048.  Few rows are spread over four waves each from 65 chunks on, since
-// the latency of a row counts then.
-static int norm_waves(int T, int cpr) {
+// to 2048.  From 65 chunks on four waves share a row where rows are few, since
+// the latency of a row counts then, and backward, whose registers leave one
+// wave a row too few rows in flight (T = 8191, H = 2048: 47 us, one wave 52 us;
+// forward at T = 32768 one wave 124 us, four 140 us).
+static int norm_waves(int T, int cpr, bool grad) {
   if (cpr > 1024) return 8;
   if (cpr > 256) return 4;
-  return (cpr > 64 && T <= 512) ? 4 : 1;
+  return (cpr > 64 && (grad || T <= 512)) ? 4 : 1;
 }
 
-template <int DT, typename F>
+// f with the chunks per thread and the waves to a row.
+template <bool GRAD, typename F>
 static void by_shape(int T, int cpr, F&& f) {
-  const int W = norm_waves(T, cpr);
+  const int W = norm_waves(T, cpr, GRAD);
   if (W == 8) f(IntC<4>{}, IntC<8>{});
   else if (W == 4 && cpr <= 256) f(IntC<1>{}, IntC<4>{});
   else if (W == 4) f(IntC<4>{}, IntC<4>{});
-  else if (cpr <= 64) f(IntC<1>{}, IntC<1>{});
-  else f(IntC<4>{}, IntC<1>{});
+  else if (GRAD || cpr <= 64) f(IntC<1>{}, IntC<1>{});
+  else if constexpr (!GRAD) f(IntC<4>{}, IntC<1>{});
 }
 
 void register_block_norm_kernels(std::vector<const void*>& k) {
@@ -406,7 +409,8 @@ void register_block_norm_kernels(std::vector<const void*>& k) {
     constexpr int DT = decltype(D)::value;
     auto one = [&](auto NC, auto W) {
       k.push_back((const void*)&k_block_norm<DT, decltype(NC)::value, decltype(W)::value>);
-      k.push_back((const void*)&k_block_norm_grad<DT, decltype(NC)::value, decltype(W)::value>);
+      if constexpr (decltype(NC)::value == 1 || decltype(W)::value > 1)
+        k.push_back((const void*)&k_block_norm_grad<DT, decltype(NC)::value, decltype(W)::value>);
     };
     one(IntC<1>{}, IntC<1>{});
     one(IntC<4>{}, IntC<1>{});
@@ -429,7 +433,7 @@ hipError_t launch_block_norm(const void* res, const void* y, const void* gate, i
                   gate_kind};
   by_dtype(dtype, [&](auto D) {
     constexpr int DT = decltype(D)::value;
-    by_shape<DT>(T, cpr, [&](auto NC, auto W) {
+    by_shape<false>(T, cpr, [&](auto NC, auto W) {
       constexpr int w = decltype(W)::value;
       MOE_LAUNCH("block_norm", s, (k_block_norm<DT, decltype(NC)::value, w>),
                  dim3(w == 1 ? (T + 3) / 4 : T), dim3(w == 1 ? 256 : 64 * w), 0, s, a);
@@ -439,14 +443,15 @@ hipError_t launch_block_norm(const void* res, const void* y, const void* gate, i
 }
 
 // Blocks of the backward kernel, each with a partial row of the weight
-// gradients: enough to fill the chip, few enough that the partials stay small
-// beside the rows.  A function of the sizes alone, so results do not depend on
-// the device's state.
+// gradients: enough to fill the chip, and 8 rows to a block at least once that
+// is so, which keeps the partials small beside the rows.  A function of the
+// sizes alone, so results do not depend on the device's state.
 static int norm_parts(int T, int H, int dtype) {
   const int cpr = H * dtype_bytes(dtype) / 16;
-  const int rows = norm_waves(T, cpr) == 1 ? 4 : 1;
+  const int rows = norm_waves(T, cpr, true) == 1 ? 4 : 1;
   const int P = (T + rows - 1) / rows;
-  return P < 512 ? P : 512;
+  const int most = T / 8 < 256 ? 256 : T / 8 < 1024 ? T / 8 : 1024;
+  return P < most ? P : most;
 }
 
 size_t block_norm_workspace_bytes(int T, int H, int dtype) {
@@ -468,7 +473,7 @@ hipError_t launch_block_norm_grad(const void* dr, const void* dn, const void* r_
                   H,                cpr,              gate_kind};
   by_dtype(dtype, [&](auto D) {
     constexpr int DT = decltype(D)::value;
-    by_shape<DT>(T, cpr, [&](auto NC, auto W) {
+    by_shape<true>(T, cpr, [&](auto NC, auto W) {
       constexpr int w = decltype(W)::value;
       MOE_LAUNCH("block_norm_grad", s, (k_block_norm_grad<DT, decltype(NC)::value, w>), dim3(P),
                  dim3(w == 1 ? 256 : 64 * w), 0, s, a);
