@@ -206,9 +206,13 @@ __device__ __forceinline__ void meet() {
 // one block of 128 along K each, through NBUF buffers.  While step s is
 // computed, the steps up to s + NBUF are on their way, across the ends of
 // tiles, so the output of a tile is written while the next one's operands come.
-template <int MODE, int DT, int BN, int BM, int WN, int WM, int NBUF>
-__global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
-  constexpr int NW = WN * WM, NT = 64 * NW;
+// KG > 1 (linear mode): KG groups of waves with buffers of their own take every
+// KG-th step and join their sums at the end, in the groups' order; a step costs
+// about half a microsecond of waiting whatever its size, which counts where
+// there are few tiles.
+template <int MODE, int DT, int BN, int BM, int WN, int WM, int NBUF, int KG = 1>
+__global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
+  constexpr int NW = WN * WM, NT = 64 * NW;    // waves and threads of a group
   constexpr int TN = BN / WN, TM = BM / WM;    // a wave's part of the tile
   constexpr int FN = TN / 16, FM = TM / 16;
   constexpr int DW = BN * 8 / NT, DX = BM * 8 / NT;  // 16-byte chunks per thread and step
@@ -225,14 +229,19 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
                 "tile shape");
   static_assert(MODE == kTileLinear || BM == kPM, "row tiles of the items");
   static_assert(MODE != kTileGateUp || BC == kQB, "a tile holds one scale of h");
-  __shared__ __align__(1024) uint8_t lds[NBUF * kBuf];
+  static_assert(KG == 1 || (MODE == kTileLinear && (KG - 1) * BN * BM * 4 + NW * 16 * TN * ES <= KG * NBUF * kBuf),
+                "the groups' sums fit");
+  __shared__ __align__(1024) uint8_t lds_all[KG * NBUF * kBuf];
   __shared__ float wsc[NS * kTileScales];
   __shared__ __align__(16) uint8_t side[MODE == kTileGateUp ? WN * BM * 4
                                         : MODE == kTileDown ? NW * 16 * TN * ES : 16];
-  const int tid = threadIdx.x, lane = tid & 63;
+  const int kg = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane((int)threadIdx.x / NT);
+  const int tid = (int)threadIdx.x - kg * NT, lane = tid & 63;
+  uint8_t* lds = lds_all + kg * (NBUF * kBuf);
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wv % WN, wm = wv / WN;
   const int nb = (a.K + kQB - 1) / kQB;
+  const int steps = (nb + KG - 1) / KG;        // of a group and tile
   const int ntb = MODE == kTileLinear ? 1 : a.ntb;
 
   const uint8_t* codes = a.codes;
@@ -313,7 +322,7 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
   // The weight scales of all steps, one per 128 weight rows of a tile, in LDS: a
   // load of one in the loop would wait for the DMA under way.  gate_up: the
   // gate's, then the up's.
-  for (int i = tid; i < ntb * NS * nb; i += NT) {
+  for (int i = threadIdx.x; i < ntb * NS * nb; i += NT * KG) {
     const int tile = i / (NS * nb), h = i / nb % NS, b = i % nb;
     const int row = n0 + tile * BC + (MODE == kTileGateUp ? h * a.N : h * kQB);
     wsc[i] = scales[(size_t)((MODE == kTileGateUp ? row : min(row, a.N - 1)) / kQB) * nb + b];
@@ -336,7 +345,7 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
   // come, to where nobody reads): every wave then has the same number of
   // operations under way at every wait, and the loop has no branch, behind
   // which the compiler would move the sums of half a step and spill.
-  int d_left = ntb * nb, d_k = 0, d_at = 0;
+  int d_left = KG == 1 ? ntb * nb : (nb - kg + KG - 1) / KG, d_k = kg, d_at = 0;
   uint32_t d_col = 0;                          // offset of the tile's weights
   auto dma_tokens = [&]() __attribute__((always_inline)) {
     u32x4 xb = xbuf, sb = sbuf;
@@ -360,7 +369,7 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
     for (int i = 0; i < DW; ++i) dma_b128<decltype(once)::value>(wb, woff[i] - back, so, ldsw + d_at + i * NT * 16);
     --d_left;
     d_at = d_at == (NBUF - 1) * kBuf ? 0 : d_at + kBuf;
-    ++d_k;
+    d_k += KG;
     if (MODE != kTileLinear) {
       d_col += d_k == nb ? (uint32_t)BC * (uint32_t)a.K : 0u;
       d_k = d_k == nb ? 0 : d_k;
@@ -401,7 +410,7 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
   // the last two rows every wave has read the last of the weights, and the step
   // after has landed (what was asked for later may be under way), so its first
   // operands are read while those products run.  Two product rows: one barrier.
-  auto step = [&](int at, const float* sc, auto last, auto count, auto once) __attribute__((always_inline)) {
+  auto step = [&](int at, const float* sc, bool some, auto last, auto count, auto once) __attribute__((always_inline)) {
     constexpr int LV = decltype(count)::value;
     constexpr bool kLast = decltype(last)::value;
     const uint8_t* pw = lds + at + wn * TN * kQB;
@@ -410,7 +419,8 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
     const int next = at == (NBUF - 1) * kBuf ? 0 : at + kBuf;
     Frag<EX> tf[FM];
     float s0[FM], s1[FM];
-    const float w0 = sc[0], w1 = MODE == kTileGateUp ? sc[nb] : 0.f;
+    // a group's step past the end adds zeros
+    const float w0 = KG == 1 || some ? sc[0] : 0.f, w1 = MODE == kTileGateUp ? sc[nb] : 0.f;
 #pragma unroll
     for (int j = 0; j < LV; ++j) {
       tf[j].set(j < PRE ? tn[j < PRE ? j : 0] : frag(pt, 16 * j));
@@ -508,7 +518,7 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
   // c ^ (row % chunks), for the banks.  A wave's LDS operations keep their order.
   auto put_out = [&](int n, auto count) __attribute__((always_inline)) {
     constexpr int LV = decltype(count)::value;
-    uint8_t* mine = (MODE == kTileDown ? side : lds) + wv * (16 * TN * ES);
+    uint8_t* mine = (MODE == kTileDown ? side : lds) + (KG > 1 ? (KG - 1) * BN * BM * 4 : 0) + wv * (16 * TN * ES);
     const int c = lane % CR, nc = n + wn * TN + c * (16 / ES);
 #pragma unroll
     for (int j = 0; j < LV; ++j) {
@@ -548,13 +558,35 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
       for (int i = 0; i < FN; ++i)
 #pragma unroll
         for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-      for (int b = 0; b + 1 < nb; ++b, on()) step(at, sc + b, std::false_type{}, count, once);
+      const float* end = sc + nb;
+      sc += kg;
+      for (int b = 0; b + 1 < steps; ++b, sc += KG, on())
+        step(at, sc, true, std::false_type{}, count, once);
       if (MODE != kTileLinear && tile + 1 < ntb) {
-        step(at, sc + nb - 1, std::false_type{}, count, once);
+        step(at, sc, true, std::false_type{}, count, once);
         on();
       } else {
-        step(at, sc + nb - 1, std::true_type{}, count, once);
+        step(at, sc, sc < end, std::true_type{}, count, once);
         wait_step<0>();  // nothing is under way to LDS any more
+      }
+      if (KG > 1) {
+        // lane by lane, 16 bytes at a time
+        f32x4* mine = (f32x4*)lds_all + tid;
+        if (kg > 0) {
+#pragma unroll
+          for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j)
+              mine[(((kg - 1) * FN + i) * FM + j) * NT] = acc[i][j];
+        }
+        meet();
+        if (kg > 0) return;
+#pragma unroll
+        for (int g = 0; g < KG - 1; ++g)
+#pragma unroll
+          for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j) acc[i][j] += mine[((g * FN + i) * FM + j) * NT];
       }
       if (MODE == kTileGateUp) put_h(n0 + tile * BC, count);
       else put_out(n0 + tile * BC, count);
@@ -581,15 +613,44 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_tile(TileArgs a) {
   }
 }
 
+// The linear mode's tiles, largest first: f with the kernel, BN, BM and threads.
+// Rows of f32 take twice the operand registers, hence fewer shapes.
+template <int DT, typename F>
+static void by_linear_tile(int shape, F&& f) {
+  if constexpr (DT != MOE_DT_F32) {
+    if (shape == 0) f(&k_fp8_tile<kTileLinear, DT, 256, 256, 2, 4, 2>, 256, 256, 512);
+    else if (shape == 1) f(&k_fp8_tile<kTileLinear, DT, 128, 128, 2, 2, 2, 2>, 128, 128, 512);
+    else if (shape == 2) f(&k_fp8_tile<kTileLinear, DT, 128, 64, 2, 2, 3, 2>, 128, 64, 512);
+    else f(&k_fp8_tile<kTileLinear, DT, 64, 64, 2, 2, 4, 2>, 64, 64, 512);
+  } else {
+    if (shape <= 1) f(&k_fp8_tile<kTileLinear, DT, 128, 128, 2, 2, 2>, 128, 128, 256);
+    else f(&k_fp8_tile<kTileLinear, DT, 64, 64, 2, 2, 4, 2>, 64, 64, 512);
+  }
+}
+
+// The largest tile whose grid still fills most of the 256 compute units.  Tile
+// kernel's time (bf16, us with about 3.5 us of event overhead) with the tile
+// taken and its neighbours:
+//   rows x N x K           256x256  128x128  128x64  64x64
+//   8192 x 4096 x 4096         138*     206     266    393
+//   2048 x 4096 x 4096          -        54*     66     97
+//   333 x 8192 x 8192           -        48*     60     71
+//   333 x 4168 x 2064           -        18      15*    20
+//   64 x 8192 x 8192            -        39      30     26*
+//   64 x 2048 x 2048            -        14      11     10*
+static int linear_tile(int T, int N) {
+  auto tiles = [&](int bn, int bm) { return (long)((N + bn - 1) / bn) * ((T + bm - 1) / bm); };
+  if (tiles(256, 256) >= 192) return 0;
+  if (tiles(128, 128) >= 192) return 1;
+  return tiles(128, 64) >= 160 ? 2 : 3;
+}
+
 void register_fp8_tile_kernels(std::vector<const void*>& k) {
   auto add = [&](auto D) {
     constexpr int DT = decltype(D)::value;
     k.push_back((const void*)&k_fp8_quant<DT>);
-    if constexpr (DT != MOE_DT_F32)
-      k.push_back((const void*)&k_fp8_tile<kTileLinear, DT, 256, 256, 2, 4, 2>);
-    else
-      k.push_back((const void*)&k_fp8_tile<kTileLinear, DT, 128, 128, 2, 2, 3>);
-    k.push_back((const void*)&k_fp8_tile<kTileLinear, DT, 128, 64, 4, 1, 3>);
+    for (int s = 0; s < 4; ++s)
+      by_linear_tile<DT>(s, [&](auto kernel, int, int, int) { k.push_back((const void*)kernel); });
   };
   for (int dt = MOE_DT_BF16; dt <= MOE_DT_F32; ++dt) by_dtype(dt, add);
   k.push_back((const void*)&k_fp8_prep);
@@ -632,27 +693,12 @@ hipError_t launch_fp8_linear(const moe_fp8_matrix& M, const void* x, int T, int 
   a.R = T;
   a.N = M.N;
   a.K = M.K;
-  const long big = (long)((M.N + 255) / 256) * ((T + 255) / 256);
   by_dtype(dtype, [&](auto D) {
-    constexpr int DT = decltype(D)::value;
-    if (big >= 192) {
-      if constexpr (DT != MOE_DT_F32) {
-        a.nt = (M.N + 255) / 256;
-        MOE_LAUNCH("fp8_tile_256", s, (k_fp8_tile<kTileLinear, DT, 256, 256, 2, 4, 2>),
-                   dim3((unsigned)big), dim3(512), 0, s, a);
-      } else {
-        // f16 operands take twice the registers
-        a.nt = (M.N + 127) / 128;
-        const unsigned n = (unsigned)a.nt * (unsigned)((T + 127) / 128);
-        MOE_LAUNCH("fp8_tile_128", s, (k_fp8_tile<kTileLinear, DT, 128, 128, 2, 2, 3>), dim3(n),
-                   dim3(256), 0, s, a);
-      }
-    } else {
-      a.nt = (M.N + 127) / 128;
-      const unsigned n = (unsigned)a.nt * (unsigned)((T + 63) / 64);
-      MOE_LAUNCH("fp8_tile_128", s, (k_fp8_tile<kTileLinear, DT, 128, 64, 4, 1, 3>), dim3(n),
-                 dim3(256), 0, s, a);
-    }
+    by_linear_tile<decltype(D)::value>(linear_tile(T, M.N), [&](auto kernel, int bn, int bm, int threads) {
+      a.nt = (M.N + bn - 1) / bn;
+      MOE_LAUNCH("fp8_tile", s, kernel, dim3((unsigned)a.nt * (unsigned)((T + bm - 1) / bm)),
+                 dim3(threads), 0, s, a);
+    });
   });
   return hipGetLastError();
 }

@@ -74,7 +74,7 @@ def test_quant_is_bit_exact(moe, T, K, dtype):
 # and N that end inside a block of 128
 LINEAR = [(1, 8, 16), (1, 2048, 2048), (2, 264, 144), (8, 136, 1040), (16, 24, 4112), (15, 8200, 272), (16, 8192, 128),
           (17, 8, 16), (17, 264, 144), (33, 128, 400), (64, 520, 256), (65, 72, 2064), (200, 1032, 384),
-          (300, 392, 640), (513, 136, 160)]
+          (300, 392, 640), (513, 136, 160), (130, 8200, 272), (700, 2056, 144), (90, 10248, 400)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
