@@ -32,17 +32,21 @@ struct StreamArgs {
   int tiles;               // blocks along N
 };
 
-// 32 consecutive values of a row from position k0 on, zero from K on.
+// The 16 values of a row from position k on (zeros from K on), twice: at k and
+// at k + 64.  These are the chunks that a lane holds of the weights too: lane
+// 16 q + r has chunks q and q + 4 of row r, so that a load of a wave takes whole
+// halves of 16 lines (64 bytes each).
 template <int DT>
-__device__ __forceinline__ void load32(const void* __restrict__ row, int k0, int K,
+__device__ __forceinline__ void load32(const void* __restrict__ row, int k, int K,
                                        float (&f)[32]) {
   constexpr int N = Chunk<DT>::N;
   const u32x4* p = (const u32x4*)row;
   u32x4 v[32 / N];
 #pragma unroll
   for (int i = 0; i < 32 / N; ++i) {
+    const int at = k + (i < 16 / N ? i * N : 64 + i * N - 16);
     v[i] = u32x4{0u, 0u, 0u, 0u};
-    if (k0 + i * N < K) v[i] = p[k0 / N + i];
+    if (at < K) v[i] = p[at / N];
   }
 #pragma unroll
   for (int i = 0; i < 32 / N; ++i) {
@@ -114,20 +118,20 @@ __global__ __launch_bounds__(512) void k_fp8_stream(StreamArgs a) {
 #pragma unroll
     for (int i = 0; i < RT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     for (int b = kw; b < nb; b += KW) {
-      const int k0 = b * kQB + 32 * q;
+      const int k = b * kQB + 16 * q;
       Frag<EX> w[RT];
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
         // chunks past the row's end are read from its start instead: their
         // counterparts in the token rows are zeros
-        const u32x4 lo = *(const u32x4*)(wrow[i] + (k0 < a.K ? k0 : 0));
-        const u32x4 hi = *(const u32x4*)(wrow[i] + (k0 + 16 < a.K ? k0 + 16 : 0));
+        const u32x4 lo = *(const u32x4*)(wrow[i] + (k < a.K ? k : 0));
+        const u32x4 hi = *(const u32x4*)(wrow[i] + (k + 64 < a.K ? k + 64 : 0));
         w[i].set(join8(lo, hi));
       }
       float f[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) f[j] = 0.f;
-      if (on) load32<DT>(xrow, k0, a.K, f);
+      if (on) load32<DT>(xrow, k, a.K, f);
       float am = 0.f;
 #pragma unroll
       for (int j = 0; j < 32; ++j) am = fmaxf(am, fabsf(f[j]));
@@ -196,7 +200,7 @@ void register_fp8_stream_kernels(std::vector<const void*>& k) {
   reg<MOE_DT_F16>(k);
   reg<MOE_DT_F32>(k);
   k.push_back((const void*)&k_fp8_stream<MOE_DT_BF16, kStreamGateUp, 2, 8>);
-  k.push_back((const void*)&k_fp8_stream<MOE_DT_F32, kStreamDown, 2, 4>);
+  k.push_back((const void*)&k_fp8_stream<MOE_DT_F32, kStreamDown, 2, 2>);
 }
 
 hipError_t launch_fp8_stream_linear(const moe_fp8_matrix& M, const void* x, int T, int dtype,
@@ -209,7 +213,11 @@ hipError_t launch_fp8_stream_linear(const moe_fp8_matrix& M, const void* x, int 
   a.R = T;
   a.N = M.N;
   a.K = M.K;
-  const int RT = M.N >= 8192 ? 2 : 1;
+  // Two row tiles to a wave share the quantisation of its rows, which pays where
+  // the rows' bytes count and blocks are plenty (8192 x 8192, by events: 16 rows
+  // 26 us, one tile 30 us; 1 row 24 us, one tile 19 us; 8 rows of 4096 x 4096
+  // 12.5 us, one tile 10.4 us).
+  const int RT = M.N >= 8192 && T > 8 ? 2 : 1;
   a.tiles = (M.N + 16 * RT - 1) / (16 * RT);
   by_dtype(dtype, [&](auto D) {
     constexpr int DT = decltype(D)::value;
@@ -253,8 +261,8 @@ hipError_t launch_fp8_stream_experts(const moe_fp8_weights& W, const uint16_t* x
   a.out = y;
   a.N = W.H;
   a.K = W.I;
-  a.tiles = W.H / 64;
-  MOE_LAUNCH("fp8_stream_down", s, (k_fp8_stream<MOE_DT_F32, kStreamDown, 2, 4>),
+  a.tiles = W.H / 128;
+  MOE_LAUNCH("fp8_stream_down", s, (k_fp8_stream<MOE_DT_F32, kStreamDown, 2, 2>),
              dim3((unsigned)G * a.tiles), dim3(512), 0, s, a);
   return hipGetLastError();
 }
