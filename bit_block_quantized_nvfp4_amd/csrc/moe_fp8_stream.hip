@@ -33,36 +33,27 @@ struct StreamArgs {
 };
 
 // The 16 values of a row from position k on (zeros from K on), twice: at k and
-// at k + 64.  These are the chunks that a lane holds of the weights too: lane
-// 16 q + r has chunks q and q + 4 of row r, so that a load of a wave takes whole
-// halves of 16 lines (64 bytes each).
+// at k + 64, as loaded.  These are the chunks that a lane holds of the weights
+// too: lane 16 q + r has chunks q and q + 4 of row r, so that a load of a wave
+// takes whole halves of 16 lines (64 bytes each).
 template <int DT>
 __device__ __forceinline__ void load32(const void* __restrict__ row, int k, int K,
-                                       float (&f)[32]) {
+                                       u32x4 (&v)[32 / Chunk<DT>::N]) {
   constexpr int N = Chunk<DT>::N;
   const u32x4* p = (const u32x4*)row;
-  u32x4 v[32 / N];
 #pragma unroll
   for (int i = 0; i < 32 / N; ++i) {
     const int at = k + (i < 16 / N ? i * N : 64 + i * N - 16);
-    v[i] = u32x4{0u, 0u, 0u, 0u};
     if (at < K) v[i] = p[at / N];
-  }
-#pragma unroll
-  for (int i = 0; i < 32 / N; ++i) {
-    float c[N];
-    Chunk<DT>::unpack(v[i], c);
-#pragma unroll
-    for (int j = 0; j < N; ++j) f[i * N + j] = c[j];
   }
 }
 
-template <int DT, int MODE, int RT, int KW>
-__global__ __launch_bounds__(512) void k_fp8_stream(StreamArgs a) {
-  constexpr int RW = 8 / KW;            // tile groups of the block
+template <int DT, int MODE, int RT, int KW, int NW>
+__global__ __launch_bounds__(64 * NW) void k_fp8_stream(StreamArgs a) {
+  constexpr int RW = NW / KW;            // tile groups of the block
   constexpr bool EX = MODE == kStreamLinear && DT == MOE_DT_F32;
   constexpr int kPad = 1;
-  __shared__ f32x4 red[8][RT][64 + kPad];
+  __shared__ f32x4 red[NW][RT][64 + kPad];
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int kw = wv % KW, rw = wv / KW;
@@ -128,21 +119,32 @@ __global__ __launch_bounds__(512) void k_fp8_stream(StreamArgs a) {
         const u32x4 hi = *(const u32x4*)(wrow[i] + (k + 64 < a.K ? k + 64 : 0));
         w[i].set(join8(lo, hi));
       }
-      float f[32];
+      constexpr int N = Chunk<DT>::N;
+      u32x4 v[32 / N];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) f[j] = 0.f;
-      if (on) load32<DT>(xrow, k, a.K, f);
+      for (int i = 0; i < 32 / N; ++i) v[i] = u32x4{0u, 0u, 0u, 0u};
+      if (on) load32<DT>(xrow, k, a.K, v);
       float am = 0.f;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) am = fmaxf(am, fabsf(f[j]));
+      for (int i = 0; i < 32 / N; ++i) {
+        float f[N];
+        Chunk<DT>::unpack(v[i], f);
+#pragma unroll
+        for (int j = 0; j < N; ++j) am = fmaxf(am, fabsf(f[j]));
+      }
       am = fmaxf(am, __shfl_xor(am, 16));
       am = fmaxf(am, __shfl_xor(am, 32));
       am = q_floor(am);
       const float m = 448.0f / am, sx = am / 448.0f;
       i32x8 xq;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        xq[j] = (int)fp8x4(f[4 * j] * m, f[4 * j + 1] * m, f[4 * j + 2] * m, f[4 * j + 3] * m);
+      for (int i = 0; i < 32 / N; ++i) {
+        float f[N];
+        Chunk<DT>::unpack(v[i], f);
+#pragma unroll
+        for (int j = 0; j < N; j += 4)
+          xq[(i * N + j) / 4] = (int)fp8x4(f[j] * m, f[j + 1] * m, f[j + 2] * m, f[j + 3] * m);
+      }
       Frag<EX> xf;
       xf.set(xq);
 #pragma unroll
@@ -192,15 +194,16 @@ __global__ __launch_bounds__(512) void k_fp8_stream(StreamArgs a) {
 
 template <int DT>
 static void reg(std::vector<const void*>& k) {
-  k.push_back((const void*)&k_fp8_stream<DT, kStreamLinear, 1, 8>);
-  k.push_back((const void*)&k_fp8_stream<DT, kStreamLinear, 2, 8>);
+  k.push_back((const void*)&k_fp8_stream<DT, kStreamLinear, 1, 8, 8>);
+  k.push_back((const void*)&k_fp8_stream<DT, kStreamLinear, 2, 8, 8>);
 }
 void register_fp8_stream_kernels(std::vector<const void*>& k) {
   reg<MOE_DT_BF16>(k);
   reg<MOE_DT_F16>(k);
   reg<MOE_DT_F32>(k);
-  k.push_back((const void*)&k_fp8_stream<MOE_DT_BF16, kStreamGateUp, 2, 8>);
-  k.push_back((const void*)&k_fp8_stream<MOE_DT_F32, kStreamDown, 2, 2>);
+  k.push_back((const void*)&k_fp8_stream<MOE_DT_BF16, kStreamGateUp, 2, 8, 8>);
+  k.push_back((const void*)&k_fp8_stream<MOE_DT_BF16, kStreamGateUp, 2, 4, 4>);
+  k.push_back((const void*)&k_fp8_stream<MOE_DT_F32, kStreamDown, 2, 2, 2>);
 }
 
 hipError_t launch_fp8_stream_linear(const moe_fp8_matrix& M, const void* x, int T, int dtype,
@@ -222,10 +225,10 @@ hipError_t launch_fp8_stream_linear(const moe_fp8_matrix& M, const void* x, int 
   by_dtype(dtype, [&](auto D) {
     constexpr int DT = decltype(D)::value;
     if (RT == 1)
-      MOE_LAUNCH("fp8_stream", s, (k_fp8_stream<DT, kStreamLinear, 1, 8>), dim3(a.tiles),
+      MOE_LAUNCH("fp8_stream", s, (k_fp8_stream<DT, kStreamLinear, 1, 8, 8>), dim3(a.tiles),
                  dim3(512), 0, s, a);
     else
-      MOE_LAUNCH("fp8_stream", s, (k_fp8_stream<DT, kStreamLinear, 2, 8>), dim3(a.tiles),
+      MOE_LAUNCH("fp8_stream", s, (k_fp8_stream<DT, kStreamLinear, 2, 8, 8>), dim3(a.tiles),
                  dim3(512), 0, s, a);
   });
   return hipGetLastError();
@@ -251,8 +254,15 @@ hipError_t launch_fp8_stream_experts(const moe_fp8_weights& W, const uint16_t* x
   a.topk = K;
   a.has_shared = W.has_shared;
   a.tiles = W.I / 16;
-  MOE_LAUNCH("fp8_stream_gate_up", s, (k_fp8_stream<MOE_DT_BF16, kStreamGateUp, 2, 8>),
-             dim3((unsigned)G * a.tiles), dim3(512), 0, s, a);
+  // Blocks of 4 waves where there are enough of them (T = 8, up to 81 groups:
+  // 36 us, of 8 waves 40 us), of 8 for fewer, each wave a shorter stretch of K
+  // (T = 1, 11 groups: 12.4 us, of 4 waves 13.6 us; by events).
+  if (G > 64)
+    MOE_LAUNCH("fp8_stream_gate_up", s, (k_fp8_stream<MOE_DT_BF16, kStreamGateUp, 2, 4, 4>),
+               dim3((unsigned)G * a.tiles), dim3(256), 0, s, a);
+  else
+    MOE_LAUNCH("fp8_stream_gate_up", s, (k_fp8_stream<MOE_DT_BF16, kStreamGateUp, 2, 8, 8>),
+               dim3((unsigned)G * a.tiles), dim3(512), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   a.codes = W.dn_codes;
@@ -261,9 +271,9 @@ hipError_t launch_fp8_stream_experts(const moe_fp8_weights& W, const uint16_t* x
   a.out = y;
   a.N = W.H;
   a.K = W.I;
-  a.tiles = W.H / 128;
-  MOE_LAUNCH("fp8_stream_down", s, (k_fp8_stream<MOE_DT_F32, kStreamDown, 2, 2>),
-             dim3((unsigned)G * a.tiles), dim3(512), 0, s, a);
+  a.tiles = W.H / 32;
+  MOE_LAUNCH("fp8_stream_down", s, (k_fp8_stream<MOE_DT_F32, kStreamDown, 2, 2, 2>),
+             dim3((unsigned)G * a.tiles), dim3(128), 0, s, a);
   return hipGetLastError();
 }
 

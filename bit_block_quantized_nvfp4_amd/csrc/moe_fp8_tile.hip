@@ -718,7 +718,7 @@ static int tiles_per_block(size_t S, int G, int nt) {
 
 size_t fp8_expert_ffn_workspace_bytes(int T, int K, int H, int I, int has_shared) {
   const size_t S = (size_t)T * K + (has_shared ? T : 0);
-  if (T <= kFp8StreamMaxT) return up256(S * I * sizeof(float));
+  if (T <= kDecodeMaxT) return up256(S * I * sizeof(float));
   return up256((size_t)T * H) + up256((size_t)T * (H / kQB) * sizeof(float)) + up256(S * I) +
          up256(S * (I / kQB) * sizeof(float)) + 16 * (max_tiles(S, kPMaxG) + 1);
 }
@@ -726,7 +726,9 @@ size_t fp8_expert_ffn_workspace_bytes(int T, int K, int H, int I, int has_shared
 hipError_t launch_fp8_expert_ffn(const moe_fp8_weights& W, const uint16_t* x, int T, int K,
                                  const int32_t* offsets, const int32_t* sorted_slot,
                                  const int32_t* groups, uint16_t* y, void* ws, hipStream_t s) {
-  if (T <= kFp8StreamMaxT)
+  // the layer's own switch; measured, both paths take the same time at T = 8
+  // (H = 2048, I = 512, top 10 of 512), tiles 17% less at T = 16, streams 30% less at T = 2
+  if (T <= kDecodeMaxT)
     return launch_fp8_stream_experts(W, x, T, K, offsets, sorted_slot, groups, (float*)ws, y, s);
   const size_t S = (size_t)T * K + (W.has_shared ? T : 0);
   uint8_t* xq = (uint8_t*)ws;

@@ -165,8 +165,9 @@ hipError_t launch_block_norm_grad(const void* dr, const void* dn, const void* r_
                                   int H, int dtype, void* dres, void* dy, void* dgate,
                                   float* dw_post, float* dw_pre, void* ws, hipStream_t s);
 
-// e4m3 products with a scale per block of 128 (moe_fp8_stream.hip: up to
-// kFp8StreamMaxT rows, one MFMA operand; moe_fp8_tile.hip: more).
+// e4m3 products with a scale per block of 128: moe_fp8_stream.hip, rows of one
+// MFMA operand at most (dense: up to kFp8StreamMaxT; experts: the decode
+// batches); moe_fp8_tile.hip, more.
 constexpr int kFp8StreamMaxT = 16;
 void register_fp8_stream_kernels(std::vector<const void*>& k);
 void register_fp8_tile_kernels(std::vector<const void*>& k);

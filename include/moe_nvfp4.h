@@ -488,7 +488,7 @@ int moe_block_norm_grad(const void* dr, const void* dn, const void* r_out, const
  * so it is exact and is laid out once) on the gradient of out.
  *
  *   x [T][K], out [T][N] of dtype
- *   ws  at least moe_fp8_linear_workspace_bytes(T, K) bytes (0 up to 16 rows)
+ *   ws  at least moe_fp8_linear_workspace_bytes(T, K) bytes (0: none needed)
  *
  * A NaN or an infinity in a row makes that row's outputs NaN and no others.
  * Limits: K a multiple of 16, N a multiple of 8, both in [16, 65536] and
@@ -522,7 +522,7 @@ int moe_fp8_linear(const moe_fp8_matrix* M, const void* x, int T, int dtype, voi
  *
  * with xq, hq the rows quantised as above (x [T][H] bf16, h not rounded in
  * between).  offsets, sorted_slot and groups are moe_permute's; y_slots goes to
- * moe_combine.  Up to 16 tokens the active experts' weights stream once, in
+ * moe_combine.  Up to 8 tokens the active experts' weights stream once, in
  * two launches; more run as the quantisation and two grouped products.
  *
  *   ws  at least moe_fp8_expert_ffn_workspace_bytes(T, K, H, I, has_shared)
