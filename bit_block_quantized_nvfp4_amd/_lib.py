@@ -149,6 +149,26 @@ def lib():
     return _lib
 
 
+_bind = None
+
+
+def binding():
+    """Import (once) and return the compiled argument marshalling of ops.py."""
+    global _bind
+    if _bind is None:
+        import torch  # its libraries have to be loaded first
+
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise ImportError(
+                "bit_block_quantized_nvfp4_amd/_binding.so is not built; run "
+                "bit_block_quantized_nvfp4_amd/build.py") from e
+        _binding.set_errors(MoeError, torch.OutOfMemoryError)
+        _bind = _binding
+    return _bind
+
+
 def check(status: int) -> int:
     if status < 0:
         raise MoeError(status, lib().moe_last_error().decode(errors="replace"))

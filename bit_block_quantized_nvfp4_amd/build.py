@@ -1,8 +1,10 @@
-"""Build libmoe_nvfp4.so (HIP, gfx950) in-tree with hipcc.
+"""Build libmoe_nvfp4.so (HIP, gfx950) in-tree with hipcc, and _binding.so.
 
 Each ``csrc/*.hip`` file is compiled to an object under ``_build/`` in
 parallel, then linked into ``libmoe_nvfp4.so`` next to this file.  Every HIP
-file is compiled with packed-FP32 instructions disabled.
+file is compiled with packed-FP32 instructions disabled.  ``csrc/binding.cpp``
+is host code only: a Python module beside it that checks and passes on torch
+tensors.
 """
 from __future__ import annotations
 
@@ -11,11 +13,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_nvfp4.so")
+BINDING = os.path.join(HERE, "_binding.so")
 ARCH = "gfx950"
 
 HIP_FLAGS = [
@@ -31,6 +35,20 @@ def hipcc() -> str:
         if c and os.path.exists(c):
             return c
     raise RuntimeError("hipcc not found: the MoE library needs ROCm's hipcc")
+
+
+def binding_command(out: str) -> list:
+    import torch
+    from torch.utils import cpp_extension
+
+    inc = [*cpp_extension.include_paths(), os.path.join(os.path.dirname(os.path.dirname(hipcc())), "include"),
+           sysconfig.get_paths()["include"]]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+            "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[f for p in inc for f in ("-isystem", p)], os.path.join(CSRC, "binding.cpp"), "-o", out,
+            "-L" + cpp_extension.TORCH_LIB_PATH, "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python",
+            "-L" + HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
 
 
 def build(verbose: bool = False) -> str:
@@ -65,6 +83,11 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
     os.replace(tmp, LIB)
+    tmp = BINDING + ".tmp"
+    r = subprocess.run(binding_command(tmp), stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    if r.returncode != 0:
+        raise RuntimeError("binding compile failed:\n" + r.stdout.decode(errors="replace"))
+    os.replace(tmp, BINDING)
     return LIB
 
 

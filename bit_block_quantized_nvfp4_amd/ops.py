@@ -1,4 +1,5 @@
-"""Python binding of the C ABI (include/moe_nvfp4.h): argument marshalling only.
+"""Python binding of the C ABI (include/moe_nvfp4.h): argument marshalling only
+(csrc/binding.cpp does it for the sort, norm and e4m3 operators).
 
 Every function takes and returns torch tensors on the current HIP device and
 enqueues the library's kernels on torch's current stream.  Outputs (and, unless
@@ -288,37 +289,16 @@ def moe_expert_ffn_noalloc(W: NVFP4Weights, x: torch.Tensor, K: int, offsets: to
 def moe_combine(y_slots: torch.Tensor, w: torch.Tensor, slot_pos: torch.Tensor, K: int,
                 has_shared: bool, out: Optional[torch.Tensor] = None):
     """Weighted sum of each token's rows.  y_slots is bf16, float16 or float32."""
-    if y_slots.dtype != torch.bfloat16:
-        return _combine_typed(y_slots, w, slot_pos, None, K, has_shared, out)
-    _need(y_slots, torch.bfloat16, name="y_slots")
-    _need(w, torch.float32, name="w")
-    T = w.shape[0]
-    H = y_slots.shape[1]
-    _need(slot_pos, torch.int32, (T * K + (T if has_shared else 0),), "slot_pos")
-    out = torch.empty((T, H), dtype=torch.bfloat16, device=y_slots.device) if out is None else out
-    _need(out, torch.bfloat16, (T, H), "out")
-    check(_lib.lib().moe_combine(_ptr(y_slots), _ptr(w), _ptr(slot_pos), T, K, H, int(has_shared),
-                                 _ptr(out), _stream()))
-    return out
+    return _lib.binding().combine(y_slots, w, slot_pos, None, K, has_shared, out)
 
 
 def moe_combine_gated(y_slots: torch.Tensor, w: torch.Tensor, slot_pos: torch.Tensor,
                       gate: torch.Tensor, K: int, out: Optional[torch.Tensor] = None):
     """Combine with the shared expert scaled by sigmoid(gate[t]).  y_slots is
     bf16, float16 or float32."""
-    if y_slots.dtype != torch.bfloat16:
-        return _combine_typed(y_slots, w, slot_pos, gate, K, True, out)
-    _need(y_slots, torch.bfloat16, name="y_slots")
-    _need(w, torch.float32, name="w")
-    T = w.shape[0]
-    H = y_slots.shape[1]
-    _need(slot_pos, torch.int32, (T * K + T,), "slot_pos")
-    _need(gate, torch.float32, (T,), "gate")
-    out = torch.empty((T, H), dtype=torch.bfloat16, device=y_slots.device) if out is None else out
-    _need(out, torch.bfloat16, (T, H), "out")
-    check(_lib.lib().moe_combine_gated(_ptr(y_slots), _ptr(w), _ptr(slot_pos), _ptr(gate), T, K, H,
-                                       _ptr(out), _stream()))
-    return out
+    if gate is None:
+        raise ValueError("gate is missing")
+    return _lib.binding().combine(y_slots, w, slot_pos, gate, K, True, out)
 
 
 def moe_layer(W: NVFP4Weights, x: torch.Tensor, logits: torch.Tensor, K: int,
@@ -381,118 +361,18 @@ def moe_layer(W: NVFP4Weights, x: torch.Tensor, logits: torch.Tensor, K: int,
                 slot_pos=slot_pos, groups=groups, y_slots=y_slots, out=out)
 
 
-_DTYPES = {torch.bfloat16: _lib.MOE_DT_BF16, torch.float16: _lib.MOE_DT_F16,
-           torch.float32: _lib.MOE_DT_F32}
-
-
-def _dtype(t: torch.Tensor, name: str) -> int:
-    dt = _DTYPES.get(t.dtype)
-    if dt is None:
-        raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
-    return dt
-
-
-def _dev(t: torch.Tensor, name: str) -> torch.device:
-    """t's device, which has to be the current one: the kernels go to its stream."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    d = t.device
-    if d.index != torch._C._cuda_getDevice():
-        raise ValueError(f"{name} is on {d}, not on the current device")
-    return d
-
-
-def _want(t: torch.Tensor, dtype, shape, dev, name: str) -> int:
-    """t's pointer, after checks of dtype, shape, device and contiguity."""
-    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
-        if t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
-        _need(t, dtype, shape, name)
-    return t.data_ptr()
-
-
-def _out(t: Optional[torch.Tensor], dtype, shape, dev, name: str) -> torch.Tensor:
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _want(t, dtype, shape, dev, name)
-    return t
-
-
-def _like(t: Optional[torch.Tensor], ref: torch.Tensor, dev, name: str) -> torch.Tensor:
-    """Output of ref's type and shape: a new one, or t checked against them."""
-    if t is None:
-        return torch.empty_like(ref)
-    _want(t, ref.dtype, ref.shape, dev, name)
-    return t
-
-
-def _slots(slot_pos: torch.Tensor, K: int, has_shared: bool) -> int:
-    """Tokens of a permutation with K routed slots (and a shared one) each."""
-    per = K + int(has_shared)
-    n = slot_pos.numel()
-    if K < 1 or n == 0 or n % per:
-        raise ValueError(f"slot_pos has {n} entries, not a positive multiple of {per} slots a token")
-    return n // per
-
-
-def _scratch(ws: Optional[torch.Tensor], nbytes: int, dev) -> torch.Tensor:
-    if ws is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    if ws.device != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < nbytes:
-        raise ValueError(f"workspace of {nbytes} contiguous bytes on {dev} needed")
-    return ws
-
-
 def moe_dispatch(x: torch.Tensor, slot_pos: torch.Tensor, K: int, has_shared: bool,
                  xs: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """Rows of x in expert order: xs[slot_pos[s]] = x[token of s], [T*K (+ T), H].
-    Rows that no slot points at stay as they are in xs."""
-    dev, dt = _dev(x, "x"), _dtype(x, "x")
-    T = _slots(slot_pos, K, has_shared)
-    if x.dim() != 2:
-        raise ValueError("x must have two dimensions")
-    H = x.shape[1]
-    _want(x, x.dtype, (T, H), dev, "x")
-    S = T * (K + int(has_shared))
-    _want(slot_pos, torch.int32, (S,), dev, "slot_pos")
-    xs = _out(xs, x.dtype, (S, H), dev, "xs")
-    check(_lib.lib().moe_dispatch(x.data_ptr(), slot_pos.data_ptr(), T, K, H, int(has_shared), dt,
-                                  xs.data_ptr(), _stream()))
-    return xs
+    """Rows of x (bf16, float16 or float32 [T, H]) in expert order:
+    xs[slot_pos[s]] = x[token of s], [T*K (+ T), H].  Rows that no slot points at
+    stay as they are in xs."""
+    return _lib.binding().dispatch(x, slot_pos, K, has_shared, xs)
 
 
 def moe_dispatch_grad(dxs: torch.Tensor, slot_pos: torch.Tensor, K: int, has_shared: bool,
                       dx: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient of moe_dispatch: dx[t] = sum of dxs over the slots of t (f32 sums)."""
-    dev, dt = _dev(dxs, "dxs"), _dtype(dxs, "dxs")
-    T = _slots(slot_pos, K, has_shared)
-    if dxs.dim() != 2:
-        raise ValueError("dxs must have two dimensions")
-    H, S = dxs.shape[1], T * (K + int(has_shared))
-    _want(dxs, dxs.dtype, (S, H), dev, "dxs")
-    _want(slot_pos, torch.int32, (S,), dev, "slot_pos")
-    dx = _out(dx, dxs.dtype, (T, H), dev, "dx")
-    check(_lib.lib().moe_dispatch_grad(dxs.data_ptr(), slot_pos.data_ptr(), T, K, H,
-                                       int(has_shared), dt, dx.data_ptr(), _stream()))
-    return dx
-
-
-def _combine_typed(y_slots, w, slot_pos, gate, K, has_shared, out):
-    dev, dt = _dev(y_slots, "y_slots"), _dtype(y_slots, "y_slots")
-    T = _slots(slot_pos, K, has_shared)
-    if y_slots.dim() != 2:
-        raise ValueError("y_slots must have two dimensions")
-    H, S = y_slots.shape[1], T * (K + int(has_shared))
-    _want(y_slots, y_slots.dtype, (S, H), dev, "y_slots")
-    _want(w, torch.float32, (T, K), dev, "w")
-    _want(slot_pos, torch.int32, (S,), dev, "slot_pos")
-    if gate is not None:
-        _want(gate, torch.float32, (T,), dev, "gate")
-    out = _out(out, y_slots.dtype, (T, H), dev, "out")
-    check(_lib.lib().moe_combine_typed(y_slots.data_ptr(), w.data_ptr(), slot_pos.data_ptr(),
-                                       _ptr(gate), T, K, H, int(has_shared), dt, out.data_ptr(),
-                                       _stream()))
-    return out
+    return _lib.binding().dispatch_grad(dxs, slot_pos, K, has_shared, dx)
 
 
 def moe_combine_grad(dout: torch.Tensor, y_slots: torch.Tensor, w: torch.Tensor,
@@ -503,54 +383,15 @@ def moe_combine_grad(dout: torch.Tensor, y_slots: torch.Tensor, w: torch.Tensor,
     """Gradients of moe_combine (gate None) or moe_combine_gated by the rows, the
     routing weights and the gate logit: (dy_slots, dw, dgate or None).  Rows of
     dy_slots that no slot points at stay as they are; dw is 0 for skipped slots."""
-    dev, dt = _dev(dout, "dout"), _dtype(dout, "dout")
-    T = _slots(slot_pos, K, has_shared)
-    if dout.dim() != 2:
-        raise ValueError("dout must have two dimensions")
-    H, S = dout.shape[1], T * (K + int(has_shared))
-    _want(dout, dout.dtype, (T, H), dev, "dout")
-    _want(y_slots, dout.dtype, (S, H), dev, "y_slots")
-    _want(w, torch.float32, (T, K), dev, "w")
-    _want(slot_pos, torch.int32, (S,), dev, "slot_pos")
-    if gate is not None:
-        _want(gate, torch.float32, (T,), dev, "gate")
-        dgate = _like(dgate, gate, dev, "dgate")
-    elif dgate is not None:
-        raise ValueError("dgate is given without a gate")
-    dy_slots = _like(dy_slots, y_slots, dev, "dy_slots")
-    dw = _like(dw, w, dev, "dw")
-    check(_lib.lib().moe_combine_grad(dout.data_ptr(), y_slots.data_ptr(), w.data_ptr(),
-                                      slot_pos.data_ptr(), _ptr(gate), T, K, H, int(has_shared),
-                                      dt, dy_slots.data_ptr(), dw.data_ptr(), _ptr(dgate),
-                                      _stream()))
-    return dy_slots, dw, dgate
+    return _lib.binding().combine_grad(dout, y_slots, w, slot_pos, K, has_shared, gate, dy_slots,
+                                       dw, dgate)
 
 
 def moe_route_topk_grad(ids: torch.Tensor, w: torch.Tensor, dw: torch.Tensor, E: int,
                         dlogits: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient of moe_route_topk's weights by the logits, [T, E] (zero for the
     experts not chosen; the choice itself has no gradient)."""
-    dev = _dev(ids, "ids")
-    if ids.dim() != 2:
-        raise ValueError("ids must have two dimensions")
-    T, K = ids.shape
-    _want(ids, torch.int32, (T, K), dev, "ids")
-    _want(w, torch.float32, (T, K), dev, "w")
-    _want(dw, torch.float32, (T, K), dev, "dw")
-    dlogits = _out(dlogits, torch.float32, (T, E), dev, "dlogits")
-    check(_lib.lib().moe_route_topk_grad(ids.data_ptr(), w.data_ptr(), dw.data_ptr(), T, E, K,
-                                         dlogits.data_ptr(), _stream()))
-    return dlogits
-
-
-def _gate_kind(gate, rows: torch.Tensor, dev) -> int:
-    if gate is None:
-        return _lib.MOE_GATE_NONE
-    if gate.dim() == 1:
-        _want(gate, torch.float32, (rows.shape[0],), dev, "gate")
-        return _lib.MOE_GATE_TOKEN
-    _want(gate, rows.dtype, rows.shape, dev, "gate")
-    return _lib.MOE_GATE_ELEMENT
+    return _lib.binding().route_topk_grad(ids, w, dw, E, dlogits)
 
 
 def moe_block_norm(residual: torch.Tensor, y: Optional[torch.Tensor] = None,
@@ -570,32 +411,8 @@ def moe_block_norm(residual: torch.Tensor, y: Optional[torch.Tensor] = None,
     residual, y: [T, H] bf16, float16 or float32; w_post, w_pre: float32 [H];
     gate: None, float32 [T] or [T, H] like y.  Without y, r is residual itself
     and only n is computed.  r_out may be residual (an update in place)."""
-    dev, dt = _dev(residual, "residual"), _dtype(residual, "residual")
-    if residual.dim() != 2:
-        raise ValueError("residual must have two dimensions")
-    T, H = shape = residual.shape
-    _want(residual, residual.dtype, shape, dev, "residual")
-    if y is None and (gate is not None or w_post is not None or r_out is not None or w_pre is None):
-        raise ValueError("without y only w_pre and n_out are given")
-    kind = _gate_kind(gate, residual, dev)
-    if y is not None:
-        _want(y, residual.dtype, shape, dev, "y")
-        r_out = _like(r_out, residual, dev, "r_out")
-    if w_post is not None:
-        _want(w_post, torch.float32, (H,), dev, "w_post")
-        rstd_post = _out(rstd_post, torch.float32, (T,), dev, "rstd_post")
-    elif rstd_post is not None:
-        raise ValueError("rstd_post is given without w_post")
-    if w_pre is not None:
-        _want(w_pre, torch.float32, (H,), dev, "w_pre")
-        n_out = _like(n_out, residual, dev, "n_out")
-        rstd_pre = _out(rstd_pre, torch.float32, (T,), dev, "rstd_pre")
-    elif n_out is not None or rstd_pre is not None:
-        raise ValueError("n_out or rstd_pre is given without w_pre")
-    check(_lib.lib().moe_block_norm(residual.data_ptr(), _ptr(y), _ptr(gate), kind, _ptr(w_post),
-                                    _ptr(w_pre), res_scale, out_scale, eps, T, H, dt, _ptr(r_out),
-                                    _ptr(n_out), _ptr(rstd_post), _ptr(rstd_pre), _stream()))
-    return (residual if y is None else r_out), n_out, rstd_post, rstd_pre
+    return _lib.binding().block_norm(residual, y, gate, w_post, w_pre, res_scale, out_scale, eps,
+                                     r_out, n_out, rstd_post, rstd_pre)
 
 
 def moe_block_norm_grad(dr: Optional[torch.Tensor], dn: Optional[torch.Tensor], r: torch.Tensor,
@@ -609,58 +426,12 @@ def moe_block_norm_grad(dr: Optional[torch.Tensor], dn: Optional[torch.Tensor], 
     n (dn; None exactly where w_pre is).  r, y, gate and the statistics are the
     forward call's.  Returns (dresidual, dy, dgate, dw_post, dw_pre), None in
     the place of what was not given; dw_* are float32 sums over the tokens."""
-    dev, dt = _dev(r, "r"), _dtype(r, "r")
-    if r.dim() != 2:
-        raise ValueError("r must have two dimensions")
-    T, H = shape = r.shape
-    _want(r, r.dtype, shape, dev, "r")
-    if dr is None and dn is None:
-        raise ValueError("dr and dn are both missing")
-    if dr is not None:
-        _want(dr, r.dtype, shape, dev, "dr")
-    if (dn is None) != (w_pre is None):
-        raise ValueError("dn and w_pre are given together")
-    dy = dgate = dw_post = dw_pre = None
-    if y is None and (gate is not None or w_post is not None):
-        raise ValueError("a gate or w_post is given without y")
-    kind = _gate_kind(gate, r, dev)
-    f32 = torch.float32
-    if w_pre is not None:
-        _want(dn, r.dtype, shape, dev, "dn")
-        _want(w_pre, f32, (H,), dev, "w_pre")
-        if rstd_pre is None:
-            raise ValueError("w_pre needs rstd_pre")
-        _want(rstd_pre, f32, (T,), dev, "rstd_pre")
-        dw_pre = torch.empty_like(w_pre)
-    if y is not None:
-        _want(y, r.dtype, shape, dev, "y")
-        dy = torch.empty_like(r)
-        if gate is not None:
-            dgate = torch.empty_like(gate)
-    if w_post is not None:
-        _want(w_post, f32, (H,), dev, "w_post")
-        if rstd_post is None:
-            raise ValueError("w_post needs rstd_post")
-        _want(rstd_post, f32, (T,), dev, "rstd_post")
-        dw_post = torch.empty_like(w_post)
-    dres = torch.empty_like(r)
-    L = _lib.lib()
-    nb = L.moe_block_norm_workspace_bytes(T, H, dt)
-    ws = _scratch(ws, nb, dev)
-    check(L.moe_block_norm_grad(_ptr(dr), _ptr(dn), r.data_ptr(), _ptr(y), _ptr(gate), kind,
-                                _ptr(w_post), _ptr(w_pre), _ptr(rstd_post), _ptr(rstd_pre),
-                                res_scale, out_scale, T, H, dt, dres.data_ptr(), _ptr(dy),
-                                _ptr(dgate), _ptr(dw_post), _ptr(dw_pre), ws.data_ptr(), nb,
-                                _stream()))
-    return dres, dy, dgate, dw_post, dw_pre
+    return _lib.binding().block_norm_grad(dr, dn, r, y, gate, w_post, w_pre, rstd_post, rstd_pre,
+                                          res_scale, out_scale, ws)
 
 
 _FP8 = torch.float8_e4m3fn
 _BLOCK = 128
-
-
-def _codes(t: torch.Tensor, shape, dev, name: str) -> None:
-    _want(t, _FP8 if t.dtype == _FP8 else torch.uint8, shape, dev, name)
 
 
 @dataclass
@@ -690,14 +461,6 @@ class FP8Matrix:
         return FP8Matrix(self.codes.view(torch.uint8).t().contiguous().view(self.codes.dtype),
                          self.scales.t().contiguous())
 
-    def struct(self, dev) -> _lib.MoeFp8Matrix:
-        if self.codes.dim() != 2:
-            raise ValueError("codes must have two dimensions")
-        N, K = self.codes.shape
-        _codes(self.codes, (N, K), dev, "codes")
-        _want(self.scales, torch.float32, (-(-N // _BLOCK), -(-K // _BLOCK)), dev, "scales")
-        return _lib.MoeFp8Matrix(self.codes.data_ptr(), self.scales.data_ptr(), N, K)
-
 
 @dataclass
 class FP8Weights:
@@ -711,51 +474,19 @@ class FP8Weights:
     I: int
     has_shared: bool
 
-    def struct(self, dev) -> _lib.MoeFp8Weights:
-        G, H, I = self.E + int(self.has_shared), self.H, self.I
-        _codes(self.gu_codes, (G, 2 * I, H), dev, "gu_codes")
-        _want(self.gu_scales, torch.float32, (G, 2 * I // _BLOCK, H // _BLOCK), dev, "gu_scales")
-        _codes(self.dn_codes, (G, H, I), dev, "dn_codes")
-        _want(self.dn_scales, torch.float32, (G, H // _BLOCK, I // _BLOCK), dev, "dn_scales")
-        return _lib.MoeFp8Weights(self.gu_codes.data_ptr(), self.gu_scales.data_ptr(),
-                                  self.dn_codes.data_ptr(), self.dn_scales.data_ptr(), self.E, H,
-                                  I, int(self.has_shared))
-
 
 def moe_fp8_quant(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
                   scales: Optional[torch.Tensor] = None):
     """Rows of x (bf16, float16 or float32 [T, K]) as e4m3 codes with a float32
     scale per 128 along K: (codes float8_e4m3fn [T, K], scales [T, ceil(K/128)])."""
-    dev, dt = _dev(x, "x"), _dtype(x, "x")
-    if x.dim() != 2:
-        raise ValueError("x must have two dimensions")
-    T, K = x.shape
-    _want(x, x.dtype, (T, K), dev, "x")
-    codes = _out(codes, _FP8, (T, K), dev, "codes")
-    scales = _out(scales, torch.float32, (T, -(-K // _BLOCK)), dev, "scales")
-    check(_lib.lib().moe_fp8_quant(x.data_ptr(), T, K, dt, codes.data_ptr(), scales.data_ptr(),
-                                   _stream()))
-    return codes, scales
+    return _lib.binding().fp8_quant(x, codes, scales)
 
 
 def moe_fp8_linear(M: FP8Matrix, x: torch.Tensor, ws: Optional[torch.Tensor] = None,
                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """x [T, K] times the matrix's transpose, [T, N] in x's type: x is quantised
     as by moe_fp8_quant, the product summed in f32."""
-    dev, dt = _dev(x, "x"), _dtype(x, "x")
-    st = M.struct(dev)
-    if x.dim() != 2 or x.shape[1] != st.K:
-        raise ValueError(f"x must be [T, {st.K}], got {tuple(x.shape)}")
-    T = x.shape[0]
-    _want(x, x.dtype, (T, st.K), dev, "x")
-    out = _out(out, x.dtype, (T, st.N), dev, "out")
-    L = _lib.lib()
-    nb = L.moe_fp8_linear_workspace_bytes(T, st.K)
-    if nb:
-        ws = _scratch(ws, nb, dev)
-    check(L.moe_fp8_linear(ctypes.byref(st), x.data_ptr(), T, dt, out.data_ptr(), _ptr(ws), nb,
-                           _stream()))
-    return out
+    return _lib.binding().fp8_linear(M.codes, M.scales, x, ws, out)
 
 
 def moe_fp8_expert_ffn(W: FP8Weights, x: torch.Tensor, K: int, offsets: torch.Tensor,
@@ -764,25 +495,9 @@ def moe_fp8_expert_ffn(W: FP8Weights, x: torch.Tensor, K: int, offsets: torch.Te
                        y_slots: Optional[torch.Tensor] = None) -> torch.Tensor:
     """moe_expert_ffn for a bank in e4m3 with block scales: the rows and the
     intermediate are quantised per 128.  Returns y_slots [T*K (+ T), H] bf16."""
-    dev = _dev(x, "x")
-    if x.dim() != 2 or x.shape[1] != W.H:
-        raise ValueError("x width does not match the weight bank")
-    T, H = x.shape
-    _want(x, torch.bfloat16, (T, H), dev, "x")
-    S = T * (K + int(W.has_shared))
-    G = W.E + int(W.has_shared)
-    _want(offsets, torch.int32, (G + 1,), dev, "offsets")
-    _want(sorted_slot, torch.int32, (S,), dev, "sorted_slot")
-    _want(groups, torch.int32, (G + 1,), dev, "groups")
-    y_slots = _out(y_slots, torch.bfloat16, (S, H), dev, "y_slots")
-    st = W.struct(dev)
-    L = _lib.lib()
-    nb = L.moe_fp8_expert_ffn_workspace_bytes(T, K, H, W.I, int(W.has_shared))
-    ws = _scratch(ws, nb, dev)
-    check(L.moe_fp8_expert_ffn(ctypes.byref(st), x.data_ptr(), T, K, offsets.data_ptr(),
-                               sorted_slot.data_ptr(), groups.data_ptr(), y_slots.data_ptr(),
-                               ws.data_ptr(), nb, _stream()))
-    return y_slots
+    return _lib.binding().fp8_expert_ffn(W.gu_codes, W.gu_scales, W.dn_codes, W.dn_scales, W.E, W.H,
+                                         W.I, W.has_shared, x, K, offsets, sorted_slot, groups, ws,
+                                         y_slots)
 
 
 def timing_enable(on: bool = True) -> None:
