@@ -228,7 +228,9 @@ PyObject* combine(Args a) {
   const int dt = dtype_of(y, "y_slots"), T = tokens(pos, K, sh);
   two_dims(y, "y_slots");
   const int64_t H = y.size(1), S = (int64_t)T * (K + sh);
-  need(y, y.scalar_type(), {S, H}, dev, "y_slots");
+  // a longer buffer of rows may serve fewer tokens
+  if (y.size(0) < S) refuse("y_slots must have ", S, " rows at least, got ", y.size(0));
+  need(y, y.scalar_type(), y.sizes(), dev, "y_slots");
   const float* wp = (const float*)need(w, at::kFloat, {T, K}, dev, "w");
   const int32_t* pp = (const int32_t*)need(pos, at::kInt, {S}, dev, "slot_pos");
   const float* gp = gate ? (const float*)need(*gate, at::kFloat, {T}, dev, "gate") : nullptr;

@@ -341,8 +341,9 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
 
   // The next step to bring: how many are left, its block along K and buffer.
   // Tokens (with their scales) and weights of a step are asked for at different
-  // times, tokens first.  Past the last step the buffers are empty ones (zeros
-  // come, to where nobody reads): every wave then has the same number of
+  // times, tokens first.  Past the last step the buffers are empty ones, at
+  // offset 0 (the range check subtracts the scalar offset from the size), and
+  // zeros come, to where nobody reads: every wave then has the same number of
   // operations under way at every wait, and the loop has no branch, behind
   // which the compiler would move the sums of half a step and spill.
   int d_left = KG == 1 ? ntb * nb : (nb - kg + KG - 1) / KG, d_k = kg, d_at = 0;
@@ -351,7 +352,7 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
     u32x4 xb = xbuf, sb = sbuf;
     xb.z = d_left > 0 ? xb.z : 0u;
     sb.z = d_left > 0 ? sb.z : 0u;
-    const uint32_t kb = dma_offset((uint32_t)d_k * 4u);
+    const uint32_t kb = dma_offset(d_left > 0 ? (uint32_t)d_k * 4u : 0u);
 #pragma unroll
     for (int i = 0; i < DX; ++i)
       dma_b128(xb, xoff[i], kb * (kQB / 4), ldsw + d_at + kTok + i * NT * 16);
@@ -364,7 +365,7 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
     // a chunk past the end of a weight row is read from the start of the block
     // instead: the tokens' codes there are zeros
     const uint32_t back = MODE == kTileLinear && (int)k + chunk >= a.K ? (uint32_t)chunk : 0u;
-    const uint32_t so = dma_offset(MODE == kTileLinear ? k : k + d_col);
+    const uint32_t so = dma_offset(d_left <= 0 ? 0u : MODE == kTileLinear ? k : k + d_col);
 #pragma unroll
     for (int i = 0; i < DW; ++i) dma_b128<decltype(once)::value>(wb, woff[i] - back, so, ldsw + d_at + i * NT * 16);
     --d_left;

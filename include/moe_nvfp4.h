@@ -491,6 +491,7 @@ int moe_block_norm_grad(const void* dr, const void* dn, const void* r_out, const
  *   ws  at least moe_fp8_linear_workspace_bytes(T, K) bytes (0: none needed)
  *
  * A NaN or an infinity in a row makes that row's outputs NaN and no others.
+ * The outputs may not overlap the inputs.
  * Limits: K a multiple of 16, N a multiple of 8, both in [16, 65536] and
  * [8, 65536]; pointers of codes, x and out aligned to 16 bytes.
  */
@@ -527,8 +528,9 @@ int moe_fp8_linear(const moe_fp8_matrix* M, const void* x, int T, int dtype, voi
  *
  *   ws  at least moe_fp8_expert_ffn_workspace_bytes(T, K, H, I, has_shared)
  *
- * Rows whose sorted_slot entry is out of range are skipped.  Limits: those of
- * the permutation; H and I multiples of 128 in [128, 8192], T*H < 2^32;
+ * Rows whose sorted_slot entry is out of range are skipped.  y_slots may not
+ * overlap x.  Limits: those of the permutation; H and I multiples of 128 in
+ * [128, 8192], T*H < 2^32;
  * pointers of codes, x and y_slots aligned to 16 bytes.
  */
 typedef struct moe_fp8_weights {

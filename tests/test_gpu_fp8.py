@@ -214,6 +214,33 @@ def test_experts(moe, T, E, K, H, I, shared):
     _check_experts(moe, bank, x, ids, E, H, I, shared)
 
 
+# enough row tiles that a block takes two column tiles in a row, of gate_up with
+# a single block along K, and of down with one and with two
+@pytest.mark.parametrize("T,E,K,H,I", [(100, 512, 8, 128, 1024), (60, 320, 10, 2048, 128), (80, 512, 8, 1024, 256)])
+def test_experts_many_groups(moe, T, E, K, H, I):
+    flush(f"fp8 experts, many groups T={T} E={E} H={H} I={I}")
+    torch.manual_seed(T)
+    codes = lambda *s: (torch.randn(s, device="cuda") * 100).clamp(-448, 448).to(torch.float8_e4m3fn)  # noqa: E731
+    bank = (codes(E + 1, 2 * I, H), (torch.rand(E + 1, 2 * I // 128, H // 128, device="cuda") + 0.5) / (100 * H ** 0.5),
+            codes(E + 1, H, I), (torch.rand(E + 1, H // 128, I // 128, device="cuda") + 0.5) / (100 * I ** 0.5))
+    x = torch.randn(T, H, device="cuda").bfloat16()
+    ids = torch.topk(torch.randn(T, E, device="cuda"), K, dim=1).indices.int()
+    ids[:, 0] = 3  # one group of several rows tiles' worth
+    counts, offsets, ss, pos, groups = moe.moe_permute(ids, E, True)
+    y = f64(moe.moe_fp8_expert_ffn(moe.FP8Weights(*bank, E, H, I, True), x, K, offsets, ss, groups))
+    off, slots = offsets.cpu().numpy(), ss.cpu().numpy()
+    xf = x.float().cpu().numpy()
+    for g in [0, 1, 3, E // 2, E - 1, E]:
+        a, b = off[g], off[g + 1]
+        if a == b:
+            continue
+        rows = slots[a:b] // K if g < E else slots[a:b] - T * K
+        w = [(c[g].double().cpu().numpy(), s[g].cpu().numpy()) for c, s in (bank[:2], bank[2:])]
+        ref, err = fp8block.expert(xf[rows], w[0], w[1], I)
+        within(y[a:b], ref, rounded(ref, torch.bfloat16, err), f"group {g}")
+    assert np.isfinite(y).all()
+
+
 @pytest.mark.parametrize("T", [12, 60])
 def test_experts_with_repeated_and_foreign_ids(moe, T):
     """An expert named twice for a token gets two rows (more than 16 in a decode

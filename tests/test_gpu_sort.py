@@ -119,6 +119,17 @@ def test_special_values_stay_in_their_rows(moe):
     assert (~torch.isfinite(dw.cpu())).nonzero().tolist() in ([[2, 0], [4, 0], [4, 1]],)
 
 
+def test_combine_takes_a_longer_buffer(moe):
+    gen = torch.Generator().manual_seed(6)
+    T, K, H = 3, 2, 24
+    pos, w = gpu(permutation(gen, T, K, False)), gpu(torch.rand(T, K, generator=gen))
+    for dtype in DTYPES:
+        y = gpu(normal(gen, (20, H), dtype))
+        assert torch.equal(moe.moe_combine(y, w, pos, K, False), moe.moe_combine(y[:6].contiguous(), w, pos, K, False))
+        with pytest.raises(ValueError, match="6 rows"):
+            moe.moe_combine(y[:5], w, pos, K, False)
+
+
 def test_f16_overflow_and_subnormals(moe):
     T, K, H = 2, 2, 8
     pos = torch.tensor([0, 1, 2, 3], dtype=torch.int32)
