@@ -579,7 +579,7 @@ int moe_fp8_quant(const void* x, int T, int K, int dtype, uint8_t* codes, float*
     return fail(MOE_EINVAL, "moe_fp8_quant: rows must be aligned to 16 bytes");
   int rc = ensure_init();
   if (rc != MOE_OK) return rc;
-  return launched(moe::launch_fp8_quant(x, T, K, dtype, K, codes, scales, (hipStream_t)stream),
+  return launched(moe::launch_fp8_quant(x, T, K, dtype, codes, scales, (hipStream_t)stream),
                   "moe_fp8_quant launch");
 }
 

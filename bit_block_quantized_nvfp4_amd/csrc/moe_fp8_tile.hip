@@ -16,6 +16,8 @@
 // permutation is applied to the addresses that it reads.
 #include <math.h>
 
+#include <algorithm>
+
 #include "moe_ffn_common.hpp"
 #include "moe_fp8.hpp"
 #include "moe_internal.hpp"
@@ -23,9 +25,14 @@
 
 namespace moe {
 
+// Rows whose scales of one block along K stand together where a dense product
+// reads them (a multiple of every row tile).
+constexpr int kScaleRows = 256;
+
 // One thread per 8 values, 16 lanes to a block of 128.  ldq: bytes of a code
-// row (K, or K rounded up to 128 with zeros behind).
-template <int DT>
+// row (K, or K rounded up to 128 with zeros behind).  Scale of row t and block
+// b: place t nb + b; TILED: b + nb (t / 256) runs of 256, in it place t % 256.
+template <int DT, bool TILED>
 __device__ __forceinline__ void quant_block(unsigned block, const void* __restrict__ x, int T,
                                             int K, int ldq, int lg, int cb,
                                             uint8_t* __restrict__ codes,
@@ -60,15 +67,17 @@ __device__ __forceinline__ void quant_block(unsigned block, const void* __restri
     *(u32x2*)(codes + (size_t)t * ldq + 8 * c) =
         u32x2{fp8x4(f[0] * m, f[1] * m, f[2] * m, f[3] * m),
               fp8x4(f[4] * m, f[5] * m, f[6] * m, f[7] * m)};
-  if ((c & 15) == 0) scales[(size_t)t * nb + c / 16] = am / 448.0f;
+  if ((c & 15) == 0)
+    scales[TILED ? ((size_t)(t / kScaleRows) * nb + c / 16) * kScaleRows + t % kScaleRows
+                 : (size_t)t * nb + c / 16] = am / 448.0f;
 }
 
-template <int DT>
+template <int DT, bool TILED>
 __global__ __launch_bounds__(256) void k_fp8_quant(const void* __restrict__ x, int T, int K,
                                                    int ldq, int lg, int cb,
                                                    uint8_t* __restrict__ codes,
                                                    float* __restrict__ scales) {
-  quant_block<DT>(blockIdx.x, x, T, K, ldq, lg, cb, codes, scales);
+  quant_block<DT, TILED>(blockIdx.x, x, T, K, ldq, lg, cb, codes, scales);
 }
 
 // The row tiles of the grouped products: items[0] = their number, then from
@@ -125,7 +134,7 @@ __global__ __launch_bounds__(256) void k_fp8_prep(const uint16_t* __restrict__ x
                                                   const int32_t* __restrict__ offsets, int G,
                                                   int32_t* __restrict__ items) {
   if (blockIdx.x == 0) write_items(offsets, G, items);
-  else quant_block<MOE_DT_BF16>(blockIdx.x - 1, x, T, K, K, lg, cb, codes, scales);
+  else quant_block<MOE_DT_BF16, false>(blockIdx.x - 1, x, T, K, K, lg, cb, codes, scales);
 }
 
 enum { kTileLinear = 0, kTileGateUp = 1, kTileDown = 2 };
@@ -134,9 +143,10 @@ struct TileArgs {
   const uint8_t* codes;    // weights [N][K] (of group 0)
   const float* scales;     // [ceil(N/128)][nb]
   const uint8_t* xq;       // token codes [rows][nb * 128]
-  const float* xs;         // token scales [rows][nb]
+  const float* xs;         // token scales: linear [row / 256][nb][256], gate_up
+                           // [T][nb], down [item][nb][kPM]
   void* out;
-  float* out_scales;       // gate_up: scales of h
+  float* out_scales;       // gate_up: scales of h, as down reads them
   const int32_t* items;    // grouped modes: row tiles (write_items)
   const int32_t* sorted_slot;
   int R;                   // rows (linear)
@@ -233,6 +243,7 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
                 "the groups' sums fit");
   __shared__ __align__(1024) uint8_t lds_all[KG * NBUF * kBuf];
   __shared__ float wsc[NS * kTileScales];
+  __shared__ float nowhere[64];                // for loads that bring nothing: they write zeros
   __shared__ __align__(16) uint8_t side[MODE == kTileGateUp ? WN * BM * 4
                                         : MODE == kTileDown ? NW * 16 * TN * ES : 16];
   const int kg = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane((int)threadIdx.x / NT);
@@ -246,6 +257,7 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
 
   const uint8_t* codes = a.codes;
   const float* scales = a.scales;
+  size_t item_at = 0;                          // the item's scales of h
   int m0, rows, n0;                            // first token row, rows left, first column
   bool single = false;                         // the group has no other row tile
   if (MODE == kTileLinear) {
@@ -261,9 +273,12 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
     n0 = (in / gm) * BN;
     rows = a.R - m0;
   } else {
-    // the column tiles of one row tile back to back on one XCD
+    // the column tiles of two row tiles back to back on one XCD: the tiles of a
+    // group of several share its weights in the L2 (T = 4096: 271 + 174 us; in
+    // runs of one row tile 278 + 179 us, of four 282 + 178 us)
     const int per = a.nt / ntb;
-    const int lin = pf_item_of_block(blockIdx.x, gridDim.x, per), item = lin / per;
+    const int lin = pf_item_of_block(blockIdx.x, gridDim.x, 2 * per), item = lin / per;
+    item_at = (size_t)item * ((MODE == kTileGateUp ? a.N : a.K) / kQB) * kPM;
     const int n = a.items[0];
     const i32x4 e = ((const i32x4*)(a.items + 4))[item];
     if (item >= n) return;
@@ -302,9 +317,16 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
                             (uint32_t)min(BN * ntb, a.N - n0) * (uint32_t)a.K);
   const u32x4 xbuf = MODE == kTileGateUp ? buf_of(a.xq, (uint32_t)a.T * ldx)
                                    : buf_of(a.xq + (size_t)m0 * ldx, (uint32_t)rows * ldx);
-  const u32x4 sbuf = MODE == kTileGateUp
-                   ? buf_of(a.xs, (uint32_t)a.T * (uint32_t)nb * 4u)
-                   : buf_of(a.xs + (size_t)m0 * nb, (uint32_t)rows * (uint32_t)nb * 4u);
+  // Token scales: 64 rows of a step are one load of a wave, 256 bytes in one
+  // piece where the row tile is known when they are written: scattered ones take
+  // a lookup each, 64 of them as many as 8 KB of codes.  8192 x 4096 x 4096: 166
+  // us with all eight waves bringing 64 scattered scales, 148 us with the four
+  // that have to, 146 us so; 8192 x 8192 x 8192: 538, 513 and 492 us.
+  constexpr int SR = MODE == kTileLinear ? kScaleRows : MODE == kTileDown ? kPM : 1;
+  const u32x4 sbuf = MODE == kTileGateUp ? buf_of(a.xs, (uint32_t)a.T * (uint32_t)nb * 4u)
+                   : MODE == kTileDown   ? buf_of(a.xs + item_at, (uint32_t)(nb * SR) * 4u)
+                   : buf_of(a.xs + (size_t)(m0 / SR) * nb * SR + m0 % SR,
+                            (uint32_t)(nb * SR - m0 % SR) * 4u);
   // Chunk i of this thread: LDS row lr, place tid % 8; rows of one thread are
   // NT / 8 apart, a multiple of 8, so its chunk of the row is always the same.
   const int chunk = 16 * ((tid & 7) ^ ((tid >> 3) & 7));
@@ -314,10 +336,13 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
     woff[i] = (uint32_t)wrow_of((i * NT + tid) >> 3) * (uint32_t)a.K + chunk;
 #pragma unroll
   for (int i = 0; i < DX; ++i) xoff[i] = (uint32_t)xrow_of((i * NT + tid) >> 3) * ldx + chunk;
-  const int srow = 64 * (wv % (BM / 64)) + lane;  // every wave brings 64 token scales
-  const uint32_t soff = (uint32_t)xrow_of(srow) * (uint32_t)nb * 4u;
+  // the first BM / 64 waves bring 64 token scales each, the others none
+  const bool brings = wv < BM / 64;
+  const int srow = 64 * (wv % (BM / 64)) + lane;
+  const uint32_t soff = MODE == kTileGateUp ? (uint32_t)xrow_of(srow) * (uint32_t)nb * 4u : srow * 4u;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
   const uint32_t ldsw = lds0 + wv * 1024;
+  const uint32_t ldsn = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) float*)nowhere;
 
   // The weight scales of all steps, one per 128 weight rows of a tile, in LDS: a
   // load of one in the loop would wait for the DMA under way.  gate_up: the
@@ -351,12 +376,13 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
   auto dma_tokens = [&]() __attribute__((always_inline)) {
     u32x4 xb = xbuf, sb = sbuf;
     xb.z = d_left > 0 ? xb.z : 0u;
-    sb.z = d_left > 0 ? sb.z : 0u;
-    const uint32_t kb = dma_offset(d_left > 0 ? (uint32_t)d_k * 4u : 0u);
+    sb.z = d_left > 0 && brings ? sb.z : 0u;
+    const uint32_t k = d_left > 0 ? (uint32_t)d_k : 0u;
+    const uint32_t kx = dma_offset(k * kQB), ks = dma_offset(brings ? k * (SR * 4) : 0u);
 #pragma unroll
     for (int i = 0; i < DX; ++i)
-      dma_b128(xb, xoff[i], kb * (kQB / 4), ldsw + d_at + kTok + i * NT * 16);
-    dma_b32(sb, soff, kb, lds0 + d_at + kScale + 256 * (wv % (BM / 64)));
+      dma_b128(xb, xoff[i], kx, ldsw + d_at + kTok + i * NT * 16);
+    dma_b32(sb, soff, ks, brings ? lds0 + d_at + kScale + 256 * wv : ldsn);
   };
   auto dma_weights = [&](auto once) __attribute__((always_inline)) {
     u32x4 wb = wbuf;
@@ -509,7 +535,7 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
           *(uint32_t*)(dst + 16 * i + 4 * fq) = fp8x4(acc[i][j][0] * m, acc[i][j][1] * m,
                                                       acc[i][j][2] * m, acc[i][j][3] * m);
         if (wn == 0 && fq == 0)
-          a.out_scales[(size_t)(m0 + r) * (a.N / kQB) + n / kQB] = am / 448.0f;
+          a.out_scales[item_at + (size_t)(n / kQB) * kPM + r] = am / 448.0f;
       }
     }
   };
@@ -649,7 +675,8 @@ static int linear_tile(int T, int N) {
 void register_fp8_tile_kernels(std::vector<const void*>& k) {
   auto add = [&](auto D) {
     constexpr int DT = decltype(D)::value;
-    k.push_back((const void*)&k_fp8_quant<DT>);
+    k.push_back((const void*)&k_fp8_quant<DT, false>);
+    k.push_back((const void*)&k_fp8_quant<DT, true>);
     for (int s = 0; s < 4; ++s)
       by_linear_tile<DT>(s, [&](auto kernel, int, int, int) { k.push_back((const void*)kernel); });
   };
@@ -659,14 +686,20 @@ void register_fp8_tile_kernels(std::vector<const void*>& k) {
   k.push_back((const void*)&k_fp8_tile<kTileDown, MOE_DT_BF16, 128, 128, 2, 2, 2>);
 }
 
-hipError_t launch_fp8_quant(const void* x, int T, int K, int dtype, int ldq, uint8_t* codes,
-                            float* scales, hipStream_t s) {
+template <bool TILED>
+static hipError_t quantise(const void* x, int T, int K, int dtype, int ldq, uint8_t* codes,
+                           float* scales, hipStream_t s) {
   const RowGrid g = row_grid(T, (K + kQB - 1) / kQB * 16);
   by_dtype(dtype, [&](auto D) {
-    MOE_LAUNCH("fp8_quant", s, k_fp8_quant<decltype(D)::value>, dim3(g.blocks), dim3(256), 0, s, x,
+    MOE_LAUNCH("fp8_quant", s, (k_fp8_quant<decltype(D)::value, TILED>), dim3(g.blocks), dim3(256), 0, s, x,
                T, K, ldq, g.lg, g.cb, codes, scales);
   });
   return hipGetLastError();
+}
+
+hipError_t launch_fp8_quant(const void* x, int T, int K, int dtype, uint8_t* codes, float* scales,
+                            hipStream_t s) {
+  return quantise<false>(x, T, K, dtype, K, codes, scales, s);
 }
 
 static size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -674,7 +707,8 @@ static int blocks_of(int K) { return (K + kQB - 1) / kQB; }
 
 size_t fp8_linear_workspace_bytes(int T, int K) {
   if (T <= kFp8StreamMaxT) return 0;
-  return up256((size_t)T * blocks_of(K) * kQB) + up256((size_t)T * blocks_of(K) * sizeof(float));
+  return up256((size_t)T * blocks_of(K) * kQB) +
+         ((size_t)T + kScaleRows - 1) / kScaleRows * kScaleRows * blocks_of(K) * sizeof(float);
 }
 
 hipError_t launch_fp8_linear(const moe_fp8_matrix& M, const void* x, int T, int dtype, void* out,
@@ -683,7 +717,7 @@ hipError_t launch_fp8_linear(const moe_fp8_matrix& M, const void* x, int T, int 
   const int nb = blocks_of(M.K);
   uint8_t* xq = (uint8_t*)ws;
   float* xs = (float*)(xq + up256((size_t)T * nb * kQB));
-  hipError_t e = launch_fp8_quant(x, T, M.K, dtype, nb * kQB, xq, xs, s);
+  hipError_t e = quantise<true>(x, T, M.K, dtype, nb * kQB, xq, xs, s);
   if (e != hipSuccess) return e;
   TileArgs a{};
   a.codes = M.codes;
@@ -704,8 +738,9 @@ hipError_t launch_fp8_linear(const moe_fp8_matrix& M, const void* x, int T, int 
   return hipGetLastError();
 }
 
-// Row tiles of S rows in G groups, at most: the full ones and a partial one per group.
-static size_t max_tiles(size_t S, int G) { return S / kPM + (size_t)G; }
+// Row tiles of S rows in G groups, at most: the full ones and a partial one per
+// group, none without a row.
+static size_t max_tiles(size_t S, int G) { return std::min(S, S / kPM + (size_t)G); }
 
 // Column tiles that one block takes in a row: a longer stream hides more of a
 // block's start and of its outputs, as long as there are blocks enough to share
@@ -720,8 +755,9 @@ static int tiles_per_block(size_t S, int G, int nt) {
 size_t fp8_expert_ffn_workspace_bytes(int T, int K, int H, int I, int has_shared) {
   const size_t S = (size_t)T * K + (has_shared ? T : 0);
   if (T <= kDecodeMaxT) return up256(S * I * sizeof(float));
+  const size_t tiles = max_tiles(S, kPMaxG);
   return up256((size_t)T * H) + up256((size_t)T * (H / kQB) * sizeof(float)) + up256(S * I) +
-         up256(S * (I / kQB) * sizeof(float)) + 16 * (max_tiles(S, kPMaxG) + 1);
+         up256(tiles * (I / kQB) * kPM * sizeof(float)) + 16 * (tiles + 1);
 }
 
 hipError_t launch_fp8_expert_ffn(const moe_fp8_weights& W, const uint16_t* x, int T, int K,
@@ -732,12 +768,12 @@ hipError_t launch_fp8_expert_ffn(const moe_fp8_weights& W, const uint16_t* x, in
   if (T <= kDecodeMaxT)
     return launch_fp8_stream_experts(W, x, T, K, offsets, sorted_slot, groups, (float*)ws, y, s);
   const size_t S = (size_t)T * K + (W.has_shared ? T : 0);
+  const int G = W.E + W.has_shared;
   uint8_t* xq = (uint8_t*)ws;
   float* xs = (float*)(xq + up256((size_t)T * W.H));
   uint8_t* hq = (uint8_t*)xs + up256((size_t)T * (W.H / kQB) * sizeof(float));
   float* hs = (float*)(hq + up256(S * W.I));
-  int32_t* items = (int32_t*)((uint8_t*)hs + up256(S * (W.I / kQB) * sizeof(float)));
-  const int G = W.E + W.has_shared;
+  int32_t* items = (int32_t*)((uint8_t*)hs + up256(max_tiles(S, G) * (W.I / kQB) * kPM * sizeof(float)));
   const RowGrid g = row_grid(T, W.H / kQB * 16);
   MOE_LAUNCH("fp8_prep", s, k_fp8_prep, dim3(g.blocks + 1), dim3(256), 0, s, x, T, W.H, g.lg, g.cb,
              xq, xs, offsets, G, items);

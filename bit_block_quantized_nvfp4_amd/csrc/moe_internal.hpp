@@ -171,7 +171,7 @@ hipError_t launch_block_norm_grad(const void* dr, const void* dn, const void* r_
 constexpr int kFp8StreamMaxT = 16;
 void register_fp8_stream_kernels(std::vector<const void*>& k);
 void register_fp8_tile_kernels(std::vector<const void*>& k);
-hipError_t launch_fp8_quant(const void* x, int T, int K, int dtype, int ldq, uint8_t* codes,
+hipError_t launch_fp8_quant(const void* x, int T, int K, int dtype, uint8_t* codes,
                             float* scales, hipStream_t s);
 size_t fp8_linear_workspace_bytes(int T, int K);
 hipError_t launch_fp8_linear(const moe_fp8_matrix& M, const void* x, int T, int dtype, void* out,
