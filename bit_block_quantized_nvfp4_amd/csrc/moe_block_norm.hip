@@ -17,6 +17,9 @@
 // Bound by memory: each row of each tensor is read (non-temporal: 135 us, as
 // ordinary loads 144 us at T = 32768, H = 2048 with an element gate) and written
 // once, a row's values stay in registers between the statistics and their use.
+// H = 2048, bf16: T = 32768 with an element gate 122 us (671 MB, 5.5 TB/s; a 1
+// GB device copy runs at 5.1); backward T = 8191 with a token gate 44 us + 6 us
+// for the weight gradients (201 MB of rows and 17 MB of partials, 4.9 TB/s).
 #include <math.h>
 
 #include "moe_internal.hpp"

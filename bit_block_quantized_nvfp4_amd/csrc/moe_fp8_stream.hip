@@ -9,6 +9,11 @@
 // the same instructions as sixteen; the rows' own reads are masked off past
 // the last.  Each wave quantises the blocks it needs by itself (32 values a
 // lane): repeated per tile, but it saves a launch and its wait.
+// Measured: one row of 2048 x 2048 4.4 us, of which a launch is nearly all; 16
+// rows of 8192 x 8192 21 us (67 MB, 3.2 TB/s: each wave waits for one block's
+// operands at a time; two blocks under way took more registers and longer).
+// Experts, T = 8, about 64 of 512 groups (H = 2048, I = 512): gate_up 35 us (135
+// MB, 3.9 TB/s), down 22 us (69 MB, 3.2 TB/s).
 #include <math.h>
 
 #include "moe_ffn_common.hpp"

@@ -10,7 +10,11 @@
 //
 // All are bound by memory: every row of x, xs, y, dy is moved once.  Sums are
 // f32, in slot order (then the shared expert), with one rounding at the end;
-// no sum crosses blocks, so no result depends on timing.
+// no sum crosses blocks, so no result depends on timing.  H = 2048, K = 10 + 1
+// of 512, where a 1 GB device copy runs at 5.1 TB/s: dispatch of 4096 rows of
+// f16 33 us (201 MB, 6.1 TB/s), combine 37 us (5.4 TB/s); of 8192 rows of bf16
+// dispatch_grad 67 us (403 MB, 6.0 TB/s), combine_grad 147 us (772 MB, 5.3
+// TB/s), topk_grad 6.4 us (17 MB).
 #include <math.h>
 
 #include "moe_internal.hpp"
