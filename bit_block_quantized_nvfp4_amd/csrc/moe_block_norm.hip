@@ -18,8 +18,8 @@
 // ordinary loads 144 us at T = 32768, H = 2048 with an element gate) and written
 // once, a row's values stay in registers between the statistics and their use.
 // H = 2048, bf16: T = 32768 with an element gate 122 us (671 MB, 5.5 TB/s; a 1
-// GB device copy runs at 5.1); backward T = 8191 with a token gate 44 us + 6 us
-// for the weight gradients (201 MB of rows and 17 MB of partials, 4.9 TB/s).
+// GB device copy runs at 5.1); backward T = 8191 with a token gate 44 us + 4 us
+// for the weight gradients (201 MB of rows and 8 MB of partials, 4.8 TB/s).
 #include <math.h>
 
 #include "moe_internal.hpp"
@@ -33,7 +33,7 @@ template <int W>
 __device__ __forceinline__ float row_sum(float v, float* slot) {
   v = wave_sum_dpp(v);
   if (W == 1) return v;
-  if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
+  if ((threadIdx.x & 63) == 0) slot[(threadIdx.x >> 6) % W] = v;
   __syncthreads();
   float r = 0.f;
 #pragma unroll
@@ -175,18 +175,17 @@ struct NormBwd {
   int T, H, cpr, gate_kind;
 };
 
-// As the forward kernel, but each wave (or block) takes every P-th row and
-// keeps its share of the weight gradients in registers; at the end the block
-// writes one partial row of each.
-template <int DT, int NC, int W>
-__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_block_norm_grad(NormBwd a) {
+// A block has R rows in flight, W waves to a row.  Each such group takes every
+// P R-th row and keeps its share of the weight gradients in registers; at the
+// end the groups join theirs and the block writes one partial row of each.
+template <int DT, int NC, int W, int R>
+__global__ __launch_bounds__(64 * W * R) void k_block_norm_grad(NormBwd a) {
   constexpr int N = Chunk<DT>::N;
   constexpr int TPR = 64 * W;
-  constexpr int RPB = W == 1 ? 4 : 1;  // rows in flight per block
-  __shared__ float red[2][W];
-  __shared__ f32x4 join[W == 1 ? 3 * 64 * NC * (N / 4) : 1];
-  const int lane = W == 1 ? (threadIdx.x & 63) : threadIdx.x;
-  const int wv = W == 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) : 0;
+  __shared__ float red[2][R][W];
+  __shared__ f32x4 join[R > 1 ? (R - 1) * TPR * NC * (N / 4) : 1];
+  const int lane = (int)threadIdx.x % TPR;
+  const int grp = R == 1 ? 0 : __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPR);
   const float inv_h = 1.0f / (float)a.H;
   float gw_post[NC][N], gw_pre[NC][N];
 #pragma unroll
@@ -194,15 +193,20 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_block_norm_grad(NormB
 #pragma unroll
     for (int j = 0; j < N; ++j) gw_post[i][j] = gw_pre[i][j] = 0.f;
 
-  for (long t = (long)blockIdx.x * RPB + wv; t < a.T; t += (long)gridDim.x * RPB) {
+  // the block's groups stay together for the barriers: past the last row a
+  // group computes with zeros
+  for (long t0 = (long)blockIdx.x * R; t0 < a.T; t0 += (long)gridDim.x * R) {
+    const bool on = R == 1 || t0 + grp < a.T;
+    const long t = on ? t0 + grp : 0;
     const size_t base = (size_t)t * a.cpr;
+    const int cols = on ? a.cpr : 0;
     float D[NC][N];
     u32x4 vr[NC], vn[NC], vx[NC], vy[NC], vg[NC];
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = lane + TPR * i;
       vr[i] = vn[i] = vx[i] = vy[i] = vg[i] = u32x4{0u, 0u, 0u, 0u};
-      if (c < a.cpr) {
+      if (c < cols) {
         if (a.dr) vr[i] = __builtin_nontemporal_load(a.dr + base + c);
         if (a.w_pre) {
           vn[i] = __builtin_nontemporal_load(a.dn + base + c);
@@ -215,7 +219,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_block_norm_grad(NormB
 #pragma unroll
     for (int i = 0; i < NC; ++i) Chunk<DT>::unpack(vr[i], D[i]);
     if (a.w_pre) {
-      const float rstd = a.rstd_pre[t];
+      const float rstd = on ? a.rstd_pre[t] : 0.f;
       float g[NC][N], xh[NC][N], s = 0.f;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
@@ -223,7 +227,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_block_norm_grad(NormB
         float wp[N];
         Chunk<DT>::unpack(vn[i], g[i]);
         Chunk<DT>::unpack(vx[i], xh[i]);
-        if (c < a.cpr) {
+        if (c < cols) {
           load_w<N>(a.w_pre, c, wp);
 #pragma unroll
           for (int j = 0; j < N; ++j) {
@@ -234,7 +238,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_block_norm_grad(NormB
           }
         }
       }
-      const float m = row_sum<W>(s, red[0]) * inv_h;
+      const float m = row_sum<W>(s, red[0][grp]) * inv_h;
 #pragma unroll
       for (int i = 0; i < NC; ++i)
 #pragma unroll
@@ -245,7 +249,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_block_norm_grad(NormB
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = lane + TPR * i;
-      if (c < a.cpr) {
+      if (c < cols) {
         float o[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) o[j] = rs * D[i][j];
@@ -256,7 +260,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_block_norm_grad(NormB
       if (W > 1) __syncthreads();  // red[] is free again
       continue;
     }
-    const float rstd = a.w_post ? a.rstd_post[t] : 1.f;
+    const float rstd = !on ? 0.f : a.w_post ? a.rstd_post[t] : 1.f;
     float sg = 1.f;
     if (a.gate_kind == MOE_GATE_TOKEN) sg = sigmoid_f32(((const float*)a.gate)[t]);
     // D becomes b D, then du w_post = b c D w_post; s sums that times yh,
@@ -270,7 +274,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_block_norm_grad(NormB
       float wp[N], gt[N];
 #pragma unroll
       for (int j = 0; j < N; ++j) wp[j] = 1.f;
-      if (c < a.cpr) {
+      if (c < cols) {
         if (a.w_post) load_w<N>(a.w_post, c, wp);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
@@ -301,14 +305,14 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_block_norm_grad(NormB
     }
     float m = 0.f;
     if (a.w_post || a.gate_kind == MOE_GATE_TOKEN) {
-      s = row_sum<W>(s, red[1]);
-      if (a.gate_kind == MOE_GATE_TOKEN && lane == 0) ((float*)a.dgate)[t] = (1.f - sg) * s;
+      s = row_sum<W>(s, red[1][grp]);
+      if (a.gate_kind == MOE_GATE_TOKEN && lane == 0 && on) ((float*)a.dgate)[t] = (1.f - sg) * s;
       if (a.w_post) m = s * inv_h;
     }
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = lane + TPR * i;
-      if (c < a.cpr) {
+      if (c < cols) {
         float o[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) o[j] = rstd * (D[i][j] - yh[i][j] * m);
@@ -318,27 +322,27 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_block_norm_grad(NormB
     if (W > 1) __syncthreads();  // red[] is free again
   }
 
-  // the block's partial sums: the four waves of W == 1 join in wave order
+  // the block's partial sums: its groups join in order
   auto put = [&](float (&gw)[NC][N], int which) {
     constexpr int Q = N / 4;
-    if (W == 1) {
+    if (R > 1) {
       __syncthreads();
-      if (wv > 0) {
+      if (grp > 0) {
 #pragma unroll
         for (int i = 0; i < NC; ++i)
 #pragma unroll
           for (int q = 0; q < Q; ++q)
-            join[((wv - 1) * NC * Q + i * Q + q) * 64 + lane] =
+            join[((grp - 1) * NC * Q + i * Q + q) * TPR + lane] =
                 f32x4{gw[i][4 * q], gw[i][4 * q + 1], gw[i][4 * q + 2], gw[i][4 * q + 3]};
       }
       __syncthreads();
-      if (wv > 0) return;
-      for (int w2 = 0; w2 < 3; ++w2)
+      if (grp > 0) return;
+      for (int g = 0; g < R - 1; ++g)
 #pragma unroll
         for (int i = 0; i < NC; ++i)
 #pragma unroll
           for (int q = 0; q < Q; ++q) {
-            const f32x4 v = join[(w2 * NC * Q + i * Q + q) * 64 + lane];
+            const f32x4 v = join[(g * NC * Q + i * Q + q) * TPR + lane];
 #pragma unroll
             for (int j = 0; j < 4; ++j) gw[i][4 * q + j] += v[j];
           }
@@ -407,13 +411,20 @@ static void by_shape(int T, int cpr, F&& f) {
   else if constexpr (!GRAD) f(IntC<4>{}, IntC<1>{});
 }
 
+// Rows in flight of a backward block of W waves a row: two where the registers
+// allow (T = 8191, H = 2048: 47 us + 6 us for half the partial rows; one row and
+// twice the blocks 47 + 8 us, half the blocks 57 + 6 us; four rows 50 + 6 us;
+// by events).
+constexpr int grad_rows(int NC, int W) { return W == 1 ? 4 : NC == 1 ? 2 : 1; }
+
 void register_block_norm_kernels(std::vector<const void*>& k) {
   auto add = [&](auto D) {
     constexpr int DT = decltype(D)::value;
     auto one = [&](auto NC, auto W) {
       k.push_back((const void*)&k_block_norm<DT, decltype(NC)::value, decltype(W)::value>);
       if constexpr (decltype(NC)::value == 1 || decltype(W)::value > 1)
-        k.push_back((const void*)&k_block_norm_grad<DT, decltype(NC)::value, decltype(W)::value>);
+        k.push_back((const void*)&k_block_norm_grad<DT, decltype(NC)::value, decltype(W)::value,
+                                                    grad_rows(decltype(NC)::value, decltype(W)::value)>);
     };
     one(IntC<1>{}, IntC<1>{});
     one(IntC<4>{}, IntC<1>{});
@@ -451,9 +462,10 @@ hipError_t launch_block_norm(const void* res, const void* y, const void* gate, i
 // sizes alone, so results do not depend on the device's state.
 static int norm_parts(int T, int H, int dtype) {
   const int cpr = H * dtype_bytes(dtype) / 16;
-  const int rows = norm_waves(T, cpr, true) == 1 ? 4 : 1;
+  const int W = norm_waves(T, cpr, true), rows = grad_rows(cpr <= 64 * W ? 1 : 4, W);
   const int P = (T + rows - 1) / rows;
-  const int most = T / 8 < 256 ? 256 : T / 8 < 1024 ? T / 8 : 1024;
+  const int top = rows == 2 ? 512 : 1024;
+  const int most = T / 8 < 256 ? 256 : T / 8 < top ? T / 8 : top;
   return P < most ? P : most;
 }
 
@@ -478,8 +490,9 @@ hipError_t launch_block_norm_grad(const void* dr, const void* dn, const void* r_
     constexpr int DT = decltype(D)::value;
     by_shape<true>(T, cpr, [&](auto NC, auto W) {
       constexpr int w = decltype(W)::value;
-      MOE_LAUNCH("block_norm_grad", s, (k_block_norm_grad<DT, decltype(NC)::value, w>), dim3(P),
-                 dim3(w == 1 ? 256 : 64 * w), 0, s, a);
+      constexpr int r = grad_rows(decltype(NC)::value, w);
+      MOE_LAUNCH("block_norm_grad", s, (k_block_norm_grad<DT, decltype(NC)::value, w, r>), dim3(P),
+                 dim3(64 * w * r), 0, s, a);
     });
   });
   hipError_t e = hipGetLastError();
