@@ -164,7 +164,7 @@ struct TileArgs {
 };
 
 // Weight scales of a block's steps in LDS, times the scales of a step: K up to
-// 65536 for one tile, or ntb * K / 128 of a bank's (K up to 8192, ntb up to 8).
+// 65536 for one tile, or ntb runs of 64 (a bank's K is up to 8192, ntb up to 8).
 constexpr int kTileScales = 512;
 // Blocks that a grouped launch keeps at least when its blocks take several tiles.
 constexpr size_t kStreamBlocks = 2048;
@@ -352,24 +352,20 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
   const uint32_t ldsw = lds0 + wv * 1024;
   const uint32_t ldsn = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) float*)nowhere;
 
-  // The weight scales of all steps, one per 128 weight rows of a tile, in LDS: a
-  // load of one in the loop would wait for the DMA under way.  gate_up: the
-  // gate's, then the up's.
-  for (int i = threadIdx.x; i < ntb * NS * nb; i += NT * KG) {
-    const int tile = i / (NS * nb), h = i / nb % NS, b = i % nb;
+  // The weight scales of all steps, one per 128 weight rows of a tile (gate_up:
+  // the gate's, then the up's), first to LDS: a load of one in the loop would
+  // wait for the DMA under way, and loads through registers here for memory
+  // before it begins.
+  const int nbp = (nb + 63) & ~63;             // a run of them, zeros behind
+  const uint32_t ldsc = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) float*)wsc;
+  for (int i = kg * NW + wv; i < ntb * NS * (nbp / 64); i += NW * KG) {
+    const int run = i / (nbp / 64), part = i % (nbp / 64);
+    const int tile = run / NS, h = run % NS;
     const int row = n0 + tile * BC + (MODE == kTileGateUp ? h * a.N : h * kQB);
-    wsc[i] = scales[(size_t)((MODE == kTileGateUp ? row : min(row, a.N - 1)) / kQB) * nb + b];
-  }
-  // rows of this lane's stores that belong to a slot, a bit each
-  uint32_t mine_ok = ~0u;
-  if (MODE == kTileDown) {
-    mine_ok = 0;
-#pragma unroll
-    for (int i = 0; i < TM * CR / 64; ++i) {
-      const int row = wm * TM + i * (64 / CR) + lane / CR;
-      if (row < rows && slot_token(a.sorted_slot[m0 + row], a.T, a.topk, a.has_shared) >= 0)
-        mine_ok |= 1u << i;
-    }
+    const int band = (MODE == kTileGateUp ? row : min(row, a.N - 1)) / kQB;
+    u32x4 run_buf = buf_of(scales + (size_t)band * nb, (uint32_t)nb * 4u);
+    asm volatile("s_nop 4" : "+s"(run_buf));   // as in dma_offset
+    dma_b32(run_buf, lane * 4, dma_offset(part * 256), ldsc + i * 256);
   }
 
   // The next step to bring: how many are left, its block along K and buffer.
@@ -416,6 +412,18 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
     dma_weights(std::false_type{});
   }
 
+  // rows of this lane's stores that belong to a slot, a bit each
+  uint32_t mine_ok = ~0u;
+  if (MODE == kTileDown) {
+    mine_ok = 0;
+#pragma unroll
+    for (int i = 0; i < TM * CR / 64; ++i) {
+      const int row = wm * TM + i * (64 / CR) + lane / CR;
+      if (row < rows && slot_token(a.sorted_slot[m0 + row], a.T, a.topk, a.has_shared) >= 0)
+        mine_ok |= 1u << i;
+    }
+  }
+
   f32x4 acc[FN][FM];
   // columns of 16 tokens of this wave with rows in them
   const int live = min(FM, max(0, (rows - wm * TM + 15) / 16));
@@ -440,7 +448,7 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
       if (j < LV) tn[j] = frag(lds + at + kTok + wm * TM * kQB, 16 * j);
   };
   // Step at buffer `at`, whose weight scales are sc[0] and (gate_up: the up
-  // rows') sc[nb].  Two barriers: behind the first product row every wave holds
+  // rows') sc[nbp].  Two barriers: behind the first product row every wave holds
   // all its token fragments, so the next tokens may go to their buffer; before
   // the last two rows every wave has read the last of the weights, and the step
   // after has landed (what was asked for later may be under way), so its first
@@ -455,7 +463,7 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
     Frag<EX> tf[FM];
     float s0[FM], s1[FM];
     // a group's step past the end adds zeros
-    const float w0 = KG == 1 || some ? sc[0] : 0.f, w1 = MODE == kTileGateUp ? sc[nb] : 0.f;
+    const float w0 = KG == 1 || some ? sc[0] : 0.f, w1 = MODE == kTileGateUp ? sc[nbp] : 0.f;
 #pragma unroll
     for (int j = 0; j < LV; ++j) {
       tf[j].set(j < PRE ? tn[j < PRE ? j : 0] : frag(pt, 16 * j));
@@ -588,7 +596,7 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
     auto on = [&]() __attribute__((always_inline)) { at = at == (NBUF - 1) * kBuf ? 0 : at + kBuf; };
     first(0, count);
     for (int tile = 0; tile < ntb; ++tile) {
-      const float* sc = wsc + tile * NS * nb + hs * nb;
+      const float* sc = wsc + (tile * NS + hs) * nbp;
 #pragma unroll
       for (int i = 0; i < FN; ++i)
 #pragma unroll
