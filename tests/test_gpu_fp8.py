@@ -102,6 +102,14 @@ def test_linear_large(moe, T, N, K):
     within(out.cpu()[rows][:, cols], ref, rounded(ref, torch.bfloat16, err), "linear large")
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,N,K", [(3, 24, 65536), (18, 24, 8336), (20, 24, 65536), (257, 8, 8208)])
+def test_linear_long_rows(moe, T, N, K, dtype):
+    """More than 64 blocks along K: several runs of weight scales, and the largest K."""
+    flush(f"linear long T={T} N={N} K={K} {dtype}")
+    _check_linear(moe, torch.Generator().manual_seed(T + K), T, N, K, dtype)
+
+
 @pytest.mark.parametrize("T", [5, 40])
 def test_gradient_by_the_input_is_the_transposed_matrix(moe, T):
     """Against the formula and against differences of the exact bilinear product."""
