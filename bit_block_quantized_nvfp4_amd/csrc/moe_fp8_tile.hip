@@ -236,14 +236,15 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
   constexpr int DW = BN * 8 / NT, DX = BM * 8 / NT;  // 16-byte chunks per thread and step
   constexpr int D = DW + DX + 1;               // memory operations per wave and step
   constexpr int kTok = BN * kQB, kScale = kTok + BM * kQB;  // LDS offsets in a buffer
-  constexpr int kBuf = kScale + BM * 4;
+  constexpr int BS = (BM + 63) / 64;           // waves that bring a step's token scales
+  constexpr int kBuf = kScale + BS * 256;
   constexpr bool EX = DT == MOE_DT_F32;
   constexpr int ES = DT == MOE_DT_F32 ? 4 : 2;
   constexpr int CR = TN * ES / 16;             // 16-byte chunks of a row of the wave's output
   constexpr int NS = (BN + kQB - 1) / kQB;     // weight scales of a step
   constexpr int BC = MODE == kTileGateUp ? BN / 2 : BN;  // columns of a tile
   static_assert(BN * 8 % NT == 0 && BM * 8 % NT == 0 && TN % 16 == 0 && TM % 16 == 0 &&
-                    BM % 64 == 0 && BM / 64 <= NW && NBUF * D < 64 && FN >= 2 && 64 % CR == 0,
+                    BM % 32 == 0 && BS <= NW && NBUF * D < 64 && FN >= 2 && 64 % CR == 0,
                 "tile shape");
   static_assert(MODE == kTileLinear || BM == kPM, "row tiles of the items");
   static_assert(MODE != kTileGateUp || BC == kQB, "a tile holds one scale of h");
@@ -344,9 +345,9 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
     woff[i] = (uint32_t)wrow_of((i * NT + tid) >> 3) * (uint32_t)a.K + chunk;
 #pragma unroll
   for (int i = 0; i < DX; ++i) xoff[i] = (uint32_t)xrow_of((i * NT + tid) >> 3) * ldx + chunk;
-  // the first BM / 64 waves bring 64 token scales each, the others none
-  const bool brings = wv < BM / 64;
-  const int srow = 64 * (wv % (BM / 64)) + lane;
+  // the first waves bring 64 token scales each, the others none
+  const bool brings = wv < BS;
+  const int srow = 64 * (wv % BS) + lane;
   const uint32_t soff = MODE == kTileGateUp ? (uint32_t)xrow_of(srow) * (uint32_t)nb * 4u : srow * 4u;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
   const uint32_t ldsw = lds0 + wv * 1024;
@@ -658,37 +659,53 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
 
 // The linear mode's tiles, largest first: f with the kernel, BN, BM and threads.
 // Rows of f32 take twice the operand registers, hence fewer shapes.
+constexpr int kTileShapes = 6;
 template <int DT, typename F>
 static void by_linear_tile(int shape, F&& f) {
   if constexpr (DT != MOE_DT_F32) {
     if (shape == 0) f(&k_fp8_tile<kTileLinear, DT, 256, 256, 2, 4, 2>, 256, 256, 512);
-    else if (shape == 1) f(&k_fp8_tile<kTileLinear, DT, 128, 128, 2, 2, 2, 2>, 128, 128, 512);
-    else if (shape == 2) f(&k_fp8_tile<kTileLinear, DT, 128, 64, 2, 2, 3, 2>, 128, 64, 512);
-    else f(&k_fp8_tile<kTileLinear, DT, 64, 64, 2, 2, 4, 2>, 64, 64, 512);
+    if (shape == 1) f(&k_fp8_tile<kTileLinear, DT, 128, 128, 2, 2, 2, 2>, 128, 128, 512);
+    if (shape == 2) f(&k_fp8_tile<kTileLinear, DT, 128, 64, 2, 2, 3, 2>, 128, 64, 512);
   } else {
-    if (shape <= 1) f(&k_fp8_tile<kTileLinear, DT, 128, 128, 2, 2, 2>, 128, 128, 256);
-    else f(&k_fp8_tile<kTileLinear, DT, 64, 64, 2, 2, 4, 2>, 64, 64, 512);
+    if (shape == 1) f(&k_fp8_tile<kTileLinear, DT, 128, 128, 2, 2, 2>, 128, 128, 256);
   }
+  if (shape == 3) f(&k_fp8_tile<kTileLinear, DT, 64, 64, 2, 2, 4, 2>, 64, 64, 512);
+  if (shape == 4) f(&k_fp8_tile<kTileLinear, DT, 32, 64, 1, 2, 3, 4>, 32, 64, 512);
+  if (shape == 5) f(&k_fp8_tile<kTileLinear, DT, 32, 32, 1, 1, 4, 4>, 32, 32, 256);
 }
 
-// The largest tile whose grid still fills most of the 256 compute units.  Tile
-// kernel's time (bf16, us with about 3.5 us of event overhead) with the tile
-// taken and its neighbours:
-//   rows x N x K           256x256  128x128  128x64  64x64
-//   8192 x 4096 x 4096         140*     200     284    376
-//   2048 x 8192 x 4096          68*      94     124    174
-//   2048 x 4096 x 4096          59       52*     64     91
-//   1024 x 4096 x 4096          53       27*     34     46
-//   512 x 4096 x 4096           52       23      18*    24
-//   333 x 8192 x 8192           95       40*     53     59
-//   333 x 4168 x 2064           32       16      13*    18
-//   64 x 8192 x 8192            93       37      27     21*
-//   64 x 2048 x 2048            29       15      11     10*
+// The shape whose rounds of 256 blocks (a block's LDS leaves a compute unit no
+// second one) take the least time together; a round's relative time hardly
+// depends on how full it is.  Tile kernel with each shape (us, with about 3.5 us
+// of event overhead; * the one taken):
+//   rows x N x K, bf16    256x256  128x128  128x64  64x64  32x64  32x32
+//   8192 x 4096 x 4096       140*     200     284    376
+//   2600 x 4096 x 4096        60*      71             125    160    243
+//   2048 x 4096 x 4096        59       52*     64      91
+//   640 x 4096 x 4096                  25*             37     42     64
+//   512 x 4096 x 4096         52       24      18*     25     34     50
+//   333 x 4168 x 2064         32       16      13*     18     26     31
+//   512 x 2048 x 2048                  14      12      10*    13     20
+//   128 x 4096 x 4096                  23      18      14     11*    16
+//   64 x 4096 x 4096                   22      17      15     12     11*
+//   32 x 8192 x 8192                   38      29      24     18     16*
+//   f32 rows
+//   2048 x 4096 x 4096                 71*            109    136    208
+//   512 x 4096 x 4096                  42              32*    38     56
+//   128 x 4096 x 4096                  39              17     12*    17
+//   32 x 4096 x 4096                   38              16     12     10*
+template <int DT>
 static int linear_tile(int T, int N) {
-  auto tiles = [&](int bn, int bm) { return (long)((N + bn - 1) / bn) * ((T + bm - 1) / bm); };
-  if (tiles(256, 256) >= 192) return 0;
-  if (tiles(128, 128) >= 192) return 1;
-  return tiles(128, 64) >= 160 ? 2 : 3;
+  int best = 0;
+  long least = 0;
+  for (int s = 0; s < kTileShapes; ++s)
+    by_linear_tile<DT>(s, [&](auto, int bn, int bm, int) {
+      constexpr int cost[2][kTileShapes] = {{64, 25, 18, 14, 11, 10}, {0, 38, 0, 16, 12, 10}};
+      const long tiles = (long)((N + bn - 1) / bn) * ((T + bm - 1) / bm);
+      const long t = (tiles + 255) / 256 * cost[DT == MOE_DT_F32][s];
+      if (least == 0 || t < least) least = t, best = s;
+    });
+  return best;
 }
 
 void register_fp8_tile_kernels(std::vector<const void*>& k) {
@@ -696,7 +713,7 @@ void register_fp8_tile_kernels(std::vector<const void*>& k) {
     constexpr int DT = decltype(D)::value;
     k.push_back((const void*)&k_fp8_quant<DT, false>);
     k.push_back((const void*)&k_fp8_quant<DT, true>);
-    for (int s = 0; s < 4; ++s)
+    for (int s = 0; s < kTileShapes; ++s)
       by_linear_tile<DT>(s, [&](auto kernel, int, int, int) { k.push_back((const void*)kernel); });
   };
   for (int dt = MOE_DT_BF16; dt <= MOE_DT_F32; ++dt) by_dtype(dt, add);
@@ -748,7 +765,7 @@ hipError_t launch_fp8_linear(const moe_fp8_matrix& M, const void* x, int T, int 
   a.N = M.N;
   a.K = M.K;
   by_dtype(dtype, [&](auto D) {
-    by_linear_tile<decltype(D)::value>(linear_tile(T, M.N), [&](auto kernel, int bn, int bm, int threads) {
+    by_linear_tile<decltype(D)::value>(linear_tile<decltype(D)::value>(T, M.N), [&](auto kernel, int bn, int bm, int threads) {
       a.nt = (M.N + bn - 1) / bn;
       MOE_LAUNCH("fp8_tile", s, kernel, dim3((unsigned)a.nt * (unsigned)((T + bm - 1) / bm)),
                  dim3(threads), 0, s, a);
