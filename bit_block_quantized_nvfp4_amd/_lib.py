@@ -120,7 +120,7 @@ _SIGS = {
     "moe_block_norm_grad": (_I, [_P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _F, _F, _I, _I, _I, _P,
                                  _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_fp8_quant": (_I, [_P, _I, _I, _I, _P, _P, _P]),
-    "moe_fp8_linear_workspace_bytes": (_SZ, [_I, _I]),
+    "moe_fp8_linear_workspace_bytes": (_SZ, [_I, _I, _I]),
     "moe_fp8_linear": (_I, [ctypes.POINTER(MoeFp8Matrix), _P, _I, _I, _P, _P, _SZ, _P]),
     "moe_fp8_expert_ffn_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
     "moe_fp8_expert_ffn": (_I, [ctypes.POINTER(MoeFp8Weights), _P, _I, _I, _P, _P, _P, _P, _P,

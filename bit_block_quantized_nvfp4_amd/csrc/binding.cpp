@@ -463,7 +463,7 @@ PyObject* fp8_linear(Args a) {
   const int T = size32(x.size(0), "T");
   need(x, x.scalar_type(), {T, K}, dev, "x");
   Tensor out = output(given, x.scalar_type(), {T, N}, dev, "out");
-  const size_t bytes = moe_fp8_linear_workspace_bytes(T, K);
+  const size_t bytes = moe_fp8_linear_workspace_bytes(T, N, K);
   Tensor ws;
   if (bytes) ws = scratch(ws_given, bytes, dev);
   check(moe_fp8_linear(&M, x.data_ptr(), T, dt, out.data_ptr(), bytes ? ws.data_ptr() : nullptr,

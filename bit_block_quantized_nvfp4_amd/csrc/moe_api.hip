@@ -583,8 +583,12 @@ int moe_fp8_quant(const void* x, int T, int K, int dtype, uint8_t* codes, float*
                   "moe_fp8_quant launch");
 }
 
-size_t moe_fp8_linear_workspace_bytes(int T, int K) {
-  return fp8_k_ok(T, K) ? moe::fp8_linear_workspace_bytes(T, K) : 0;
+static bool fp8_matrix_ok(int T, int N, int K) {
+  return fp8_k_ok(T, K) && N >= 8 && N <= 65536 && N % 8 == 0;
+}
+
+size_t moe_fp8_linear_workspace_bytes(int T, int N, int K) {
+  return fp8_matrix_ok(T, N, K) ? moe::fp8_linear_workspace_bytes(T, N, K) : 0;
 }
 
 int moe_fp8_linear(const moe_fp8_matrix* M, const void* x, int T, int dtype, void* out, void* ws,
@@ -592,11 +596,11 @@ int moe_fp8_linear(const moe_fp8_matrix* M, const void* x, int T, int dtype, voi
   if (!M || !x || !out) return fail(MOE_EINVAL, "moe_fp8_linear: null pointer");
   if (!M->codes || !M->scales) return fail(MOE_EINVAL, "moe_fp8_linear: null weight pointer");
   if (!dtype_ok(dtype)) return fail(MOE_EUNSUPPORTED, "moe_fp8_linear: unknown dtype %d", dtype);
-  if (!fp8_k_ok(T, M->K) || M->N < 8 || M->N > 65536 || M->N % 8 != 0)
+  if (!fp8_matrix_ok(T, M->N, M->K))
     return fail(MOE_EINVAL, "moe_fp8_linear: need 1 <= T <= 2^30, K a multiple of 16 in [16, 65536] and N a multiple of 8 in [8, 65536] (T=%d N=%d K=%d)", T, M->N, M->K);
   if (!aligned16((const char*)x, (const char*)out, M->codes, (const char*)ws))
     return fail(MOE_EINVAL, "moe_fp8_linear: codes, rows and workspace must be aligned to 16 bytes");
-  const size_t need = moe::fp8_linear_workspace_bytes(T, M->K);
+  const size_t need = moe::fp8_linear_workspace_bytes(T, M->N, M->K);
   if (need > 0 && (!ws || ws_bytes < need))
     return fail(MOE_EWORKSPACE, "moe_fp8_linear: workspace of %zu bytes needed, %zu given", need, ws_bytes);
   int rc = ensure_init();

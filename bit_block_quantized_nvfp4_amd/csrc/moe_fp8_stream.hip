@@ -9,9 +9,10 @@
 // the same instructions as sixteen; the rows' own reads are masked off past
 // the last.  Each wave quantises the blocks it needs by itself (32 values a
 // lane): repeated per tile, but it saves a launch and its wait.
-// Measured: one row of 2048 x 2048 4.4 us, of which a launch is nearly all; 16
-// rows of 8192 x 8192 21 us (67 MB, 3.2 TB/s: each wave waits for one block's
-// operands at a time; two blocks under way took more registers and longer).
+// Measured: one row of 2048 x 2048 4.4 us, of which a launch is most; 4096 x 4096
+// 7.8 us (16.8 MB), 65536 x 512 10.1 us (34 MB, 3.4 TB/s), 4096 x 16384 20.5 us
+// (67 MB, 3.3 TB/s).  Two blocks of 128 under way in a wave took more registers,
+// hence fewer waves, and longer.
 // Experts, T = 8, about 64 of 512 groups (H = 2048, I = 512): gate_up 35 us (135
 // MB, 3.9 TB/s), down 22 us (69 MB, 3.2 TB/s).
 #include <math.h>
@@ -197,15 +198,37 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_stream(StreamArgs a) {
   }
 }
 
-template <int DT>
-static void reg(std::vector<const void*>& k) {
-  k.push_back((const void*)&k_fp8_stream<DT, kStreamLinear, 1, 8, 8>);
-  k.push_back((const void*)&k_fp8_stream<DT, kStreamLinear, 2, 8, 8>);
+// The linear mode's shapes: f with RT and KW (= NW).  A wave with one or two
+// blocks along K waits the fewest times; where that leaves more waves than the
+// chip holds, it takes two row tiles, which share its rows' quantisation, and
+// more of K (in a row in a graph, us, RT x KW):
+//   rows x N x K        1x16   1x8   2x8   1x4   2x4
+//   1 x 4096 x 4096      7.8   8.4  11.2  12.2  14.5
+//   16 x 512 x 8192     13.7  15.4  19.0  18.3  24.8
+//   1 x 2048 x 2048      4.4   4.7   5.9   6.1   7.3
+//   1 x 4096 x 1024      4.0   3.8   4.2   4.3   4.9
+//   1 x 16384 x 1024    10.6   7.7   6.4   6.9   7.3
+//   1 x 32768 x 512     15.6  10.1   7.7   7.4   6.3
+//   1 x 2048 x 512       3.1   2.9   3.2   2.8   3.2
+template <typename F>
+static void by_linear_shape(int N, int K, F&& f) {
+  const bool wide = N >= 8192;
+  if (K >= 2048 && N <= 4096) f(IntC<1>{}, IntC<16>{});
+  else if (K >= 1024) wide ? f(IntC<2>{}, IntC<8>{}) : f(IntC<1>{}, IntC<8>{});
+  else wide ? f(IntC<2>{}, IntC<4>{}) : f(IntC<1>{}, IntC<4>{});
 }
+
 void register_fp8_stream_kernels(std::vector<const void*>& k) {
-  reg<MOE_DT_BF16>(k);
-  reg<MOE_DT_F16>(k);
-  reg<MOE_DT_F32>(k);
+  for (int dt = MOE_DT_BF16; dt <= MOE_DT_F32; ++dt)
+    by_dtype(dt, [&](auto D) {
+      for (int N : {4096, 8192})
+        for (int K : {512, 1024, 2048})
+          by_linear_shape(N, K, [&](auto RT, auto KW) {
+            constexpr int kw = decltype(KW)::value;
+            k.push_back((const void*)&k_fp8_stream<decltype(D)::value, kStreamLinear,
+                                                   decltype(RT)::value, kw, kw>);
+          });
+    });
   k.push_back((const void*)&k_fp8_stream<MOE_DT_BF16, kStreamGateUp, 2, 8, 8>);
   k.push_back((const void*)&k_fp8_stream<MOE_DT_BF16, kStreamGateUp, 2, 4, 4>);
   k.push_back((const void*)&k_fp8_stream<MOE_DT_F32, kStreamDown, 2, 2, 2>);
@@ -221,20 +244,13 @@ hipError_t launch_fp8_stream_linear(const moe_fp8_matrix& M, const void* x, int 
   a.R = T;
   a.N = M.N;
   a.K = M.K;
-  // Two row tiles to a wave share the quantisation of its rows, which pays where
-  // the rows' bytes count and blocks are plenty (8192 x 8192, by events: 16 rows
-  // 26 us, one tile 30 us; 1 row 24 us, one tile 19 us; 8 rows of 4096 x 4096
-  // 12.5 us, one tile 10.4 us).
-  const int RT = M.N >= 8192 && T > 8 ? 2 : 1;
-  a.tiles = (M.N + 16 * RT - 1) / (16 * RT);
   by_dtype(dtype, [&](auto D) {
-    constexpr int DT = decltype(D)::value;
-    if (RT == 1)
-      MOE_LAUNCH("fp8_stream", s, (k_fp8_stream<DT, kStreamLinear, 1, 8, 8>), dim3(a.tiles),
-                 dim3(512), 0, s, a);
-    else
-      MOE_LAUNCH("fp8_stream", s, (k_fp8_stream<DT, kStreamLinear, 2, 8, 8>), dim3(a.tiles),
-                 dim3(512), 0, s, a);
+    by_linear_shape(M.N, M.K, [&](auto RT, auto KW) {
+      constexpr int DT = decltype(D)::value, rt = decltype(RT)::value, kw = decltype(KW)::value;
+      a.tiles = (M.N + 16 * rt - 1) / (16 * rt);
+      MOE_LAUNCH("fp8_stream", s, (k_fp8_stream<DT, kStreamLinear, rt, kw, kw>), dim3(a.tiles),
+                 dim3(64 * kw), 0, s, a);
+    });
   });
   return hipGetLastError();
 }

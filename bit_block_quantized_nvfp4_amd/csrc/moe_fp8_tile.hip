@@ -741,15 +741,28 @@ hipError_t launch_fp8_quant(const void* x, int T, int K, int dtype, uint8_t* cod
 static size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 static int blocks_of(int K) { return (K + kQB - 1) / kQB; }
 
-size_t fp8_linear_workspace_bytes(int T, int K) {
-  if (T <= kFp8StreamMaxT) return 0;
+// Few rows stream the weights in one launch; but where both N and K are large,
+// or the rows themselves are, the tiles' longer runs of loads are worth the launch
+// of their quantisation (both in a row in a graph, us, streamed against tiles: 1
+// row of 4096 x 4096 7.8 against 9.9, 16 rows 9.1 against 10.4; 1 row of 4096 x
+// 8192 12.3 against 13.9, of 65536 x 512 10.1 against 14.5; 1 row of 8192 x 4096
+// 12.7 against 12.3, 16 rows of 6144 x 4096 14.9 against 11.3, 1 row of 8192 x
+// 8192 21.9 against 17.3; 16 rows of 2048 x 8192 14.5 against 13.5, 8 rows 11.8
+// against 13.2).
+static bool fp8_linear_streams(int T, int N, int K) {
+  if (T > 16 || (T > 8 && K >= 8192)) return false;
+  return N <= 4096 || K < 2048 || (long)N * K < 3L << 23;
+}
+
+size_t fp8_linear_workspace_bytes(int T, int N, int K) {
+  if (fp8_linear_streams(T, N, K)) return 0;
   return up256((size_t)T * blocks_of(K) * kQB) +
          ((size_t)T + kScaleRows - 1) / kScaleRows * kScaleRows * blocks_of(K) * sizeof(float);
 }
 
 hipError_t launch_fp8_linear(const moe_fp8_matrix& M, const void* x, int T, int dtype, void* out,
                              void* ws, hipStream_t s) {
-  if (T <= kFp8StreamMaxT) return launch_fp8_stream_linear(M, x, T, dtype, out, s);
+  if (fp8_linear_streams(T, M.N, M.K)) return launch_fp8_stream_linear(M, x, T, dtype, out, s);
   const int nb = blocks_of(M.K);
   uint8_t* xq = (uint8_t*)ws;
   float* xs = (float*)(xq + up256((size_t)T * nb * kQB));

@@ -166,14 +166,13 @@ hipError_t launch_block_norm_grad(const void* dr, const void* dn, const void* r_
                                   float* dw_post, float* dw_pre, void* ws, hipStream_t s);
 
 // e4m3 products with a scale per block of 128: moe_fp8_stream.hip, rows of one
-// MFMA operand at most (dense: up to kFp8StreamMaxT; experts: the decode
-// batches); moe_fp8_tile.hip, more.
-constexpr int kFp8StreamMaxT = 16;
+// MFMA operand at most (dense: fp8_linear_streams; experts: the decode batches);
+// moe_fp8_tile.hip, the others.
 void register_fp8_stream_kernels(std::vector<const void*>& k);
 void register_fp8_tile_kernels(std::vector<const void*>& k);
 hipError_t launch_fp8_quant(const void* x, int T, int K, int dtype, uint8_t* codes,
                             float* scales, hipStream_t s);
-size_t fp8_linear_workspace_bytes(int T, int K);
+size_t fp8_linear_workspace_bytes(int T, int N, int K);
 hipError_t launch_fp8_linear(const moe_fp8_matrix& M, const void* x, int T, int dtype, void* out,
                              void* ws, hipStream_t s);
 hipError_t launch_fp8_stream_linear(const moe_fp8_matrix& M, const void* x, int T, int dtype,

@@ -482,13 +482,13 @@ int moe_block_norm_grad(const void* dr, const void* dn, const void* r_out, const
  *
  * moe_fp8_linear: out[t][n] = sum_b s[t][b] scales[n/128][b] sum_{k in b}
  * code_x[t][k] codes[n][k], f32 sums, one rounding to dtype.  Up to 16 rows
- * run as one launch that streams the weights once; more run as the
- * quantisation and a tiled product.  The gradient by x is the same call with
+ * run as one launch that streams the weights once, unless N and K are both
+ * large; else it is the quantisation and a tiled product.  The gradient by x is the same call with
  * the transposed matrix (codes^T, scales^T: blocks of 128 x 128 stay blocks,
  * so it is exact and is laid out once) on the gradient of out.
  *
  *   x [T][K], out [T][N] of dtype
- *   ws  at least moe_fp8_linear_workspace_bytes(T, K) bytes (0: none needed)
+ *   ws  at least moe_fp8_linear_workspace_bytes(T, N, K) bytes (0: none needed)
  *
  * A NaN or an infinity in a row makes that row's outputs NaN and no others.
  * The outputs may not overlap the inputs.
@@ -504,7 +504,7 @@ typedef struct moe_fp8_matrix {
 
 int moe_fp8_quant(const void* x, int T, int K, int dtype, uint8_t* codes, float* scales,
                   void* stream);
-size_t moe_fp8_linear_workspace_bytes(int T, int K);
+size_t moe_fp8_linear_workspace_bytes(int T, int N, int K);
 int moe_fp8_linear(const moe_fp8_matrix* M, const void* x, int T, int dtype, void* out, void* ws,
                    size_t ws_bytes, void* stream);
 

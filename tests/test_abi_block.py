@@ -125,8 +125,9 @@ def test_fp8_refusals(L, lib):
     _is(L, lib, q(P, 4, 128, 5, P, P, None), L.MOE_EUNSUPPORTED, b"dtype")
     _is(L, lib, q(ODD, 4, 128, BF, P, P, None), E, b"aligned")
     wsb = lib.moe_fp8_linear_workspace_bytes
-    assert wsb(16, 128) == 0 and wsb(17, 100) == 0 and wsb(17, 144) >= 17 * 256 + 17 * 2 * 4
-    need = wsb(17, 256)
+    assert wsb(16, 16, 128) == 0 and wsb(17, 16, 100) == 0 and wsb(17, 12, 144) == 0
+    assert wsb(17, 16, 144) >= 17 * 256 + 17 * 2 * 4
+    need = wsb(17, 16, 256)
 
     def f(codes=64, scales=64, N=16, K=256, x=P, T=17, dt=BF, o=P, ws=P, nb=need, M=True):
         m = L.MoeFp8Matrix(codes, scales, N, K)

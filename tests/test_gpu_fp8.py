@@ -102,18 +102,20 @@ def test_linear_large(moe, T, N, K):
     within(out.cpu()[rows][:, cols], ref, rounded(ref, torch.bfloat16, err), "linear large")
 
 
-# a grid of each tile shape, blocks along K that do not divide among the waves
+# a grid of each tile shape, blocks along K that do not divide among the waves,
+# and the few rows that run in wide streams or in tiles
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("T,N,K", [(64, 2056, 1168), (130, 2056, 1040), (600, 1032, 400), (330, 4104, 1040),
-                                   (500, 4104, 272), (1000, 8200, 144)])
+                                   (500, 4104, 272), (1000, 8200, 144), (3, 4104, 2064), (5, 8200, 1040),
+                                   (9, 24, 8208), (2, 6152, 4096)])
 def test_linear_every_tile(moe, T, N, K, dtype):
     flush(f"linear tiles T={T} N={N} K={K} {dtype}")
     gen = torch.Generator().manual_seed(T + N)
     codes, scales = _matrix(gen, N, K)
     x = normal(gen, (T, K), dtype)
     out = moe.moe_fp8_linear(moe.FP8Matrix(gpu(codes), gpu(scales)), gpu(x))
-    rows = np.unique(np.r_[0:T:37, 31:33, 63:min(65, T), T - 1])
-    cols = np.unique(np.r_[0:N:61, 31:33, 127:130, N - 9:N])
+    rows = np.unique(np.minimum(np.r_[0:T:37, 31:33, 63:65, T - 1], T - 1))
+    cols = np.unique(np.minimum(np.r_[0:N:61, 31:33, 127:130, N - 9:N], N - 1))
     ref, mag = fp8block.linear(x.float().numpy()[rows], _w64(codes, scales)[cols])
     err = (128 + -(-K // 128) + 4) * U32 * mag
     if dtype != torch.float32:
