@@ -232,6 +232,8 @@ void register_fp8_stream_kernels(std::vector<const void*>& k) {
   k.push_back((const void*)&k_fp8_stream<MOE_DT_BF16, kStreamGateUp, 2, 8, 8>);
   k.push_back((const void*)&k_fp8_stream<MOE_DT_BF16, kStreamGateUp, 2, 4, 4>);
   k.push_back((const void*)&k_fp8_stream<MOE_DT_F32, kStreamDown, 2, 2, 2>);
+  k.push_back((const void*)&k_fp8_stream<MOE_DT_F32, kStreamDown, 4, 2, 2>);
+  k.push_back((const void*)&k_fp8_stream<MOE_DT_F32, kStreamDown, 4, 1, 1>);
 }
 
 hipError_t launch_fp8_stream_linear(const moe_fp8_matrix& M, const void* x, int T, int dtype,
@@ -275,10 +277,18 @@ hipError_t launch_fp8_stream_experts(const moe_fp8_weights& W, const uint16_t* x
   a.topk = K;
   a.has_shared = W.has_shared;
   a.tiles = W.I / 16;
-  // Blocks of 4 waves where there are enough of them (T = 8, up to 81 groups:
-  // 36 us, of 8 waves 40 us), of 8 for fewer, each wave a shorter stretch of K
-  // (T = 1, 11 groups: 12.4 us, of 4 waves 13.6 us; by events).
-  if (G > 64)
+  // Blocks of 4 waves where there are enough of them, of 8 for fewer, each wave a
+  // shorter stretch of K.  Down: four row tiles to a wave share its rows'
+  // quantisation once there are groups enough, and one wave does all of a short
+  // K.  The call in a row in a graph, H = 2048, I = 512, top 10 of 512 and a
+  // shared one, us (gate_up waves, down row tiles x waves; * the one taken):
+  //   T (groups)   8, 2x2  4, 2x2  8, 4x2  4, 4x2  4, 4x1
+  //   1 (11)        16.9*   18.8    18.0    19.9    21.0
+  //   2 (21)        25.5    24.8    26.0    24.1*   25.1
+  //   4 (41)        39.9    38.7    37.4    36.5*   37.3
+  //   6 (61)        51.1                    45.2    44.9*
+  //   8 (81)        60.0    56.2            54.2    52.8*
+  if (G > 16)
     MOE_LAUNCH("fp8_stream_gate_up", s, (k_fp8_stream<MOE_DT_BF16, kStreamGateUp, 2, 4, 4>),
                dim3((unsigned)G * a.tiles), dim3(256), 0, s, a);
   else
@@ -292,9 +302,15 @@ hipError_t launch_fp8_stream_experts(const moe_fp8_weights& W, const uint16_t* x
   a.out = y;
   a.N = W.H;
   a.K = W.I;
-  a.tiles = W.H / 32;
-  MOE_LAUNCH("fp8_stream_down", s, (k_fp8_stream<MOE_DT_F32, kStreamDown, 2, 2, 2>),
-             dim3((unsigned)G * a.tiles), dim3(128), 0, s, a);
+  auto down = [&](auto RT, auto KW) {
+    constexpr int rt = decltype(RT)::value, kw = decltype(KW)::value;
+    a.tiles = W.H / (16 * rt);
+    MOE_LAUNCH("fp8_stream_down", s, (k_fp8_stream<MOE_DT_F32, kStreamDown, rt, kw, kw>),
+               dim3((unsigned)G * a.tiles), dim3(64 * kw), 0, s, a);
+  };
+  if (G <= 16) down(IntC<2>{}, IntC<2>{});
+  else if (G <= 48 || W.I > 512) down(IntC<4>{}, IntC<2>{});
+  else down(IntC<4>{}, IntC<1>{});
   return hipGetLastError();
 }
 

@@ -205,7 +205,7 @@ def test_linear_repeats_bitwise_and_on_another_stream(moe):
 # groups of one row, of several tiles, empty ones
 EXPERTS = [(1, 8, 2, 256, 128, False), (4, 8, 2, 256, 128, True), (8, 64, 10, 384, 256, True), (16, 3, 3, 128, 384, True),
            (17, 8, 2, 256, 128, False), (40, 64, 10, 384, 256, True), (200, 4, 2, 128, 128, True),
-           (300, 5, 1, 640, 384, False)]
+           (300, 5, 1, 640, 384, False), (3, 64, 10, 256, 128, True), (8, 64, 8, 128, 640, False)]
 
 
 def _bank(gen, E, H, I, shared):
