@@ -14,7 +14,7 @@
 // (67 MB, 3.3 TB/s).  Two blocks of 128 under way in a wave took more registers,
 // hence fewer waves, and longer.
 // Experts, T = 8, about 64 of 512 groups (H = 2048, I = 512): gate_up 35 us (135
-// MB, 3.9 TB/s), down 22 us (69 MB, 3.2 TB/s).
+// MB, 3.9 TB/s), down 19 us (69 MB, 3.6 TB/s).
 #include <math.h>
 
 #include "moe_ffn_common.hpp"
