@@ -17,12 +17,11 @@
 //
 // Measured.  Dense, bf16 rows: 8192 x 4096 x 4096 22 us + 134 us (2.1 PFLOP/s;
 // a library's plain f8 product reaches 2.9 at 8192 x 8192 x 8192, this one 2.2),
-// bound by the LDS, whose reads of the operands and writes by
-// the DMA take as long as the MFMAs.  Experts, T = 4096
-// (H = 2048, I = 512, top 10 of 512 and a shared one): 8 + 271 + 174 us; 1.35 GB
-// and 0.68 GB come from memory and 0.18 GB go there, about 5 TB/s, since nearly
-// all of it is weights that one row tile reads: bound by memory, more rows (T =
-// 16384) by the matrix unit.
+// bound by the LDS, whose reads of the operands and writes by the DMA take as
+// long as the MFMAs.  Experts, T = 4096 (H = 2048, I = 512, top 10 of 512 and a
+// shared one): 8 + 271 + 174 us; 1.35 GB and 0.68 GB come from memory and 0.18
+// GB go there, about 5 TB/s, since nearly all of it is weights that one row tile
+// reads: bound by memory, more rows (T = 16384) by the matrix unit.
 #include <math.h>
 
 #include <algorithm>
