@@ -2,7 +2,7 @@
 // in, checks, outputs where none are given, one call of the C ABI on torch's
 // current stream, tensors out.  No arithmetic.  ops.py documents the arguments
 // and passes them on by position; doing the marshalling here instead of there
-// takes a call's host time from about 7 to 4 us, which is most of a decode
+// takes a call's host time from 8 or more to 4 us, which is most of a decode
 // step's call.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>

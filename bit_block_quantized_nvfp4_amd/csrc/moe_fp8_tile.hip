@@ -639,8 +639,8 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
   // A wave computes only its columns of 16 tokens with rows in them, in a loop
   // made for their number: a test at each product would break up the schedule.
   // Every such loop has the same barriers.  The weights of a group with one row
-  // tile are read once (gate_up at T = 1024: 176 us, as ordinary loads 190 us;
-  // where a second tile reads them, 294 us instead of 288 us at T = 4096).
+  // tile are read once (gate_up at T = 1024 takes 7% less than with ordinary
+  // loads; non-temporal ones where a second tile reads them 2% more at T = 4096).
   if constexpr (MODE == kTileLinear) {
     run(IntC<FM>{}, std::false_type{});
   } else {
@@ -813,8 +813,7 @@ hipError_t launch_fp8_expert_ffn(const moe_fp8_weights& W, const uint16_t* x, in
                                  const int32_t* offsets, const int32_t* sorted_slot,
                                  const int32_t* groups, uint16_t* y, void* ws, hipStream_t s) {
   // the layer's own switch; measured (H = 2048, I = 512, top 10 of 512), streams
-  // take 52 us at T = 8, tiles 61 us at T = 9 and 73 us at T = 16, streams 17% more
-  // there
+  // against tiles: T = 9 57 and 61 us, T = 11 65 and 63 us, T = 16 81 and 75 us
   if (T <= kDecodeMaxT)
     return launch_fp8_stream_experts(W, x, T, K, offsets, sorted_slot, groups, (float*)ws, y, s);
   const size_t S = (size_t)T * K + (W.has_shared ? T : 0);
