@@ -231,7 +231,7 @@ hipError_t launch_slot_sum(const void* y, const float* w, const int32_t* slot_po
   const int cpr = H * dtype_bytes(dtype) / 16;
   const RowGrid g = row_grid(T, cpr);
   by_dtype(dtype, [&](auto D) {
-    MOE_LAUNCH(w ? "combine_typed" : "dispatch_grad", s, k_slot_sum<decltype(D)::value>,
+    MOE_LAUNCH(w ? "combine" : "dispatch_grad", s, k_slot_sum<decltype(D)::value>,
                dim3(g.blocks), dim3(256), 0, s, (const u32x4*)y, w, slot_pos, gate, T, K, cpr,
                g.lg, g.cb, has_shared, (u32x4*)out);
   });

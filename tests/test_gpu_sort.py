@@ -130,6 +130,25 @@ def test_combine_takes_a_longer_buffer(moe):
             moe.moe_combine(y[:5], w, pos, K, False)
 
 
+@pytest.mark.parametrize("gated", [False, True])
+def test_combine_of_many_rows_has_the_bits_of_few(moe, gated):
+    T, K, H, n = 1500, 10, 2048, 60
+    flush(f"combine bits T={T} gated={gated}")
+    gen = torch.Generator().manual_seed(3)
+    pos = gpu(permutation(gen, T, K, True))
+    pos[5::11] = -1
+    y, w, gate = torch.randn(T * K + T, H, device="cuda").bfloat16(), torch.rand(T, K, device="cuda"), torch.randn(T, device="cuda")
+    y[100, 3], y[200, 5] = float("nan"), float("inf")
+    call = lambda y, w, pos, g: (moe.moe_combine_gated(y, w, pos, g, K) if gated  # noqa: E731
+                                 else moe.moe_combine(y, w, pos, K, True))
+    out = call(y, w, pos, gate)
+    for t in range(0, T, n):
+        slots = torch.cat([pos[t * K:(t + n) * K], pos[T * K + t:T * K + t + n]])
+        few = torch.where(slots >= 0, torch.arange(len(slots), device="cuda", dtype=torch.int32), slots)
+        part = call(y[slots.clamp_min(0).long()], w[t:t + n], few, gate[t:t + n])
+        assert torch.equal(part.view(torch.int16), out[t:t + n].view(torch.int16))
+
+
 def test_f16_overflow_and_subnormals(moe):
     T, K, H = 2, 2, 8
     pos = torch.tensor([0, 1, 2, 3], dtype=torch.int32)
