@@ -47,7 +47,7 @@ def binding_command(out: str) -> list:
             "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             *[f for p in inc for f in ("-isystem", p)], os.path.join(CSRC, "binding.cpp"), "-o", out,
-            "-L" + cpp_extension.TORCH_LIB_PATH, "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python",
+            "-L" + cpp_extension.TORCH_LIB_PATH, "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python",
             "-L" + HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
 
 

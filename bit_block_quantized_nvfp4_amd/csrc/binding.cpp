@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -128,15 +129,22 @@ void* need(const Tensor& t, ScalarType type, Shape shape, c10::Device dev, const
   return t.data_ptr();
 }
 
+// A new tensor, straight from the device's allocator: at::empty takes a quarter
+// of a microsecond longer to get there (block_norm with four of them 6.8 us a
+// call, so 6.0 us).
+Tensor fresh(ScalarType type, Shape shape, c10::Device dev) {
+  return Tensor(at::detail::empty_cuda(shape, type, dev, std::nullopt));
+}
+
 // An output: the one given, checked, or a new one.
 Tensor output(const Tensor* t, ScalarType type, Shape shape, c10::Device dev, const char* name) {
-  if (!t) return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+  if (!t) return fresh(type, shape, dev);
   need(*t, type, shape, dev, name);
   return *t;
 }
 
 Tensor scratch(const Tensor* t, size_t bytes, c10::Device dev) {
-  if (!t) return at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(dev));
+  if (!t) return fresh(at::kByte, {(int64_t)bytes}, dev);
   if (t->device() != dev || !t->is_contiguous() || (size_t)t->nbytes() < bytes)
     refuse("workspace of ", bytes, " contiguous bytes on ", dev.str(), " needed");
   return *t;
