@@ -9,12 +9,11 @@
 // the same instructions as sixteen; the rows' own reads are masked off past
 // the last.  Each wave quantises the blocks it needs by itself (32 values a
 // lane): repeated per tile, but it saves a launch and its wait.
-// Measured: one row of 2048 x 2048 4.4 us, of which a launch is most; 4096 x 4096
-// 7.8 us (16.8 MB), 65536 x 512 10.1 us (34 MB, 3.4 TB/s), 4096 x 16384 20.5 us
-// (67 MB, 3.3 TB/s).  Two blocks of 128 under way in a wave took more registers,
-// hence fewer waves, and longer.
-// Experts, T = 8, about 64 of 512 groups (H = 2048, I = 512): gate_up 35 us (135
-// MB, 3.9 TB/s), down 19 us (69 MB, 3.6 TB/s).
+// Measured, calls in a row in a graph: one row of 2048 x 2048 4.1 us, of which a
+// launch is most; 4096 x 4096 6.4 us (16.8 MB, 2.6 TB/s), 65536 x 512 8.3 us (34 MB,
+// 4.1 TB/s), 4096 x 8192 10.6 us (34 MB, 3.2 TB/s).
+// Experts, T = 8, about 75 of 512 groups (H = 2048, I = 512): gate_up 35 us (159
+// MB, 4.5 TB/s), down 20 us (79 MB, 4.0 TB/s).
 #include <math.h>
 
 #include "moe_ffn_common.hpp"
@@ -57,7 +56,6 @@ __device__ __forceinline__ void load32(const void* __restrict__ row, int k, int 
 template <int DT, int MODE, int RT, int KW, int NW>
 __global__ __launch_bounds__(64 * NW) void k_fp8_stream(StreamArgs a) {
   constexpr int RW = NW / KW;            // tile groups of the block
-  constexpr bool EX = MODE == kStreamLinear && DT == MOE_DT_F32;
   constexpr int kPad = 1;
   __shared__ f32x4 red[NW][RT][64 + kPad];
   const int lane = threadIdx.x & 63;
@@ -116,14 +114,13 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_stream(StreamArgs a) {
     for (int i = 0; i < RT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     for (int b = kw; b < nb; b += KW) {
       const int k = b * kQB + 16 * q;
-      Frag<EX> w[RT];
+      Frag<16> w[RT];
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
         // chunks past the row's end are read from its start instead: their
         // counterparts in the token rows are zeros
-        const u32x4 lo = *(const u32x4*)(wrow[i] + (k < a.K ? k : 0));
-        const u32x4 hi = *(const u32x4*)(wrow[i] + (k + 64 < a.K ? k + 64 : 0));
-        w[i].set(join8(lo, hi));
+        w[i].set({*(const u32x4*)(wrow[i] + (k < a.K ? k : 0)),
+                  *(const u32x4*)(wrow[i] + (k + 64 < a.K ? k + 64 : 0))});
       }
       constexpr int N = Chunk<DT>::N;
       u32x4 v[32 / N];
@@ -142,16 +139,17 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_stream(StreamArgs a) {
       am = fmaxf(am, __shfl_xor(am, 32));
       am = q_floor(am);
       const float m = 448.0f / am, sx = am / 448.0f;
-      i32x8 xq;
+      u32x4 xq[2];
 #pragma unroll
       for (int i = 0; i < 32 / N; ++i) {
         float f[N];
         Chunk<DT>::unpack(v[i], f);
 #pragma unroll
         for (int j = 0; j < N; j += 4)
-          xq[(i * N + j) / 4] = (int)fp8x4(f[j] * m, f[j + 1] * m, f[j + 2] * m, f[j + 3] * m);
+          xq[(i * N + j) / 16][(i * N + j) / 4 % 4] =
+              fp8x4(f[j] * m, f[j + 1] * m, f[j + 2] * m, f[j + 3] * m);
       }
-      Frag<EX> xf;
+      Frag<16> xf;
       xf.set(xq);
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
@@ -203,13 +201,13 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_stream(StreamArgs a) {
 // chip holds, it takes two row tiles, which share its rows' quantisation, and
 // more of K (in a row in a graph, us, RT x KW):
 //   rows x N x K        1x16   1x8   2x8   1x4   2x4
-//   1 x 4096 x 4096      7.8   8.4  11.2  12.2  14.5
-//   16 x 512 x 8192     13.7  15.4  19.0  18.3  24.8
-//   1 x 2048 x 2048      4.4   4.7   5.9   6.1   7.3
-//   1 x 4096 x 1024      4.0   3.8   4.2   4.3   4.9
-//   1 x 16384 x 1024    10.6   7.7   6.4   6.9   7.3
-//   1 x 32768 x 512     15.6  10.1   7.7   7.4   6.3
-//   1 x 2048 x 512       3.1   2.9   3.2   2.8   3.2
+//   1 x 4096 x 4096      6.4   7.2   8.9  10.0  12.1
+//   16 x 512 x 8192     13.0  13.2  17.1  14.6  17.8
+//   1 x 2048 x 2048      4.1   4.1   5.0   5.1   6.3
+//   1 x 4096 x 1024      3.6   3.3   3.7   3.5   4.2
+//   1 x 16384 x 1024     9.1   6.3   5.0   5.5   5.1
+//   1 x 32768 x 512     12.2   7.9   5.9   6.2   4.9
+//   1 x 2048 x 512       2.9   2.7   3.1   2.6   3.0
 template <typename F>
 static void by_linear_shape(int N, int K, F&& f) {
   const bool wide = N >= 8192;
@@ -283,11 +281,12 @@ hipError_t launch_fp8_stream_experts(const moe_fp8_weights& W, const uint16_t* x
   // K.  The call in a row in a graph, H = 2048, I = 512, top 10 of 512 and a
   // shared one, us (gate_up waves, down row tiles x waves; * the one taken):
   //   T (groups)   8, 2x2  4, 2x2  8, 4x2  4, 4x2  4, 4x1
-  //   1 (11)        16.9*   18.8    18.0    19.9    21.0
-  //   2 (21)        25.5    24.8    26.0    24.1*   25.1
-  //   4 (41)        39.9    38.7    37.4    36.5*   37.3
-  //   6 (61)        51.1                    45.2    44.9*
-  //   8 (81)        60.0    56.2            54.2    52.8*
+  //   1 (11)        15.0*   15.9    15.7    17.0    17.5
+  //   2 (21)        22.4    21.2*   21.9    21.7    22.4
+  //   4 (41)        33.9    32.4*   35.8    34.6    33.4
+  //   6 (61)        43.3    40.9    44.0    41.4    40.5*
+  //   8 (81)        51.0    52.5    57.8    51.9    47.7*
+  //   12 (121)      83.0    67.3    72.8    65.5    64.4*
   if (G > 16)
     MOE_LAUNCH("fp8_stream_gate_up", s, (k_fp8_stream<MOE_DT_BF16, kStreamGateUp, 2, 4, 4>),
                dim3((unsigned)G * a.tiles), dim3(256), 0, s, a);
@@ -308,8 +307,8 @@ hipError_t launch_fp8_stream_experts(const moe_fp8_weights& W, const uint16_t* x
     MOE_LAUNCH("fp8_stream_down", s, (k_fp8_stream<MOE_DT_F32, kStreamDown, rt, kw, kw>),
                dim3((unsigned)G * a.tiles), dim3(64 * kw), 0, s, a);
   };
-  if (G <= 16) down(IntC<2>{}, IntC<2>{});
-  else if (G <= 48 || W.I > 512) down(IntC<4>{}, IntC<2>{});
+  if (G <= 48) down(IntC<2>{}, IntC<2>{});
+  else if (W.I > 512) down(IntC<4>{}, IntC<2>{});
   else down(IntC<4>{}, IntC<1>{});
   return hipGetLastError();
 }

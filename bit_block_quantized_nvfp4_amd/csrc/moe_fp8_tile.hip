@@ -1,27 +1,29 @@
 // e4m3 products of many rows: quantisation of the rows, then tiles of BN
-// weight rows x BM token rows on the 128-wide f8 MFMA.
+// weight rows x BM token rows, the codes as f16 on the 32x32x16 f16 MFMA, whose
+// f32 sums drop nothing of a product (the f8 MFMAs do: moe_fp8.hpp).
 //
 //   z[t][n] = sum_b s[t][b] S[n / 128][b] sum_{k in block b} q[t][k] W[n][k]
 //
-// One K step is one block of 128, so a step's MFMA starts from zero and its
-// result is scaled into the f32 accumulators: 4 multiply-adds per MFMA of 32
-// cycles, which run beside the matrix unit.  Weights are the MFMA's A operand:
-// a lane then has one token per tile column, hence one scale, and four
-// consecutive outputs.
+// One K step is one block of 128, so a step's products start from zero and are
+// scaled into the f32 accumulators: 16 multiply-adds per 8 MFMAs of 32 cycles.
+// Weights are the MFMA's A operand: a lane then has one token per tile column,
+// hence one scale, and four consecutive outputs at a time.
 //
-// Both operands go from memory to LDS without registers (16 bytes a lane, the
-// next step's while this one is computed).  A row of a step is 128 bytes, its
-// 16-byte chunk c stands at place c ^ (row % 8), so that the reads of 16 rows
-// at one chunk meet every bank once; the DMA writes lanes in order, hence the
-// permutation is applied to the addresses that it reads.
+// Both operands go from memory to LDS as codes, without registers (16 bytes a
+// lane, the next step's while this one is computed); a wave converts them as it
+// reads them.  A row of a step is 128 bytes, its 16-byte chunk c stands at place
+// c ^ (row % 8), so that the reads of 8 rows at one chunk meet every bank once;
+// the DMA writes lanes in order, hence the permutation is applied to the
+// addresses that it reads.
 //
-// Measured.  Dense, bf16 rows: 8192 x 4096 x 4096 22 us + 134 us (2.1 PFLOP/s;
-// a library's plain f8 product reaches 2.9 at 8192 x 8192 x 8192, this one 2.2),
-// bound by the LDS, whose reads of the operands and writes by the DMA take as
-// long as the MFMAs.  Experts, T = 4096 (H = 2048, I = 512, top 10 of 512 and a
-// shared one): 8 + 271 + 174 us; 1.35 GB and 0.68 GB come from memory and 0.18
-// GB go there, about 5 TB/s, since nearly all of it is weights that one row tile
-// reads: bound by memory, more rows (T = 16384) by the matrix unit.
+// Measured.  Dense, bf16 rows: 8192 x 4096 x 4096 20 us + 255 us (1.08 PFLOP/s), 8192
+// x 8192 x 8192 45 us + 960 us (1.15), where a library's bf16 product of that size
+// reaches 1.21 and the MFMAs alone, on data of mixed bits, 1.65: bound by the
+// matrix unit, with 128 conversions and 64 multiply-adds a wave beside 32 MFMAs.
+// Experts (H = 2048, I = 512, top 10 of 512 and a shared one): T = 4096 8 + 341 + 216
+// us for 1.35 GB and 0.68 GB from memory (nearly all of it weights that one row
+// tile reads) and 283 GFLOP, neither of which alone takes as long; T = 16384 22 +
+// 945 + 548 us (1133 GFLOP, the matrix unit).
 #include <math.h>
 
 #include <algorithm>
@@ -229,25 +231,24 @@ __device__ __forceinline__ void meet() {
 // about half a microsecond of waiting whatever its size, which counts where
 // there are few tiles.
 template <int MODE, int DT, int BN, int BM, int WN, int WM, int NBUF, int KG = 1>
-__global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
+__global__ __launch_bounds__(64 * WN * WM * KG, 2) void k_fp8_tile(TileArgs a) {
   constexpr int NW = WN * WM, NT = 64 * NW;    // waves and threads of a group
   constexpr int TN = BN / WN, TM = BM / WM;    // a wave's part of the tile
-  constexpr int FN = TN / 16, FM = TM / 16;
+  constexpr int FN = TN / 32, FM = TM / 32;    // products of 32 x 32
   constexpr int DW = BN * 8 / NT, DX = BM * 8 / NT;  // 16-byte chunks per thread and step
   constexpr int D = DW + DX + 1;               // memory operations per wave and step
   constexpr int kTok = BN * kQB, kScale = kTok + BM * kQB;  // LDS offsets in a buffer
   constexpr int BS = (BM + 63) / 64;           // waves that bring a step's token scales
   constexpr int kBuf = kScale + BS * 256;
-  constexpr bool EX = DT == MOE_DT_F32;
   constexpr int ES = DT == MOE_DT_F32 ? 4 : 2;
   constexpr int CR = TN * ES / 16;             // 16-byte chunks of a row of the wave's output
   constexpr int NS = (BN + kQB - 1) / kQB;     // weight scales of a step
   constexpr int BC = MODE == kTileGateUp ? BN / 2 : BN;  // columns of a tile
-  static_assert(BN * 8 % NT == 0 && BM * 8 % NT == 0 && TN % 16 == 0 && TM % 16 == 0 &&
-                    BM % 32 == 0 && BS <= NW && NBUF * D < 64 && FN >= 2 && 64 % CR == 0,
+  static_assert(BN * 8 % NT == 0 && BM * 8 % NT == 0 && TN % 32 == 0 && TM % 32 == 0 &&
+                    BS <= NW && NBUF * D < 64 && 64 % CR == 0,
                 "tile shape");
   static_assert(MODE == kTileLinear || BM == kPM, "row tiles of the items");
-  static_assert(MODE != kTileGateUp || BC == kQB, "a tile holds one scale of h");
+  static_assert(MODE != kTileGateUp || (BC == kQB && FN == 2), "a tile holds one scale of h, a wave a gate and an up row");
   static_assert(KG == 1 || (MODE == kTileLinear && (KG - 1) * BN * BM * 4 + NW * 16 * TN * ES <= KG * NBUF * kBuf),
                 "the groups' sums fit");
   __shared__ __align__(1024) uint8_t lds_all[KG * NBUF * kBuf];
@@ -283,8 +284,8 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
     rows = a.R - m0;
   } else {
     // the column tiles of two row tiles back to back on one XCD: the tiles of a
-    // group of several share its weights in the L2 (T = 4096: 271 + 174 us; in
-    // runs of one row tile 278 + 179 us, of four 282 + 178 us)
+    // group of several share its weights in the L2 (the call at T = 16384 1476 us,
+    // in runs of one row tile 1490 us; T = 4096 545 and 546 us)
     const int per = a.nt / ntb;
     const int lin = pf_item_of_block(blockIdx.x, gridDim.x, 2 * per), item = lin / per;
     item_at = (size_t)item * ((MODE == kTileGateUp ? a.N : a.K) / kQB) * kPM;
@@ -328,9 +329,9 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
                                    : buf_of(a.xq + (size_t)m0 * ldx, (uint32_t)rows * ldx);
   // Token scales: 64 rows of a step are one load of a wave, 256 bytes in one
   // piece where the row tile is known when they are written: scattered ones take
-  // a lookup each, 64 of them as many as 8 KB of codes.  8192 x 4096 x 4096: 166
-  // us with all eight waves bringing 64 scattered scales, 148 us with the four
-  // that have to, 146 us so; 8192 x 8192 x 8192: 538, 513 and 492 us.
+  // a lookup each, 64 of them as many as 8 KB of codes (with tiles of 256 x 256
+  // and products of half the time, 8192 x 8192 x 8192 took 538 us with all eight
+  // waves bringing 64 scattered scales, 513 us with the four that have to, 492 us so).
   constexpr int SR = MODE == kTileLinear ? kScaleRows : MODE == kTileDown ? kPM : 1;
   const u32x4 sbuf = MODE == kTileGateUp ? buf_of(a.xs, (uint32_t)a.T * (uint32_t)nb * 4u)
                    : MODE == kTileDown   ? buf_of(a.xs + item_at, (uint32_t)(nb * SR) * 4u)
@@ -425,35 +426,35 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
     }
   }
 
-  f32x4 acc[FN][FM];
-  // columns of 16 tokens of this wave with rows in them
-  const int live = min(FM, max(0, (rows - wm * TM + 15) / 16));
+  f32x16 acc[FN][FM];
+  // columns of 32 tokens of this wave with rows in them
+  const int live = min(FM, max(0, (rows - wm * TM + 31) / 32));
   const int hs = MODE == kTileGateUp ? 0 : wn * TN / kQB;
 
-  // this lane's two chunks of row 16 i + lane % 16
-  const int fr = lane & 15, fq = lane >> 4;
-  const uint32_t c0 = (uint32_t)(fr * kQB + ((fq ^ (fr & 7)) << 4));
-  const uint32_t c1 = (uint32_t)(fr * kQB + (((fq + 4) ^ (fr & 7)) << 4));
-  auto frag = [&](const uint8_t* p, int row16) __attribute__((always_inline)) {
-    return join8(*(const u32x4*)(p + row16 * kQB + c0), *(const u32x4*)(p + row16 * kQB + c1));
+  // this lane's four chunks of row 32 i + lane % 32
+  const int fr = lane & 31, fq = lane >> 5;
+  struct Codes {
+    u32x4 c[4];
   };
-  // The next step's first operands, read while the last products of a step run
-  // (none where the registers end before).
-  constexpr int PRE = FN * FM * 4 + FM * 16 > 160 ? 0 : FM;
-  i32x8 tn[PRE > 0 ? PRE : 1], wnx;
-  auto first = [&](int at, auto count) __attribute__((always_inline)) {
-    constexpr int LV = decltype(count)::value;
-    if (PRE > 0 && LV > 0) wnx = frag(lds + at + wn * TN * kQB, 0);
+  auto codes_at = [&](const uint8_t* p, int row32) __attribute__((always_inline)) {
+    Codes r;
 #pragma unroll
-    for (int j = 0; j < PRE; ++j)
-      if (j < LV) tn[j] = frag(lds + at + kTok + wm * TM * kQB, 16 * j);
+    for (int i = 0; i < 4; ++i)
+      r.c[i] = *(const u32x4*)(p + (row32 + fr) * kQB + (((fq + 2 * i) ^ (fr & 7)) << 4));
+    return r;
+  };
+  // The next step's first operands, read while the last products of a step run.
+  Codes wnx, tnx;
+  auto first = [&](int at, auto count) __attribute__((always_inline)) {
+    if (decltype(count)::value == 0) return;
+    wnx = codes_at(lds + at + wn * TN * kQB, 0);
+    tnx = codes_at(lds + at + kTok + wm * TM * kQB, 0);
   };
   // Step at buffer `at`, whose weight scales are sc[0] and (gate_up: the up
-  // rows') sc[nbp].  Two barriers: behind the first product row every wave holds
-  // all its token fragments, so the next tokens may go to their buffer; before
-  // the last two rows every wave has read the last of the weights, and the step
-  // after has landed (what was asked for later may be under way), so its first
-  // operands are read while those products run.  Two product rows: one barrier.
+  // rows') sc[nbp].  One barrier, behind the products of the first weight rows:
+  // every wave has then read all its operands, so the buffer may be filled again,
+  // and the step after has landed (what was asked for later may be under way), so
+  // its first operands are read while the last products run.
   auto step = [&](int at, const float* sc, bool some, auto last, auto count, auto once) __attribute__((always_inline)) {
     constexpr int LV = decltype(count)::value;
     constexpr bool kLast = decltype(last)::value;
@@ -461,85 +462,73 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
     const uint8_t* pt = lds + at + kTok + wm * TM * kQB;
     const float* ps = (const float*)(lds + at + kScale) + wm * TM + fr;
     const int next = at == (NBUF - 1) * kBuf ? 0 : at + kBuf;
-    Frag<EX> tf[FM];
+    Frag<32> wf, tf[FM];
     float s0[FM], s1[FM];
     // a group's step past the end adds zeros
     const float w0 = KG == 1 || some ? sc[0] : 0.f, w1 = MODE == kTileGateUp ? sc[nbp] : 0.f;
+    Codes wc, tc;
+    if (LV > 0) {
+      wf.set(wnx.c);
+      tf[0].set(tnx.c);
+    }
+    if (LV > 1) tc = codes_at(pt, 32);
+    if (LV > 0 && FN > 1) wc = codes_at(pw, 32);
 #pragma unroll
     for (int j = 0; j < LV; ++j) {
-      tf[j].set(j < PRE ? tn[j < PRE ? j : 0] : frag(pt, 16 * j));
-      const float sx = ps[16 * j];
+      const float sx = ps[32 * j];
       s0[j] = sx * w0;
       s1[j] = MODE == kTileGateUp ? sx * w1 : s0[j];
     }
-    i32x8 wc = {};
-    if (LV > 0) wc = PRE > 0 ? wnx : frag(pw, 0);
-    // row i's products run while row i - 1's are scaled into the sums
-    f32x4 p[2][FM];
-    auto add = [&](int i) __attribute__((always_inline)) {
+    // a product runs while the one before is scaled into the sums
+    f32x16 p[2];
+    auto add = [&](int b) __attribute__((always_inline)) {
+      const int i = b / (LV > 0 ? LV : 1), j = b % (LV > 0 ? LV : 1);
+      const float s = i == 0 ? s0[j] : s1[j];
 #pragma unroll
-      for (int j = 0; j < LV; ++j) {
-        const float s = (MODE == kTileGateUp && i >= FN / 2) ? s1[j] : s0[j];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(s, p[i & 1][j][q], acc[i][j][q]);
-      }
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = fmaf(s, p[b & 1][e], acc[i][j][e]);
     };
 #pragma unroll
     for (int i = 0; i < FN; ++i) {
-      Frag<EX> wf;
-      wf.set(wc);
-      if (LV > 0 && i + 1 < FN) wc = frag(pw, 16 * (i + 1));
-      if (i == FN - 2 && !kLast) {
-        wait_step<(NBUF - 2) * D + (FN > 2 ? DX + 1 : 0)>();
-        if (FN == 2) dma_tokens();
+      if (LV > 0 && i > 0) wf.set(wc.c);
+#pragma unroll
+      for (int j = 0; j < LV; ++j) {
+        if (i == 0 && j > 0) tf[j].set(tc.c);
+        const int b = i * LV + j;
+        p[b & 1] = mfma128(wf, tf[j]);
+        if (b > 0) add(b - 1);
+      }
+      if (i == 0 && !kLast) {
+        __builtin_amdgcn_sched_barrier(0);
+        wait_step<(NBUF - 2) * D>();
+        dma_tokens();
         dma_weights(once);
         first(next, count);
       }
-#pragma unroll
-      for (int j = 0; j < LV; ++j) p[i & 1][j] = mfma128(wf, tf[j]);
-      if (i > 0) add(i - 1);
-      if (FN > 2 && i == 0 && !kLast) {
-        __builtin_amdgcn_sched_barrier(0);
-        meet();
-        dma_tokens();
-      }
-      if (!EX) {
-#pragma unroll
-        for (int j = 0; j < LV; ++j) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // one MFMA
-          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);  // four vector operations
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
     }
-    add(FN - 1);
+    if constexpr (LV > 0) add(FN * LV - 1);
   };
 
   // gate_up: h = silu(gate) up in f32, its absmax over the tile's 128 columns
   // (one scale of h), then its codes.  n: the tile's first column.
   auto put_h = [&](int n, auto count) __attribute__((always_inline)) {
     constexpr int LV = decltype(count)::value;
-    constexpr int HN = FN / 2;
     float* amax = (float*)side;                // [WN][BM]
 #pragma unroll
     for (int j = 0; j < LV; ++j) {
       float am = 0.f;
 #pragma unroll
-      for (int i = 0; i < HN; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float h = silu_f32(acc[i][j][q]) * acc[HN + i][j][q];
-          acc[i][j][q] = h;
-          am = fmaxf(am, fabsf(h));
-        }
-      am = fmaxf(am, __shfl_xor(am, 16));
+      for (int e = 0; e < 16; ++e) {
+        const float h = silu_f32(acc[0][j][e]) * acc[FN - 1][j][e];
+        acc[0][j][e] = h;
+        am = fmaxf(am, fabsf(h));
+      }
       am = fmaxf(am, __shfl_xor(am, 32));
-      if (fq == 0) amax[wn * BM + wm * TM + 16 * j + fr] = am;
+      if (fq == 0) amax[wn * BM + wm * TM + 32 * j + fr] = am;
     }
     meet();
 #pragma unroll
     for (int j = 0; j < LV; ++j) {
-      const int r = wm * TM + 16 * j + fr;
+      const int r = wm * TM + 32 * j + fr;
       float am = amax[r];
 #pragma unroll
       for (int w = 1; w < WN; ++w) am = fmaxf(am, amax[w * BM + r]);
@@ -548,9 +537,10 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
       if (r < rows) {
         uint8_t* dst = (uint8_t*)a.out + (size_t)(m0 + r) * a.N + n + wn * (TN / 2);
 #pragma unroll
-        for (int i = 0; i < HN; ++i)
-          *(uint32_t*)(dst + 16 * i + 4 * fq) = fp8x4(acc[i][j][0] * m, acc[i][j][1] * m,
-                                                      acc[i][j][2] * m, acc[i][j][3] * m);
+        for (int g = 0; g < 4; ++g)
+          *(uint32_t*)(dst + 8 * g + 4 * fq) =
+              fp8x4(acc[0][j][4 * g] * m, acc[0][j][4 * g + 1] * m, acc[0][j][4 * g + 2] * m,
+                    acc[0][j][4 * g + 3] * m);
         if (wn == 0 && fq == 0)
           a.out_scales[item_at + (size_t)(n / kQB) * kPM + r] = am / 448.0f;
       }
@@ -565,24 +555,29 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
     uint8_t* mine = (MODE == kTileDown ? side : lds) + (KG > 1 ? (KG - 1) * BN * BM * 4 : 0) + wv * (16 * TN * ES);
     const int c = lane % CR, nc = n + wn * TN + c * (16 / ES);
 #pragma unroll
-    for (int j = 0; j < LV; ++j) {
+    for (int jh = 0; jh < 2 * LV; ++jh) {
+      const int j = jh / 2;
+      if (fr / 16 == jh % 2) {
 #pragma unroll
-      for (int i = 0; i < FN; ++i) {
-        const int at = (16 * i + 4 * fq) * ES;
-        uint8_t* dst = mine + fr * (TN * ES) + (((at / 16) ^ (fr & (CR - 1))) << 4) + (at & 15);
-        const f32x4 v = acc[i][j];
-        if (DT == MOE_DT_F32)
-          *(f32x4*)dst = v;
-        else if (DT == MOE_DT_BF16)
-          *(u32x2*)dst = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-        else
-          *(u32x2*)dst = u32x2{pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3])};
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int at = (32 * i + 8 * g + 4 * fq) * ES;
+            uint8_t* dst = mine + (fr & 15) * (TN * ES) + (((at / 16) ^ (fr & (CR - 1))) << 4) + (at & 15);
+            const f32x4 v = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+            if (DT == MOE_DT_F32)
+              *(f32x4*)dst = v;
+            else if (DT == MOE_DT_BF16)
+              *(u32x2*)dst = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+            else
+              *(u32x2*)dst = u32x2{pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3])};
+          }
       }
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
       for (int r0 = 0; r0 < 16; r0 += 64 / CR) {
-        const int r = r0 + lane / CR, row = wm * TM + 16 * j + r;
-        const bool on = MODE == kTileDown ? (mine_ok >> ((16 * j + r0) * CR / 64) & 1) : row < rows;
+        const int r = r0 + lane / CR, row = wm * TM + 16 * jh + r;
+        const bool on = MODE == kTileDown ? (mine_ok >> ((16 * jh + r0) * CR / 64) & 1) : row < rows;
         const u32x4 v = *(const u32x4*)(mine + r * (TN * ES) + ((c ^ (r & (CR - 1))) << 4));
         if (on && nc < a.N && r < 16)
           *(u32x4*)((uint8_t*)a.out + ((size_t)(m0 + row) * a.N + nc) * ES) = v;
@@ -601,54 +596,55 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
 #pragma unroll
       for (int i = 0; i < FN; ++i)
 #pragma unroll
-        for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < FM; ++j) acc[i][j] = f32x16{};
       const float* end = sc + nb;
       sc += kg;
-      for (int b = 0; b + 1 < steps; ++b, sc += KG, on())
+      // grouped modes: the last step of the last tile asks for operands too, and
+      // gets zeros (a branch there would double the step, and spill)
+      for (int b = MODE == kTileLinear; b < steps; ++b, sc += KG, on())
         step(at, sc, true, std::false_type{}, count, once);
-      if (MODE != kTileLinear && tile + 1 < ntb) {
-        step(at, sc, true, std::false_type{}, count, once);
-        on();
-      } else {
-        step(at, sc, sc < end, std::true_type{}, count, once);
-        wait_step<0>();  // nothing is under way to LDS any more
-      }
+      if (MODE == kTileLinear) step(at, sc, sc < end, std::true_type{}, count, once);
+      if (MODE == kTileLinear || tile + 1 == ntb) wait_step<0>();  // nothing is under way to LDS any more
       if (KG > 1) {
         // lane by lane, 16 bytes at a time
         f32x4* mine = (f32x4*)lds_all + tid;
         if (kg > 0) {
 #pragma unroll
-          for (int i = 0; i < FN; ++i)
+          for (int i = 0; i < FN * FM; ++i)
 #pragma unroll
-            for (int j = 0; j < FM; ++j)
-              mine[(((kg - 1) * FN + i) * FM + j) * NT] = acc[i][j];
+            for (int g = 0; g < 4; ++g) {
+              const f32x16& v = acc[i / FM][i % FM];
+              mine[(((kg - 1) * FN * FM + i) * 4 + g) * NT] = f32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
+            }
         }
         meet();
         if (kg > 0) return;
 #pragma unroll
-        for (int g = 0; g < KG - 1; ++g)
+        for (int o = 0; o < KG - 1; ++o)
 #pragma unroll
-          for (int i = 0; i < FN; ++i)
+          for (int i = 0; i < FN * FM; ++i)
 #pragma unroll
-            for (int j = 0; j < FM; ++j) acc[i][j] += mine[((g * FN + i) * FM + j) * NT];
+            for (int g = 0; g < 4; ++g) {
+              const f32x4 v = mine[((o * FN * FM + i) * 4 + g) * NT];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[i / FM][i % FM][4 * g + e] += v[e];
+            }
       }
       if (MODE == kTileGateUp) put_h(n0 + tile * BC, count);
       else put_out(n0 + tile * BC, count);
     }
   };
-  // A wave computes only its columns of 16 tokens with rows in them, in a loop
+  // A wave computes only its columns of 32 tokens with rows in them, in a loop
   // made for their number: a test at each product would break up the schedule.
   // Every such loop has the same barriers.  The weights of a group with one row
-  // tile are read once (gate_up at T = 1024 takes 7% less than with ordinary
-  // loads; non-temporal ones where a second tile reads them 2% more at T = 4096).
+  // tile are read once (the call at T = 512 takes 270 us, with ordinary loads 286
+  // us; at T = 1024 311 and 320 us).
   if constexpr (MODE == kTileLinear) {
     run(IntC<FM>{}, std::false_type{});
   } else {
-    static_assert(FM == 4, "the loops below");
+    static_assert(FM == 2, "the loops below");
     auto by_live = [&](auto once) __attribute__((always_inline)) {
-      if (live == 4) run(IntC<4>{}, once);
-      else if (live == 3) run(IntC<3>{}, once);
-      else if (live == 2) run(IntC<2>{}, once);
+      if (live == 2) run(IntC<2>{}, once);
       else if (live == 1) run(IntC<1>{}, once);
       else run(IntC<0>{}, once);
     };
@@ -658,17 +654,12 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void k_fp8_tile(TileArgs a) {
 }
 
 // The linear mode's tiles, largest first: f with the kernel, BN, BM and threads.
-// Rows of f32 take twice the operand registers, hence fewer shapes.
 constexpr int kTileShapes = 6;
 template <int DT, typename F>
 static void by_linear_tile(int shape, F&& f) {
-  if constexpr (DT != MOE_DT_F32) {
-    if (shape == 0) f(&k_fp8_tile<kTileLinear, DT, 256, 256, 2, 4, 2>, 256, 256, 512);
-    if (shape == 1) f(&k_fp8_tile<kTileLinear, DT, 128, 128, 2, 2, 2, 2>, 128, 128, 512);
-    if (shape == 2) f(&k_fp8_tile<kTileLinear, DT, 128, 64, 2, 2, 3, 2>, 128, 64, 512);
-  } else {
-    if (shape == 1) f(&k_fp8_tile<kTileLinear, DT, 128, 128, 2, 2, 2>, 128, 128, 256);
-  }
+  if (shape == 0) f(&k_fp8_tile<kTileLinear, DT, 256, 128, 4, 2, 3>, 256, 128, 512);
+  if (shape == 1) f(&k_fp8_tile<kTileLinear, DT, 128, 128, 2, 2, 2, 2>, 128, 128, 512);
+  if (shape == 2) f(&k_fp8_tile<kTileLinear, DT, 128, 64, 2, 2, 3, 2>, 128, 64, 512);
   if (shape == 3) f(&k_fp8_tile<kTileLinear, DT, 64, 64, 2, 2, 4, 2>, 64, 64, 512);
   if (shape == 4) f(&k_fp8_tile<kTileLinear, DT, 32, 64, 1, 2, 3, 4>, 32, 64, 512);
   if (shape == 5) f(&k_fp8_tile<kTileLinear, DT, 32, 32, 1, 1, 4, 4>, 32, 32, 256);
@@ -676,33 +667,32 @@ static void by_linear_tile(int shape, F&& f) {
 
 // The shape whose rounds of 256 blocks (a block's LDS leaves a compute unit no
 // second one) take the least time together; a round's relative time hardly
-// depends on how full it is.  Tile kernel with each shape (us, with about 3.5 us
-// of event overhead; * the one taken):
-//   rows x N x K, bf16    256x256  128x128  128x64  64x64  32x64  32x32
-//   8192 x 4096 x 4096       140*     200     284    376
-//   2600 x 4096 x 4096        60*      71             125    160    243
-//   2048 x 4096 x 4096        59       52*     64      91
-//   640 x 4096 x 4096                  25*             37     42     64
-//   512 x 4096 x 4096         52       24      18*     25     34     50
-//   333 x 4168 x 2064         32       16      13*     18     26     31
-//   512 x 2048 x 2048                  14      12      10*    13     20
-//   128 x 4096 x 4096                  23      18      14     11*    16
-//   64 x 4096 x 4096                   22      17      15     12     11*
-//   32 x 8192 x 8192                   38      29      24     18     16*
-//   f32 rows
-//   2048 x 4096 x 4096                 71*            109    136    208
-//   512 x 4096 x 4096                  42              32*    38     56
-//   128 x 4096 x 4096                  39              17     12*    17
-//   32 x 4096 x 4096                   38              16     12     10*
+// depends on how full it is.  The whole call with each shape (us, in a row in a
+// graph; * the one taken):
+//   rows x N x K, bf16    256x128  128x128  128x64  64x64  32x64  32x32
+//   8192 x 4096 x 4096       269*     294     355    447    571    891
+//   8192 x 8192 x 8192      1028*    1054    1306   1635   1977   2903
+//   2600 x 4096 x 4096       117      105*    130    158    191    288
+//   2048 x 4096 x 4096        70*      74      91    118    149    228
+//   1024 x 4096 x 4096        59       40*     48     63     78    117
+//   640 x 4096 x 4096         58       35*     45     47     50     74
+//   512 x 4096 x 4096         57       35      27*    34     41     61
+//   333 x 4168 x 2064         34       23      18*    22     30     36
+//   512 x 2048 x 2048         32       21      16     13*    16     23
+//   256 x 4096 x 4096         55       32      24     19*    22     32
+//   128 x 4096 x 4096         54       32      23     18     13*    18
+//   64 x 4096 x 4096          53       31      23     17     12     11*
+//   32 x 8192 x 8192         100       55      39     28     20     17*
+// f32 rows take up to a tenth longer with the larger tiles, in the same order.
 template <int DT>
 static int linear_tile(int T, int N) {
   int best = 0;
   long least = 0;
   for (int s = 0; s < kTileShapes; ++s)
     by_linear_tile<DT>(s, [&](auto, int bn, int bm, int) {
-      constexpr int cost[2][kTileShapes] = {{64, 25, 18, 14, 11, 10}, {0, 38, 0, 16, 12, 10}};
+      constexpr int cost[kTileShapes] = {58, 34, 24, 16, 11, 8};
       const long tiles = (long)((N + bn - 1) / bn) * ((T + bm - 1) / bm);
-      const long t = (tiles + 255) / 256 * cost[DT == MOE_DT_F32][s];
+      const long t = (tiles + 255) / 256 * cost[s];
       if (least == 0 || t < least) least = t, best = s;
     });
   return best;
@@ -741,16 +731,16 @@ hipError_t launch_fp8_quant(const void* x, int T, int K, int dtype, uint8_t* cod
 static size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 static int blocks_of(int K) { return (K + kQB - 1) / kQB; }
 
-// Few rows stream the weights in one launch; but where both N and K are large,
-// or the rows themselves are, the tiles' longer runs of loads are worth the launch
-// of their quantisation (both in a row in a graph, us, streamed against tiles: 1
-// row of 4096 x 4096 7.8 against 9.9, 16 rows 9.1 against 10.4; 1 row of 4096 x
-// 8192 12.3 against 13.9, of 65536 x 512 10.1 against 14.5; 1 row of 8192 x 4096
-// 12.7 against 12.3, 16 rows of 6144 x 4096 14.9 against 11.3, 1 row of 8192 x
-// 8192 21.9 against 17.3; 16 rows of 2048 x 8192 14.5 against 13.5, 8 rows 11.8
-// against 13.2).
+// Up to 16 rows stream the weights in one launch; but where both N and K are
+// large the tiles' longer runs of loads are worth the launch of their quantisation
+// (both in a row in a graph, us, streamed against tiles: 1 row of 4096 x 4096 6.5
+// against 9.5, 16 rows 8.5 against 9.9; 1 row of 4096 x 8192 10.6 against 14.4, 16
+// rows 14.2 against 14.7; 1 row of 65536 x 512 8.3 against 12.6, 16 rows 11.1
+// against 13.6; 16 rows of 2048 x 8192 13.5 against 14.2; 16 rows of 6144 x 4096
+// 13.3 against 9.9, 1 row of 8192 x 8192 18.3 against 15.9, of 8192 x 4096 9.2
+// against 10.1).
 static bool fp8_linear_streams(int T, int N, int K) {
-  if (T > 16 || (T > 8 && K >= 8192)) return false;
+  if (T > 16) return false;
   return N <= 4096 || K < 2048 || (long)N * K < 3L << 23;
 }
 
@@ -801,9 +791,16 @@ static int tiles_per_block(size_t S, int G, int nt) {
   return n;
 }
 
+// Batches up to this many tokens stream the experts' weights (16 rows of a group
+// are one pass).  Streams against tiles, us: H = 2048, I = 512, top 10 of 512, T =
+// 9 52 and 68, 11 62 and 72, 13 66 and 78, 16 87 and 80; H = 4096, I = 1024, top 2
+// of 8, T = 9 31 and 41, 13 30 and 47, 16 39 and 42; H = 1024, I = 256, top 10 of
+// 512, T = 9 20 and 27, 13 23 and 31, 16 27 and 33.
+constexpr int kFp8StreamT = 13;
+
 size_t fp8_expert_ffn_workspace_bytes(int T, int K, int H, int I, int has_shared) {
   const size_t S = (size_t)T * K + (has_shared ? T : 0);
-  if (T <= kDecodeMaxT) return up256(S * I * sizeof(float));
+  if (T <= kFp8StreamT) return up256(S * I * sizeof(float));
   const size_t tiles = max_tiles(S, kPMaxG);
   return up256((size_t)T * H) + up256((size_t)T * (H / kQB) * sizeof(float)) + up256(S * I) +
          up256(tiles * (I / kQB) * kPM * sizeof(float)) + 16 * (tiles + 1);
@@ -812,9 +809,7 @@ size_t fp8_expert_ffn_workspace_bytes(int T, int K, int H, int I, int has_shared
 hipError_t launch_fp8_expert_ffn(const moe_fp8_weights& W, const uint16_t* x, int T, int K,
                                  const int32_t* offsets, const int32_t* sorted_slot,
                                  const int32_t* groups, uint16_t* y, void* ws, hipStream_t s) {
-  // the layer's own switch; measured (H = 2048, I = 512, top 10 of 512), streams
-  // against tiles: T = 9 57 and 61 us, T = 11 65 and 63 us, T = 16 81 and 75 us
-  if (T <= kDecodeMaxT)
+  if (T <= kFp8StreamT)
     return launch_fp8_stream_experts(W, x, T, K, offsets, sorted_slot, groups, (float*)ws, y, s);
   const size_t S = (size_t)T * K + (W.has_shared ? T : 0);
   const int G = W.E + W.has_shared;

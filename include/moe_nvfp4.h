@@ -481,11 +481,12 @@ int moe_block_norm_grad(const void* dr, const void* dn, const void* r_out, const
  * moe_fp8_quant writes the codes [T][K] and scales [T][ceil(K/128)] of rows x.
  *
  * moe_fp8_linear: out[t][n] = sum_b s[t][b] scales[n/128][b] sum_{k in b}
- * code_x[t][k] codes[n][k], f32 sums, one rounding to dtype.  Up to 16 rows
- * run as one launch that streams the weights once, unless N and K are both
- * large; else it is the quantisation and a tiled product.  The gradient by x is the same call with
- * the transposed matrix (codes^T, scales^T: blocks of 128 x 128 stay blocks,
- * so it is exact and is laid out once) on the gradient of out.
+ * code_x[t][k] codes[n][k], f32 sums of the exact products of codes, one
+ * rounding to dtype.  Up to 16 rows run as one launch that streams the weights
+ * once, unless N and K are both large; else it is the quantisation and a tiled
+ * product.  The gradient by x is the same call with the transposed matrix
+ * (codes^T, scales^T: blocks of 128 x 128 stay blocks, so it is exact and is laid
+ * out once) on the gradient of out.
  *
  *   x [T][K], out [T][N] of dtype
  *   ws  at least moe_fp8_linear_workspace_bytes(T, N, K) bytes (0: none needed)
@@ -523,7 +524,7 @@ int moe_fp8_linear(const moe_fp8_matrix* M, const void* x, int T, int dtype, voi
  *
  * with xq, hq the rows quantised as above (x [T][H] bf16, h not rounded in
  * between).  offsets, sorted_slot and groups are moe_permute's; y_slots goes to
- * moe_combine.  Up to 8 tokens the active experts' weights stream once, in
+ * moe_combine.  Up to 13 tokens the active experts' weights stream once, in
  * two launches; more run as the quantisation and two grouped products.
  *
  *   ws  at least moe_fp8_expert_ffn_workspace_bytes(T, K, H, I, has_shared)
