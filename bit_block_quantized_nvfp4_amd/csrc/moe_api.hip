@@ -123,6 +123,14 @@ bool sizes_ok_common(int T, int E, int K) {
          (long long)T * K <= (1LL << 30) && (long long)T * E <= (1LL << 40);
 }
 
+// Slots and positions are int32: T*K routed ones, then T shared ones.
+bool slots_ok(int T, int K, int has_shared) {
+  return (long long)T * (K + has_shared) <= INT32_MAX;
+}
+
+// HIP launches fewer than 2^32 threads.
+bool grid_ok(uint64_t threads) { return threads < (1ull << 32); }
+
 bool dtype_ok(int dt) { return dt >= MOE_DT_BF16 && dt <= MOE_DT_F32; }
 
 template <typename... P>
@@ -130,15 +138,19 @@ bool aligned16(const P*... p) {
   return ((((uintptr_t)p) & 15) | ...) == 0;
 }
 
-// Sizes of the sort entry points (each block of a grid covers 4 KB of a row
-// at most, so T * H bounds the grid).
+// Sizes of the sort entry points.
 int sort_sizes(const char* who, int T, int K, int H, int has_shared, int dtype) {
   if (!dtype_ok(dtype)) return fail(MOE_EUNSUPPORTED, "%s: unknown dtype %d", who, dtype);
   if (T < 1 || K < 1 || K > 32 || H < 8 || H > 65536 || H % 8 != 0 ||
-      (has_shared != 0 && has_shared != 1) || (long long)T * K > (1LL << 30) ||
-      (long long)T * H > (1LL << 40))
-    return fail(MOE_EINVAL, "%s: need T >= 1, 1 <= K <= 32, H a multiple of 8 in [8, 65536], has_shared in {0,1} (T=%d K=%d H=%d)", who, T, K, H);
+      (has_shared != 0 && has_shared != 1) || (long long)T * K > (1LL << 30))
+    return fail(MOE_EINVAL, "%s: need T >= 1, 1 <= K <= 32, T*K <= 2^30, H a multiple of 8 in [8, 65536], has_shared in {0,1} (T=%d K=%d H=%d)", who, T, K, H);
+  if (!slots_ok(T, K, has_shared))
+    return fail(MOE_EINVAL, "%s: T*(K + has_shared) must be below 2^31 (T=%d K=%d)", who, T, K);
   return MOE_OK;
+}
+
+int too_many_rows(const char* who, int T) {
+  return fail(MOE_EINVAL, "%s: T=%d takes a launch of 2^32 threads or more", who, T);
 }
 
 int launched(hipError_t e, const char* what) { return e == hipSuccess ? ok() : hip_fail(e, what); }
@@ -226,6 +238,8 @@ int moe_permute(const int32_t* ids, int T, int E, int K, int has_shared, int32_t
     return fail(MOE_EINVAL, "moe_permute: null pointer");
   if (!sizes_ok_common(T, E, K) || (has_shared != 0 && has_shared != 1))
     return fail(MOE_EINVAL, "moe_permute: need T >= 1, 1 <= K <= min(E, 32), E <= 1024, has_shared in {0,1}");
+  if (!slots_ok(T, K, has_shared))
+    return fail(MOE_EINVAL, "moe_permute: T*(K + has_shared) must be below 2^31 (T=%d K=%d)", T, K);
   const size_t need = moe::permute_workspace_bytes(T, E, K);
   if (need > 0 && (!ws || ws_bytes < need))
     return fail(MOE_EWORKSPACE, "moe_permute: workspace of %zu bytes needed, %zu given", need, ws_bytes);
@@ -369,6 +383,9 @@ int moe_combine(const uint16_t* y_slots, const float* w, const int32_t* slot_pos
   if (T < 1 || K < 1 || K > 32 || H < 8 || H % 8 != 0 || (has_shared != 0 && has_shared != 1) ||
       (long long)T * K > (1LL << 30))
     return fail(MOE_EINVAL, "moe_combine: need T >= 1, 1 <= K <= 32, H a positive multiple of 8, has_shared in {0,1}");
+  if (!slots_ok(T, K, has_shared))
+    return fail(MOE_EINVAL, "moe_combine: T*(K + has_shared) must be below 2^31 (T=%d K=%d)", T, K);
+  if (!grid_ok(moe::combine_threads(T, H))) return too_many_rows("moe_combine", T);
   int rc = ensure_init();
   if (rc != MOE_OK) return rc;
   hipError_t e = moe::launch_combine(y_slots, w, slot_pos, nullptr, T, K, H, has_shared, out,
@@ -382,6 +399,9 @@ int moe_combine_gated(const uint16_t* y_slots, const float* w, const int32_t* sl
     return fail(MOE_EINVAL, "moe_combine_gated: null pointer");
   if (T < 1 || K < 1 || K > 32 || H < 8 || H % 8 != 0 || (long long)T * K > (1LL << 30))
     return fail(MOE_EINVAL, "moe_combine_gated: need T >= 1, 1 <= K <= 32, H a positive multiple of 8");
+  if (!slots_ok(T, K, 1))
+    return fail(MOE_EINVAL, "moe_combine_gated: T*(K + 1) must be below 2^31 (T=%d K=%d)", T, K);
+  if (!grid_ok(moe::combine_threads(T, H))) return too_many_rows("moe_combine_gated", T);
   int rc = ensure_init();
   if (rc != MOE_OK) return rc;
   hipError_t e = moe::launch_combine(y_slots, w, slot_pos, gate, T, K, H, 1, out, (hipStream_t)stream);
@@ -412,6 +432,7 @@ int moe_dispatch(const void* x, const int32_t* slot_pos, int T, int K, int H, in
   if (!x || !slot_pos || !xs) return fail(MOE_EINVAL, "moe_dispatch: null pointer");
   int rc = sort_sizes("moe_dispatch", T, K, H, has_shared, dtype);
   if (rc != MOE_OK) return rc;
+  if (!grid_ok(moe::slot_rows_threads(T, H, dtype))) return too_many_rows("moe_dispatch", T);
   if (!aligned16((const char*)x, (const char*)xs))
     return fail(MOE_EINVAL, "moe_dispatch: rows must be aligned to 16 bytes");
   rc = ensure_init();
@@ -425,6 +446,7 @@ int moe_dispatch_grad(const void* dxs, const int32_t* slot_pos, int T, int K, in
   if (!dxs || !slot_pos || !dx) return fail(MOE_EINVAL, "moe_dispatch_grad: null pointer");
   int rc = sort_sizes("moe_dispatch_grad", T, K, H, has_shared, dtype);
   if (rc != MOE_OK) return rc;
+  if (!grid_ok(moe::slot_rows_threads(T, H, dtype))) return too_many_rows("moe_dispatch_grad", T);
   if (!aligned16((const char*)dxs, (const char*)dx))
     return fail(MOE_EINVAL, "moe_dispatch_grad: rows must be aligned to 16 bytes");
   rc = ensure_init();
@@ -440,6 +462,8 @@ int moe_combine_typed(const void* y_slots, const float* w, const int32_t* slot_p
   if (!y_slots || !w || !slot_pos || !out) return fail(MOE_EINVAL, "moe_combine_typed: null pointer");
   int rc = sort_sizes("moe_combine_typed", T, K, H, has_shared, dtype);
   if (rc != MOE_OK) return rc;
+  if (!grid_ok(dtype == MOE_DT_BF16 ? moe::combine_threads(T, H) : moe::slot_rows_threads(T, H, dtype)))
+    return too_many_rows("moe_combine_typed", T);
   if (gate && !has_shared)
     return fail(MOE_EINVAL, "moe_combine_typed: a shared-expert gate needs has_shared");
   if (!aligned16((const char*)y_slots, (const char*)out))
@@ -463,6 +487,8 @@ int moe_combine_grad(const void* dout, const void* y_slots, const float* w,
     return fail(MOE_EINVAL, "moe_combine_grad: null pointer");
   int rc = sort_sizes("moe_combine_grad", T, K, H, has_shared, dtype);
   if (rc != MOE_OK) return rc;
+  if (!grid_ok(moe::wave_rows_threads((long long)T * (K + has_shared))))
+    return too_many_rows("moe_combine_grad", T);
   if (gate && !has_shared)
     return fail(MOE_EINVAL, "moe_combine_grad: a shared-expert gate needs has_shared");
   if ((gate != nullptr) != (dgate != nullptr))
@@ -481,6 +507,7 @@ int moe_route_topk_grad(const int32_t* ids, const float* w, const float* dw, int
   if (!ids || !w || !dw || !dlogits) return fail(MOE_EINVAL, "moe_route_topk_grad: null pointer");
   if (!sizes_ok_common(T, E, K))
     return fail(MOE_EINVAL, "moe_route_topk_grad: need T >= 1, 1 <= K <= min(E, 32), E <= 1024 (T=%d E=%d K=%d)", T, E, K);
+  if (!grid_ok(moe::wave_rows_threads(T))) return too_many_rows("moe_route_topk_grad", T);
   int rc = ensure_init();
   if (rc != MOE_OK) return rc;
   return launched(moe::launch_topk_grad(ids, w, dw, T, E, K, dlogits, (hipStream_t)stream),
@@ -503,6 +530,7 @@ int moe_block_norm(const void* residual, const void* y, const void* gate, int ga
   if (!residual) return fail(MOE_EINVAL, "moe_block_norm: null pointer");
   int rc = norm_sizes("moe_block_norm", T, H, dtype, gate_kind);
   if (rc != MOE_OK) return rc;
+  if (!grid_ok(moe::block_norm_threads(T, H, dtype))) return too_many_rows("moe_block_norm", T);
   if ((gate_kind == MOE_GATE_NONE) != (gate == nullptr))
     return fail(MOE_EINVAL, "moe_block_norm: gate and gate_kind do not agree");
   if (!y && (gate || w_post || r_out || !w_pre))
@@ -575,6 +603,7 @@ int moe_fp8_quant(const void* x, int T, int K, int dtype, uint8_t* codes, float*
   if (!dtype_ok(dtype)) return fail(MOE_EUNSUPPORTED, "moe_fp8_quant: unknown dtype %d", dtype);
   if (!fp8_k_ok(T, K))
     return fail(MOE_EINVAL, "moe_fp8_quant: need 1 <= T <= 2^30 and K a multiple of 16 in [16, 65536] (T=%d K=%d)", T, K);
+  if (!grid_ok(moe::fp8_quant_threads(T, K))) return too_many_rows("moe_fp8_quant", T);
   if (!aligned16((const char*)x, codes))
     return fail(MOE_EINVAL, "moe_fp8_quant: rows must be aligned to 16 bytes");
   int rc = ensure_init();
@@ -598,6 +627,7 @@ int moe_fp8_linear(const moe_fp8_matrix* M, const void* x, int T, int dtype, voi
   if (!dtype_ok(dtype)) return fail(MOE_EUNSUPPORTED, "moe_fp8_linear: unknown dtype %d", dtype);
   if (!fp8_matrix_ok(T, M->N, M->K))
     return fail(MOE_EINVAL, "moe_fp8_linear: need 1 <= T <= 2^30, K a multiple of 16 in [16, 65536] and N a multiple of 8 in [8, 65536] (T=%d N=%d K=%d)", T, M->N, M->K);
+  if (!grid_ok(moe::fp8_linear_threads(T, M->N, M->K))) return too_many_rows("moe_fp8_linear", T);
   if (!aligned16((const char*)x, (const char*)out, M->codes, (const char*)ws))
     return fail(MOE_EINVAL, "moe_fp8_linear: codes, rows and workspace must be aligned to 16 bytes");
   const size_t need = moe::fp8_linear_workspace_bytes(T, M->N, M->K);
@@ -631,6 +661,7 @@ int moe_fp8_expert_ffn(const moe_fp8_weights* W, const uint16_t* x, int T, int K
     return fail(MOE_EINVAL, "moe_fp8_expert_ffn: need T >= 1, 1 <= K <= min(E, 32), E <= 1024, has_shared in {0,1}");
   if (!fp8_bank_ok(W->H, W->I) || (long long)T * W->H >= (1LL << 32))
     return fail(MOE_EINVAL, "moe_fp8_expert_ffn: need H and I multiples of 128 in [128, 8192] and T*H < 2^32 (T=%d H=%d I=%d)", T, W->H, W->I);
+  if (!grid_ok(moe::fp8_expert_ffn_threads(*W, T, K))) return too_many_rows("moe_fp8_expert_ffn", T);
   if (!aligned16((const char*)x, (const char*)y_slots, W->gu_codes, W->dn_codes, (const char*)ws))
     return fail(MOE_EINVAL, "moe_fp8_expert_ffn: codes, rows and workspace must be aligned to 16 bytes");
   const size_t need = moe::fp8_expert_ffn_workspace_bytes(T, K, W->H, W->I, W->has_shared);

@@ -436,6 +436,11 @@ void register_block_norm_kernels(std::vector<const void*>& k) {
   k.push_back((const void*)&k_norm_dw);
 }
 
+uint64_t block_norm_threads(int T, int H, int dtype) {
+  const int W = norm_waves(T, H * dtype_bytes(dtype) / 16, false);
+  return W == 1 ? wave_rows_threads(T) : (uint64_t)T * 64 * W;
+}
+
 hipError_t launch_block_norm(const void* res, const void* y, const void* gate, int gate_kind,
                              const float* w_post, const float* w_pre, float res_scale,
                              float out_scale, float eps, int T, int H, int dtype, void* r_out,

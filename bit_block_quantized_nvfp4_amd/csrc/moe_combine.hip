@@ -23,6 +23,11 @@ __global__ __launch_bounds__(256) void k_combine(const uint16_t* __restrict__ y,
 
 void register_combine_kernels(std::vector<const void*>& k) { k.push_back((const void*)&k_combine); }
 
+uint64_t combine_threads(int T, int H) {
+  const uint64_t here = ((uint64_t)T * (H / 8) + 255) / 256 * 256, there = slot_rows_threads(T, H, MOE_DT_BF16);
+  return here > there ? here : there;
+}
+
 hipError_t launch_combine(const uint16_t* y, const float* w, const int32_t* slot_pos,
                           const float* gate, int T, int K, int H, int has_shared, uint16_t* out,
                           hipStream_t s) {

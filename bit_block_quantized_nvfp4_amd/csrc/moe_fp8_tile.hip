@@ -744,6 +744,17 @@ static bool fp8_linear_streams(int T, int N, int K) {
   return N <= 4096 || K < 2048 || (long)N * K < 3L << 23;
 }
 
+uint64_t fp8_quant_threads(int T, int K) { return row_grid_threads(T, blocks_of(K) * 16); }
+
+uint64_t fp8_linear_threads(int T, int N, int K) {
+  if (fp8_linear_streams(T, N, K)) return 0;  // at most 65536 / 16 blocks
+  uint64_t t = fp8_quant_threads(T, K);
+  by_linear_tile<MOE_DT_BF16>(linear_tile<MOE_DT_BF16>(T, N), [&](auto, int bn, int bm, int threads) {
+    t = std::max(t, (uint64_t)((N + bn - 1) / bn) * ((T + bm - 1) / bm) * threads);
+  });
+  return t;
+}
+
 size_t fp8_linear_workspace_bytes(int T, int N, int K) {
   if (fp8_linear_streams(T, N, K)) return 0;
   return up256((size_t)T * blocks_of(K) * kQB) +
@@ -804,6 +815,15 @@ size_t fp8_expert_ffn_workspace_bytes(int T, int K, int H, int I, int has_shared
   const size_t tiles = max_tiles(S, kPMaxG);
   return up256((size_t)T * H) + up256((size_t)T * (H / kQB) * sizeof(float)) + up256(S * I) +
          up256(tiles * (I / kQB) * kPM * sizeof(float)) + 16 * (tiles + 1);
+}
+
+uint64_t fp8_expert_ffn_threads(const moe_fp8_weights& W, int T, int K) {
+  if (T <= kFp8StreamT) return 0;  // at most 13 * 32 + 1 groups
+  const size_t S = (size_t)T * K + (W.has_shared ? T : 0), mt = max_tiles(S, W.E + W.has_shared);
+  const int ngu = W.I / 128, ndn = W.H / 128, G = W.E + W.has_shared;
+  return std::max({(uint64_t)mt * (ngu / tiles_per_block(S, G, ngu)) * 512,
+                   (uint64_t)mt * (ndn / tiles_per_block(S, G, ndn)) * 256,
+                   row_grid_threads(T, W.H / kQB * 16) + 256});
 }
 
 hipError_t launch_fp8_expert_ffn(const moe_fp8_weights& W, const uint16_t* x, int T, int K,

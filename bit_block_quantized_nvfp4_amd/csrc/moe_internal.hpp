@@ -136,6 +136,15 @@ hipError_t launch_decode_ffn(const moe_nvfp4_weights& W, const uint16_t* x, int 
                              const int32_t* groups, int act_mode, uint16_t* hbuf, uint8_t* xq,
                              float* xs, uint16_t* y, hipStream_t s);
 
+// Threads that the entry points' largest launches take.
+uint64_t combine_threads(int T, int H);
+uint64_t slot_rows_threads(int T, int H, int dtype);
+inline uint64_t wave_rows_threads(long long rows) { return ((uint64_t)rows + 3) / 4 * 256; }
+uint64_t block_norm_threads(int T, int H, int dtype);
+uint64_t fp8_quant_threads(int T, int K);
+uint64_t fp8_linear_threads(int T, int N, int K);
+uint64_t fp8_expert_ffn_threads(const moe_fp8_weights& W, int T, int K);
+
 // Token sort and its gradients (moe_sort.hip).
 void register_sort_kernels(std::vector<const void*>& k);
 hipError_t launch_dispatch(const void* x, const int32_t* slot_pos, int T, int K, int H,

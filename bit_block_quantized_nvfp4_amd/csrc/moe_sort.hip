@@ -23,7 +23,7 @@
 namespace moe {
 
 // Limit of the positions a slot may have: routed slots sort below T*K, the
-// shared slots after the routed ones.
+// shared slots after the routed ones, below T*K + T (which fits an int).
 __device__ __forceinline__ bool slot_ok(int p, int lim) { return p >= 0 && p < lim; }
 
 // One thread per 16-byte chunk of one token's row (cpr chunks a row, whatever
@@ -214,6 +214,10 @@ void register_sort_kernels(std::vector<const void*>& k) {
       k.push_back((const void*)&k_combine_grad<decltype(D)::value, false>);
       k.push_back((const void*)&k_combine_grad<decltype(D)::value, true>);
     });
+}
+
+uint64_t slot_rows_threads(int T, int H, int dtype) {
+  return row_grid_threads(T, H * dtype_bytes(dtype) / 16);
 }
 
 hipError_t launch_dispatch(const void* x, const int32_t* slot_pos, int T, int K, int H,

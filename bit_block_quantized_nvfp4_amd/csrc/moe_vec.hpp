@@ -105,5 +105,9 @@ inline RowGrid row_grid(int T, int cpr) {
   g.blocks = blocks(T, 256 >> g.lg) * (unsigned)g.cb;
   return g;
 }
+inline uint64_t row_grid_threads(int T, int cpr) {
+  const RowGrid g = row_grid(1, cpr);
+  return (uint64_t)blocks(T, 256 >> g.lg) * (uint64_t)g.cb * 256;
+}
 
 }  // namespace moe

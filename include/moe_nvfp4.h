@@ -409,8 +409,11 @@ int moe_combine_gated(const uint16_t* y_slots, const float* w, const int32_t* sl
  * A routed slot whose slot_pos lies outside [0, T*K), or a shared one outside
  * [0, T*K + T), is skipped: it adds nothing, its dw is 0 and its dgate 0, and
  * rows of xs and dy_slots that no slot points at are left as they were.
- * Limits: 1 <= K <= 32, H a multiple of 8 in [8, 65536], row pointers aligned
- * to 16 bytes.  The outputs may not overlap the inputs.
+ * Limits: 1 <= K <= 32, T*K <= 2^30, T*(K + has_shared) < 2^31, H a multiple of 8
+ * in [8, 65536], row pointers aligned to 16 bytes, and launches of fewer than
+ * 2^32 threads: one per 16 bytes of a token's row (rounded up to a power of two of
+ * them, or to 4 KB for longer rows), moe_combine_grad 64 per slot and
+ * moe_route_topk_grad 64 per token.  The outputs may not overlap the inputs.
  */
 int moe_dispatch(const void* x, const int32_t* slot_pos, int T, int K, int H, int has_shared,
                  int dtype, void* xs, void* stream);
@@ -455,7 +458,9 @@ int moe_route_topk_grad(const int32_t* ids, const float* w, const float* dw, int
  *
  * The sums over the tokens of dw_post and dw_pre are f32, split and joined in
  * an order that T and H alone determine.  Limits: H a multiple of 8 in
- * [8, 8192], all row and weight pointers aligned to 16 bytes, eps >= 0.
+ * [8, 8192], all row and weight pointers aligned to 16 bytes, eps >= 0, T <= 2^30,
+ * and for moe_block_norm launches of fewer than 2^32 threads: 64 a row, 256 from
+ * more than 4 KB a row, 512 from more than 16 KB.
  * Except r_out on residual, outputs may not overlap inputs.
  */
 int moe_block_norm(const void* residual, const void* y, const void* gate, int gate_kind,
@@ -493,8 +498,11 @@ int moe_block_norm_grad(const void* dr, const void* dn, const void* r_out, const
  *
  * A NaN or an infinity in a row makes that row's outputs NaN and no others.
  * The outputs may not overlap the inputs.
- * Limits: K a multiple of 16, N a multiple of 8, both in [16, 65536] and
- * [8, 65536]; pointers of codes, x and out aligned to 16 bytes.
+ * Limits: K a multiple of 16, N a multiple of 8, in [16, 65536] and [8, 65536];
+ * T <= 2^30, and launches of fewer than 2^32 threads: for the quantisation one per
+ * 8 values of a row of K rounded up to 128 (and to a power of two up to 2048, to
+ * multiples of 2048 beyond), for the product at most N * T / 32; pointers of
+ * codes, x and out aligned to 16 bytes.
  */
 typedef struct moe_fp8_matrix {
   const uint8_t* codes;
