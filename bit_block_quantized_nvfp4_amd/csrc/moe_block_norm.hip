@@ -53,8 +53,6 @@ __device__ __forceinline__ void load_w(const float* __restrict__ w, int c, float
   }
 }
 
-__device__ __forceinline__ float sigmoid_f32(float g) { return 1.0f / (1.0f + expf(-g)); }
-
 struct NormFwd {
   const u32x4* res;
   const u32x4* y;       // NULL: r' = res, not written
@@ -261,8 +259,12 @@ __global__ __launch_bounds__(64 * W * R) void k_block_norm_grad(NormBwd a) {
       continue;
     }
     const float rstd = !on ? 0.f : a.w_post ? a.rstd_post[t] : 1.f;
-    float sg = 1.f;
-    if (a.gate_kind == MOE_GATE_TOKEN) sg = sigmoid_f32(((const float*)a.gate)[t]);
+    float sg = 1.f, sg_rest = 0.f;
+    if (a.gate_kind == MOE_GATE_TOKEN) {
+      const float g = ((const float*)a.gate)[t];
+      sg = sigmoid_f32(g);
+      sg_rest = sigmoid_rest_f32(g);
+    }
     // D becomes b D, then du w_post = b c D w_post; s sums that times yh,
     // which is <b c D, u>, also the token gate's gradient up to (1 - c)
     float s = 0.f;
@@ -288,7 +290,7 @@ __global__ __launch_bounds__(64 * W * R) void k_block_norm_grad(NormBwd a) {
           for (int j = 0; j < N; ++j) {
             const float c1 = sigmoid_f32(gt[j]);
             D[i][j] *= c1;
-            o[j] = D[i][j] * yh[i][j] * wp[j] * (1.f - c1);
+            o[j] = D[i][j] * yh[i][j] * wp[j] * sigmoid_rest_f32(gt[j]);
           }
           ((u32x4*)a.dgate)[base + c] = Chunk<DT>::pack(o);
         } else {
@@ -306,7 +308,7 @@ __global__ __launch_bounds__(64 * W * R) void k_block_norm_grad(NormBwd a) {
     float m = 0.f;
     if (a.w_post || a.gate_kind == MOE_GATE_TOKEN) {
       s = row_sum<W>(s, red[1][grp]);
-      if (a.gate_kind == MOE_GATE_TOKEN && lane == 0 && on) ((float*)a.dgate)[t] = (1.f - sg) * s;
+      if (a.gate_kind == MOE_GATE_TOKEN && lane == 0 && on) ((float*)a.dgate)[t] = sg_rest * s;
       if (a.w_post) m = s * inv_h;
     }
 #pragma unroll

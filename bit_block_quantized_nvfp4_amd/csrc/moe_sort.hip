@@ -91,7 +91,7 @@ __global__ __launch_bounds__(256) void k_slot_sum(const u32x4* __restrict__ y,
     }
   }
   if (slot_ok(ps, TK + T)) {
-    const float sg = gate ? 1.0f / (1.0f + expf(-gate[t])) : 1.0f;
+    const float sg = gate ? sigmoid_f32(gate[t]) : 1.0f;
     float f[N];
     Chunk<DT>::unpack(y[(size_t)ps * cpr + c], f);
 #pragma unroll
@@ -119,9 +119,12 @@ __global__ __launch_bounds__(256) void k_combine_grad(
   const bool shared = k == K;
   const int p = shared ? slot_pos[(size_t)TK + t] : slot_pos[(size_t)t * K + k];
   const bool on = slot_ok(p, shared ? TK + T : TK);
-  float wt = 1.f;
+  float wt = 1.f, rest = 0.f;
   if (!shared) wt = w[(size_t)t * K + k];
-  else if (gate) wt = 1.0f / (1.0f + expf(-gate[t]));
+  else if (gate) {
+    wt = sigmoid_f32(gate[t]);
+    rest = sigmoid_rest_f32(gate[t]);
+  }
   float dot = 0.f;
   if (on) {
     const u32x4* dr = dout + (size_t)t * cpr;
@@ -158,7 +161,7 @@ __global__ __launch_bounds__(256) void k_combine_grad(
   dot = wave_sum_dpp(dot);
   if (lane == 0) {
     if (!shared) dw[(size_t)t * K + k] = dot;
-    else if (gate) dgate[t] = wt * (1.f - wt) * dot;
+    else if (gate) dgate[t] = wt * rest * dot;
   }
 }
 

@@ -3,6 +3,8 @@
 // 4 of f32.  Arithmetic is in f32; store() rounds once, to nearest even.
 #pragma once
 
+#include <math.h>
+
 #include "../../include/moe_nvfp4.h"
 #include "moe_device.hpp"
 
@@ -63,6 +65,11 @@ struct Chunk<MOE_DT_F32> {
     return v;
   }
 };
+
+// c = sigmoid(g) and 1 - c, each to a few units of its last place: 1 - c taken from
+// c would lose its bits for a positive g (all of them from 17.4 on).
+__device__ __forceinline__ float sigmoid_f32(float g) { return 1.0f / (1.0f + expf(-g)); }
+__device__ __forceinline__ float sigmoid_rest_f32(float g) { return 1.0f / (1.0f + expf(g)); }
 
 // Host side: bytes of one element of a moe_dtype, and the call of a generic
 // lambda with the type as a compile-time constant.

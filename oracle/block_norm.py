@@ -64,7 +64,8 @@ def grad(dr, dn, r, y, gate, w_post, w_pre, rstd_post, rstd_pre, a, b, magnitude
     wp = m(w_post) if w_post is not None else np.ones(y.shape[1])
     bD = abs(b) * D if magnitudes else b * D
     if gate is not None:
-        full = c * (1 - c) * bD * yh * wp
+        rest = _gate(-np.asarray(gate, dtype=np.float64), y.shape)  # 1 - c, without cancellation
+        full = c * rest * bD * yh * wp
         out["dgate"] = full.sum(axis=1) if np.ndim(gate) == 1 else full
     du = bD * c
     if w_post is None:

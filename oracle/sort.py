@@ -69,8 +69,9 @@ def combine_grad(dout, y, w, slot_pos, K, has_shared, gate, dy):
             dw[t, k] = np.dot(dout[t], y[p])
             mw[t, k] = np.dot(np.abs(dout[t]), np.abs(y[p]))
         elif gate is not None:
-            dg[t] = c * (1 - c) * np.dot(dout[t], y[p])
-            mg[t] = c * (1 - c) * np.dot(np.abs(dout[t]), np.abs(y[p]))
+            slope = c * float(sigmoid(-np.float64(gate[t])))  # c (1 - c), without cancellation
+            dg[t] = slope * np.dot(dout[t], y[p])
+            mg[t] = slope * np.dot(np.abs(dout[t]), np.abs(y[p]))
     return dy, dw, dg, mw, mg
 
 
