@@ -31,12 +31,20 @@ uint64_t combine_threads(int T, int H) {
 hipError_t launch_combine(const uint16_t* y, const float* w, const int32_t* slot_pos,
                           const float* gate, int T, int K, int H, int has_shared, uint16_t* out,
                           hipStream_t s) {
-  // Many rows go to the typed operators' kernel, which gives the same bits: a wave
-  // there has one token, whose positions are scalar loads (K = 10 + 1, H = 2048,
-  // in a row in a graph: T = 4096 33.0 us, here 37.2 us; T = 1024 10.5 and 11.0
-  // us, T = 256 5.8 and 5.3 us; 33 MB of rows 12.9 and 14.6 us).
+  // Rows that the 256 MB last-level cache does not hold go to the typed operators'
+  // kernel, which gives the same bits and reads past the caches, unless more than
+  // a quarter of its threads would stand idle behind the row's end (it gives a row
+  // 2^n threads, or a multiple of 256).  In a row in a graph, us, here and there:
+  //                      184 MB         300 MB         600 MB
+  //   H = 2048, K = 10   32.4   37.3    68.6   58.9   133.5  114.9
+  //   H = 2048, K = 2    47.2   48.6   107.5   76.7   210.9  172.1
+  //   H = 768, K = 10    32.7   38.9    69.0   61.8   134.5  120.4  (3/4 in use)
+  //   H = 768, K = 2     50.7   61.1   110.4   98.5   218.1  208.5
+  //   H = 2560, K = 10   32.7   43.1    67.6   69.3   133.2  136.5  (5/8 in use)
+  //   H = 2560, K = 2    48.1   70.8   108.8  113.8   214.3  241.2
   const size_t bytes = (size_t)T * (K + has_shared) * H * sizeof(uint16_t);
-  if (bytes >= (size_t)32 << 20)
+  const uint64_t there = slot_rows_threads(T, H, MOE_DT_BF16), used = (uint64_t)T * (H / 8);
+  if (bytes > (size_t)256 << 20 && 4 * used >= 3 * there)
     return launch_slot_sum(y, w, slot_pos, gate, T, K, H, has_shared, MOE_DT_BF16, out, s);
   const long n = (long)T * (H / 8);
   MOE_LAUNCH("combine", s, k_combine, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, y, w,
