@@ -391,8 +391,8 @@ __global__ __launch_bounds__(256) void k_norm_dw(const float* __restrict__ part,
   if (h < H) (which ? dw_pre : dw_post)[h] = r;
 }
 
-// Waves to a row: one wave holds up to 256 chunks, four up to 1024, eight up
-// to 2048.  From 65 chunks on four waves share a row where rows are few, since
+// Waves to a row: one wave holds up to 256 chunks, four up to 1024 (the widest
+// rows of 16 bits), eight up to 2048 (f32).  From 65 chunks on four waves share a row where rows are few, since
 // the latency of a row counts then, and backward, whose registers leave one
 // wave a row too few rows in flight (T = 8191, H = 2048: 47 us, one wave 52 us;
 // forward at T = 32768 one wave 124 us, four 140 us).
@@ -403,11 +403,13 @@ static int norm_waves(int T, int cpr, bool grad) {
 }
 
 // f with the chunks per thread and the waves to a row.
-template <bool GRAD, typename F>
+template <int DT, bool GRAD, typename F>
 static void by_shape(int T, int cpr, F&& f) {
   const int W = norm_waves(T, cpr, GRAD);
-  if (W == 8) f(IntC<4>{}, IntC<8>{});
-  else if (W == 4 && cpr <= 256) f(IntC<1>{}, IntC<4>{});
+  if constexpr (DT == MOE_DT_F32) {
+    if (W == 8) return f(IntC<4>{}, IntC<8>{});
+  }
+  if (W == 4 && cpr <= 256) f(IntC<1>{}, IntC<4>{});
   else if (W == 4) f(IntC<4>{}, IntC<4>{});
   else if (GRAD || cpr <= 64) f(IntC<1>{}, IntC<1>{});
   else if constexpr (!GRAD) f(IntC<4>{}, IntC<1>{});
@@ -432,7 +434,7 @@ void register_block_norm_kernels(std::vector<const void*>& k) {
     one(IntC<4>{}, IntC<1>{});
     one(IntC<1>{}, IntC<4>{});
     one(IntC<4>{}, IntC<4>{});
-    one(IntC<4>{}, IntC<8>{});
+    if constexpr (DT == MOE_DT_F32) one(IntC<4>{}, IntC<8>{});
   };
   for (int dt = MOE_DT_BF16; dt <= MOE_DT_F32; ++dt) by_dtype(dt, add);
   k.push_back((const void*)&k_norm_dw);
@@ -454,7 +456,7 @@ hipError_t launch_block_norm(const void* res, const void* y, const void* gate, i
                   gate_kind};
   by_dtype(dtype, [&](auto D) {
     constexpr int DT = decltype(D)::value;
-    by_shape<false>(T, cpr, [&](auto NC, auto W) {
+    by_shape<DT, false>(T, cpr, [&](auto NC, auto W) {
       constexpr int w = decltype(W)::value;
       MOE_LAUNCH("block_norm", s, (k_block_norm<DT, decltype(NC)::value, w>),
                  dim3(w == 1 ? (T + 3) / 4 : T), dim3(w == 1 ? 256 : 64 * w), 0, s, a);
@@ -495,7 +497,7 @@ hipError_t launch_block_norm_grad(const void* dr, const void* dn, const void* r_
                   H,                cpr,              gate_kind};
   by_dtype(dtype, [&](auto D) {
     constexpr int DT = decltype(D)::value;
-    by_shape<true>(T, cpr, [&](auto NC, auto W) {
+    by_shape<DT, true>(T, cpr, [&](auto NC, auto W) {
       constexpr int w = decltype(W)::value;
       constexpr int r = grad_rows(decltype(NC)::value, w);
       MOE_LAUNCH("block_norm_grad", s, (k_block_norm_grad<DT, decltype(NC)::value, w, r>), dim3(P),
