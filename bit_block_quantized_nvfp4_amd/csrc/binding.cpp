@@ -150,11 +150,12 @@ Tensor scratch(const Tensor* t, size_t bytes, c10::Device dev) {
   return *t;
 }
 
-// Tokens of a permutation with K routed slots (and a shared one) each.
+// Tokens of a permutation with K routed slots (and a shared one) each.  None is
+// for the library to refuse, as every size is.
 int tokens(const Tensor& slot_pos, int K, bool shared) {
   const int64_t per = (int64_t)K + shared, n = slot_pos.numel();
-  if (K < 1 || n == 0 || n % per)
-    refuse("slot_pos has ", n, " entries, not a positive multiple of ", per, " slots a token");
+  if (K < 1 || n % per)
+    refuse("slot_pos has ", n, " entries, not a multiple of ", per, " slots a token");
   if (n / per > INT32_MAX) refuse("slot_pos is too long");
   return (int)(n / per);
 }
