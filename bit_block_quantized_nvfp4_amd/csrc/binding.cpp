@@ -168,6 +168,17 @@ int size32(int64_t v, const char* name) {
 void* stream() { return (void*)c10::hip::getCurrentHIPStream().stream(); }
 void* ptr(const Tensor* t) { return t ? t->data_ptr() : nullptr; }
 
+// One call of the C ABI, without the interpreter's lock: a launch may have to wait
+// (a full queue, the first call's kernel lookup), and other Python threads go on
+// meanwhile, as they do through ctypes.  The caller's frame holds the arguments.
+template <typename F, typename... A>
+int call(F f, A... a) {
+  PyThreadState* const s = PyEval_SaveThread();
+  const int status = f(a...);
+  PyEval_RestoreThread(s);
+  return status;
+}
+
 void check(int status) {
   if (status >= 0) return;
   PyObject* e = PyObject_CallFunction(g_moe_error, "is", status, moe_last_error());
@@ -202,7 +213,7 @@ PyObject* dispatch(Args a) {
   need(x, x.scalar_type(), {T, H}, dev, "x");
   need(pos, at::kInt, {S}, dev, "slot_pos");
   Tensor xs = output(given, x.scalar_type(), {S, H}, dev, "xs");
-  check(moe_dispatch(x.data_ptr(), pos.data_ptr<int32_t>(), T, K, size32(H, "H"), sh, dt,
+  check(call(moe_dispatch, x.data_ptr(), pos.data_ptr<int32_t>(), T, K, size32(H, "H"), sh, dt,
                      xs.data_ptr(), stream()));
   return wrap(xs);
 }
@@ -220,7 +231,7 @@ PyObject* dispatch_grad(Args a) {
   need(dxs, dxs.scalar_type(), {S, H}, dev, "dxs");
   need(pos, at::kInt, {S}, dev, "slot_pos");
   Tensor dx = output(given, dxs.scalar_type(), {T, H}, dev, "dx");
-  check(moe_dispatch_grad(dxs.data_ptr(), pos.data_ptr<int32_t>(), T, K, size32(H, "H"), sh, dt,
+  check(call(moe_dispatch_grad, dxs.data_ptr(), pos.data_ptr<int32_t>(), T, K, size32(H, "H"), sh, dt,
                           dx.data_ptr(), stream()));
   return wrap(dx);
 }
@@ -246,12 +257,12 @@ PyObject* combine(Args a) {
   Tensor out = output(given, y.scalar_type(), {T, H}, dev, "out");
   const int h = size32(H, "H");
   if (dt != MOE_DT_BF16)
-    check(moe_combine_typed(y.data_ptr(), wp, pp, gp, T, K, h, sh, dt, out.data_ptr(), stream()));
+    check(call(moe_combine_typed, y.data_ptr(), wp, pp, gp, T, K, h, sh, dt, out.data_ptr(), stream()));
   else if (gp)
-    check(moe_combine_gated((const uint16_t*)y.data_ptr(), wp, pp, gp, T, K, h,
+    check(call(moe_combine_gated, (const uint16_t*)y.data_ptr(), wp, pp, gp, T, K, h,
                             (uint16_t*)out.data_ptr(), stream()));
   else
-    check(moe_combine((const uint16_t*)y.data_ptr(), wp, pp, T, K, h, sh,
+    check(call(moe_combine, (const uint16_t*)y.data_ptr(), wp, pp, T, K, h, sh,
                       (uint16_t*)out.data_ptr(), stream()));
   return wrap(out);
 }
@@ -285,7 +296,7 @@ PyObject* combine_grad(Args a) {
   }
   Tensor dy = output(dy_given, type, {S, H}, dev, "dy_slots");
   Tensor dw = output(dw_given, at::kFloat, {T, K}, dev, "dw");
-  check(moe_combine_grad(dout.data_ptr(), y.data_ptr(), w.data_ptr<float>(),
+  check(call(moe_combine_grad, dout.data_ptr(), y.data_ptr(), w.data_ptr<float>(),
                          pos.data_ptr<int32_t>(), (const float*)ptr(gate), T, K, size32(H, "H"),
                          sh, dt, dy.data_ptr(), dw.data_ptr<float>(),
                          gate ? dgate.data_ptr<float>() : nullptr, stream()));
@@ -306,7 +317,7 @@ PyObject* route_topk_grad(Args a) {
   need(w, at::kFloat, {T, K}, dev, "w");
   need(dw, at::kFloat, {T, K}, dev, "dw");
   Tensor dz = output(given, at::kFloat, {T, E}, dev, "dlogits");
-  check(moe_route_topk_grad(ids.data_ptr<int32_t>(), w.data_ptr<float>(), dw.data_ptr<float>(), T,
+  check(call(moe_route_topk_grad, ids.data_ptr<int32_t>(), w.data_ptr<float>(), dw.data_ptr<float>(), T,
                             E, K, dz.data_ptr<float>(), stream()));
   return wrap(dz);
 }
@@ -361,7 +372,7 @@ PyObject* block_norm(Args a) {
   } else if (n_given || sn_given) {
     refuse("n_out or rstd_pre is given without w_pre");
   }
-  check(moe_block_norm(res.data_ptr(), ptr(y), ptr(gate), kind, (const float*)ptr(w_post),
+  check(call(moe_block_norm, res.data_ptr(), ptr(y), ptr(gate), kind, (const float*)ptr(w_post),
                        (const float*)ptr(w_pre), res_scale, out_scale, eps, T, H, dt,
                        y ? r.data_ptr() : nullptr, w_pre ? n.data_ptr() : nullptr,
                        w_post ? sp.data_ptr<float>() : nullptr,
@@ -419,7 +430,8 @@ PyObject* block_norm_grad(Args a) {
   dres = output(nullptr, type, shape, dev, "dresidual");
   const size_t bytes = moe_block_norm_workspace_bytes(T, H, dt);
   Tensor ws = scratch(ws_given, bytes, dev);
-  check(moe_block_norm_grad(
+  check(call(
+      moe_block_norm_grad,
       ptr(dr), ptr(dn), r.data_ptr(), ptr(y), ptr(gate), kind, (const float*)ptr(w_post),
       (const float*)ptr(w_pre), (const float*)ptr(sp), (const float*)ptr(sn), res_scale, out_scale,
       T, H, dt, dres.data_ptr(), y ? dy.data_ptr() : nullptr, gate ? dgate.data_ptr() : nullptr,
@@ -447,7 +459,7 @@ PyObject* fp8_quant(Args a) {
   need(x, x.scalar_type(), {T, K}, dev, "x");
   Tensor codes = output(codes_given, at::kFloat8_e4m3fn, {T, K}, dev, "codes");
   Tensor scales = output(scales_given, at::kFloat, {T, blocks128(K)}, dev, "scales");
-  check(moe_fp8_quant(x.data_ptr(), T, K, dt, (uint8_t*)codes.data_ptr(),
+  check(call(moe_fp8_quant, x.data_ptr(), T, K, dt, (uint8_t*)codes.data_ptr(),
                       scales.data_ptr<float>(), stream()));
   return wrap_all({codes, scales});
 }
@@ -475,7 +487,7 @@ PyObject* fp8_linear(Args a) {
   const size_t bytes = moe_fp8_linear_workspace_bytes(T, N, K);
   Tensor ws;
   if (bytes) ws = scratch(ws_given, bytes, dev);
-  check(moe_fp8_linear(&M, x.data_ptr(), T, dt, out.data_ptr(), bytes ? ws.data_ptr() : nullptr,
+  check(call(moe_fp8_linear, &M, x.data_ptr(), T, dt, out.data_ptr(), bytes ? ws.data_ptr() : nullptr,
                        bytes, stream()));
   return wrap(out);
 }
@@ -515,7 +527,7 @@ PyObject* fp8_expert_ffn(Args a) {
   Tensor y = output(given, at::kBFloat16, {S, H}, dev, "y_slots");
   const size_t bytes = moe_fp8_expert_ffn_workspace_bytes(T, K, H, I, sh);
   Tensor ws = scratch(ws_given, bytes, dev);
-  check(moe_fp8_expert_ffn(&W, (const uint16_t*)x.data_ptr(), T, K, offsets.data_ptr<int32_t>(),
+  check(call(moe_fp8_expert_ffn, &W, (const uint16_t*)x.data_ptr(), T, K, offsets.data_ptr<int32_t>(),
                            slots.data_ptr<int32_t>(), groups.data_ptr<int32_t>(),
                            (uint16_t*)y.data_ptr(), ws.data_ptr(), bytes, stream()));
   return wrap(y);

@@ -1,5 +1,8 @@
 """How the compiled marshalling behaves towards torch and Python: errors of the
 library, other threads, outputs that torch can see, devices."""
+import threading
+import time
+
 import pytest
 import torch
 
@@ -24,3 +27,54 @@ def test_an_empty_batch_is_the_librarys_error(moe):
         with pytest.raises(err) as e:
             call()
         assert e.value.status == moe.ops._lib.MOE_EINVAL
+
+
+def test_a_call_that_waits_lets_other_threads_run(moe):
+    """moe_timing_read holds the timing lock until the work before it is done; a call
+    that waits for that lock must not hold the interpreter's."""
+    x = torch.randn(8, 64, device="cuda").bfloat16()
+    pos = torch.arange(16, dtype=torch.int32, device="cuda")
+    y, w = moe.moe_dispatch(x, pos, 2, False), torch.rand(8, 2, device="cuda")
+    want = moe.moe_combine(y, w, pos, 2, False)
+    # a spin of about 0.4 s, by a short one's measure
+    ends = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    torch.cuda._sleep(1000)
+    ends[0].record()
+    torch.cuda._sleep(100000)
+    ends[1].record()
+    torch.cuda.synchronize()
+    cycles = int(100000 * 400 / max(ends[0].elapsed_time(ends[1]), 1e-2))
+    flush(f"spin of {cycles} cycles")
+
+    from bit_block_quantized_nvfp4_amd import ops
+    stop, ticks = threading.Event(), []
+
+    def tick():
+        while not stop.is_set():
+            ticks.append(time.perf_counter())
+            time.sleep(0.002)
+
+    ops.timing_reset()
+    ops.timing_enable(True)
+    try:
+        torch.cuda._sleep(cycles)
+        moe.moe_combine(y, w, pos, 2, False)          # its end is the spin's
+        reader, ticker = threading.Thread(target=ops.timing_read), threading.Thread(target=tick)
+        ticker.start()
+        reader.start()
+        time.sleep(0.05)                              # the reader has the lock
+        a = time.perf_counter()
+        out = moe.moe_combine(y, w, pos, 2, False)
+        b = time.perf_counter()
+        stop.set()
+        reader.join()
+        ticker.join()
+    finally:
+        stop.set()
+        ops.timing_enable(False)
+        ops.timing_reset()
+    torch.cuda.synchronize()
+    during = sum(a < t < b for t in ticks)
+    flush(f"the call took {b - a:.3f} s, {during} ticks meanwhile")
+    assert torch.equal(out, want)
+    assert b - a > 0.1 and during >= 10
