@@ -8,7 +8,6 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
-#include <ATen/hip/EmptyTensor.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -129,11 +128,10 @@ void* need(const Tensor& t, ScalarType type, Shape shape, c10::Device dev, const
   return t.data_ptr();
 }
 
-// A new tensor, straight from the device's allocator: at::empty takes a quarter
-// of a microsecond longer to get there (block_norm with four of them 6.8 us a
-// call, so 6.0 us).
+// A new tensor, as torch.empty makes it: dispatch modes see it, and torch fills it
+// where deterministic algorithms ask for that.
 Tensor fresh(ScalarType type, Shape shape, c10::Device dev) {
-  return Tensor(at::detail::empty_cuda(shape, type, dev, std::nullopt));
+  return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
 }
 
 // An output: the one given, checked, or a new one.

@@ -5,6 +5,7 @@ import time
 
 import pytest
 import torch
+from torch.utils._python_dispatch import TorchDispatchMode
 
 from _gpu import flush, setup
 
@@ -78,3 +79,32 @@ def test_a_call_that_waits_lets_other_threads_run(moe):
     flush(f"the call took {b - a:.3f} s, {during} ticks meanwhile")
     assert torch.equal(out, want)
     assert b - a > 0.1 and during >= 10
+
+
+def test_torch_sees_new_outputs(moe):
+    """Through torch's dispatcher: a dispatch mode meets them, and where deterministic
+    algorithms are asked for, rows that a call leaves as they were are filled."""
+    T, K, H = 6, 2, 64
+    x = torch.randn(T, H, device="cuda").bfloat16()
+    pos = torch.arange(T * K, dtype=torch.int32, device="cuda")
+    y, w = moe.moe_dispatch(x, pos, K, False), torch.rand(T, K, device="cuda")
+
+    class Seen(TorchDispatchMode):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            names.append(str(func))
+            return func(*args, **(kwargs or {}))
+
+    names = []
+    with Seen():
+        out = moe.moe_combine(y, w, pos, K, False)
+    assert any("empty" in n for n in names), names
+    assert torch.equal(out, moe.moe_combine(y, w, pos, K, False))
+
+    pos[3] = -1
+    before = torch.are_deterministic_algorithms_enabled()
+    torch.use_deterministic_algorithms(True)
+    try:
+        xs = moe.moe_dispatch(x, pos, K, False)
+    finally:
+        torch.use_deterministic_algorithms(before)
+    assert torch.isnan(xs[3]).all() and not torch.isnan(xs[[0, 1, 2, 4]]).any()
