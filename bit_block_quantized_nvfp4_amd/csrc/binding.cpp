@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -97,13 +98,13 @@ struct Args {
   }
 };
 
-// t's device, which has to be the current one: the kernels go to its stream.
+// t's device.  A call makes it the current one while it lasts (OnDevice): outputs
+// and kernels go there, to that device's current stream.
 c10::Device device_of(const Tensor& t, const char* name) {
   if (!t.is_cuda()) refuse(name, " must be a device tensor");
-  if (t.device().index() != c10::hip::current_device())
-    refuse(name, " is on ", t.device().str(), ", not on the current device");
   return t.device();
 }
+using OnDevice = c10::DeviceGuard;
 
 int dtype_of(const Tensor& t, const char* name) {
   switch (t.scalar_type()) {
@@ -205,6 +206,7 @@ PyObject* dispatch(Args a) {
   const bool sh = a.truth();
   const Tensor* given = a.maybe("xs");
   const c10::Device dev = device_of(x, "x");
+  const OnDevice on(dev);
   const int dt = dtype_of(x, "x"), T = tokens(pos, K, sh);
   two_dims(x, "x");
   const int64_t H = x.size(1), S = (int64_t)T * (K + sh);
@@ -223,6 +225,7 @@ PyObject* dispatch_grad(Args a) {
   const bool sh = a.truth();
   const Tensor* given = a.maybe("dx");
   const c10::Device dev = device_of(dxs, "dxs");
+  const OnDevice on(dev);
   const int dt = dtype_of(dxs, "dxs"), T = tokens(pos, K, sh);
   two_dims(dxs, "dxs");
   const int64_t H = dxs.size(1), S = (int64_t)T * (K + sh);
@@ -243,6 +246,7 @@ PyObject* combine(Args a) {
   const bool sh = a.truth();
   const Tensor* given = a.maybe("out");
   const c10::Device dev = device_of(y, "y_slots");
+  const OnDevice on(dev);
   const int dt = dtype_of(y, "y_slots"), T = tokens(pos, K, sh);
   two_dims(y, "y_slots");
   const int64_t H = y.size(1), S = (int64_t)T * (K + sh);
@@ -277,6 +281,7 @@ PyObject* combine_grad(Args a) {
   const Tensor* dw_given = a.maybe("dw");
   const Tensor* dgate_given = a.maybe("dgate");
   const c10::Device dev = device_of(dout, "dout");
+  const OnDevice on(dev);
   const int dt = dtype_of(dout, "dout"), T = tokens(pos, K, sh);
   two_dims(dout, "dout");
   const ScalarType type = dout.scalar_type();
@@ -308,6 +313,7 @@ PyObject* route_topk_grad(Args a) {
   const int E = a.integer("E");
   const Tensor* given = a.maybe("dlogits");
   const c10::Device dev = device_of(ids, "ids");
+  const OnDevice on(dev);
   two_dims(ids, "ids");
   const int T = size32(ids.size(0), "T"), K = size32(ids.size(1), "K");
   if (E < 1) refuse("E must be positive");
@@ -343,6 +349,7 @@ PyObject* block_norm(Args a) {
   const Tensor* sp_given = a.maybe("rstd_post");
   const Tensor* sn_given = a.maybe("rstd_pre");
   const c10::Device dev = device_of(res, "residual");
+  const OnDevice on(dev);
   const int dt = dtype_of(res, "residual");
   const ScalarType type = res.scalar_type();
   two_dims(res, "residual");
@@ -391,6 +398,7 @@ PyObject* block_norm_grad(Args a) {
   const float res_scale = a.number(), out_scale = a.number();
   const Tensor* ws_given = a.maybe("ws");
   const c10::Device dev = device_of(r, "r");
+  const OnDevice on(dev);
   const int dt = dtype_of(r, "r");
   const ScalarType type = r.scalar_type();
   two_dims(r, "r");
@@ -451,6 +459,7 @@ PyObject* fp8_quant(Args a) {
   const Tensor* codes_given = a.maybe("codes");
   const Tensor* scales_given = a.maybe("scales");
   const c10::Device dev = device_of(x, "x");
+  const OnDevice on(dev);
   const int dt = dtype_of(x, "x");
   two_dims(x, "x");
   const int T = size32(x.size(0), "T"), K = size32(x.size(1), "K");
@@ -469,6 +478,7 @@ PyObject* fp8_linear(Args a) {
   const Tensor* ws_given = a.maybe("ws");
   const Tensor* given = a.maybe("out");
   const c10::Device dev = device_of(x, "x");
+  const OnDevice on(dev);
   const int dt = dtype_of(x, "x");
   two_dims(codes, "codes");
   const int N = size32(codes.size(0), "N"), K = size32(codes.size(1), "K");
@@ -505,6 +515,7 @@ PyObject* fp8_expert_ffn(Args a) {
   const Tensor* ws_given = a.maybe("ws");
   const Tensor* given = a.maybe("y_slots");
   const c10::Device dev = device_of(x, "x");
+  const OnDevice on(dev);
   if (x.dim() != 2 || x.size(1) != H) refuse("x width does not match the weight bank");
   const int T = size32(x.size(0), "T");
   if (E < 1 || I < 1 || K < 1) refuse("E, I and K must be positive");

@@ -2,7 +2,9 @@
 (csrc/binding.cpp does it for the sort, norm and e4m3 operators).
 
 Every function takes and returns torch tensors on the current HIP device and
-enqueues the library's kernels on torch's current stream.  Outputs (and, unless
+enqueues the library's kernels on torch's current stream (moe_layer and the sort,
+norm, combine and e4m3 operators: on their tensors' device, whichever is current,
+and its current stream).  Outputs (and, unless
 given, workspaces) are allocated with torch; all arithmetic runs in the HIP
 kernels of libmoe_nvfp4.so.
 """
@@ -310,7 +312,10 @@ def moe_layer(W: NVFP4Weights, x: torch.Tensor, logits: torch.Tensor, K: int,
     fused=True is the C entry moe_layer (two or three kernels for decode batches; the
     permutation's outputs in `perm` = (ids, w, counts, offsets, sorted_slot,
     slot_pos, groups) when given); fused=False runs the four separate entry
-    points.  Both give the same results."""
+    points.  Both give the same results.  Runs on x's device."""
+    if x.is_cuda and x.get_device() != torch._C._cuda_getDevice():
+        with torch.cuda.device(x.device):
+            return moe_layer(W, x, logits, K, act_mode, fused, gate, ws, perm, y_slots, out)
     if not fused:
         ids, w = moe_route_topk(logits, K)
         counts, offsets, sorted_slot, slot_pos, groups = moe_permute(ids, W.E, W.has_shared)

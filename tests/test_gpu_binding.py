@@ -108,3 +108,42 @@ def test_torch_sees_new_outputs(moe):
     finally:
         torch.use_deterministic_algorithms(before)
     assert torch.isnan(xs[3]).all() and not torch.isnan(xs[[0, 1, 2, 4]]).any()
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs two devices")
+def test_tensors_of_another_device(moe):
+    """Run where the tensors are, on that device's current stream; the current device stays."""
+    T, K, H = 9, 2, 264
+    x, w, pos = torch.randn(T, H), torch.rand(T, K), torch.randperm(T * K).int()
+    got = []
+    for dev in ("cuda:0", "cuda:1"):
+        stream = torch.cuda.Stream(dev)
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            a = [t.to(dev) for t in (x, w, pos)]
+        stream.synchronize()
+        torch.cuda.set_device(0)
+        xs = moe.moe_dispatch(a[0], a[2], K, False)
+        got.append(moe.moe_combine(xs, a[1], a[2], K, False))
+        assert torch.cuda.current_device() == 0 and got[-1].device == torch.device(dev)
+        torch.cuda.synchronize(dev)
+    assert torch.equal(got[0].cpu(), got[1].cpu())
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs two devices")
+def test_layer_on_another_device(moe):
+    """All of a layer's kernels on one stream of its tensors' device, in both forms."""
+    import numpy as np
+
+    from workloads import workload_for
+
+    wl = workload_for("tiny")
+    got = []
+    for dev in ("cuda:0", "cuda:1"):
+        W = moe.NVFP4Weights.from_bank(wl.weights, dev)
+        x = torch.from_numpy(wl.x_bf16.view(np.int16)).to(dev).view(torch.bfloat16)
+        logits = torch.from_numpy(wl.logits).to(dev)
+        torch.cuda.synchronize(dev)
+        for fused in (False, True):
+            got.append(moe.moe_layer(W, x, logits, wl.K, fused=fused)["out"])
+            torch.cuda.synchronize(dev)
+    assert all(torch.equal(got[0].cpu(), g.cpu()) for g in got[1:])
