@@ -4,11 +4,13 @@ Each ``csrc/*.hip`` file is compiled to an object under ``_build/`` in
 parallel, then linked into ``libmoe_nvfp4.so`` next to this file.  Every HIP
 file is compiled with packed-FP32 instructions disabled.  ``csrc/binding.cpp``
 is host code only: a Python module beside it that checks and passes on torch
-tensors.
+tensors.  The library stands by itself: it is in place before the module is
+begun, and where torch is missing the module is left out.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -37,13 +39,21 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found: the MoE library needs ROCm's hipcc")
 
 
+def cxx() -> str:
+    """The host compiler of the Python module: CXX, g++, or ROCm's own clang++."""
+    for c in (os.environ.get("CXX"), "g++", os.path.join(os.path.dirname(hipcc()), "amdclang++")):
+        if c and shutil.which(c):
+            return c
+    raise RuntimeError("no host C++ compiler found for the Python module (the library itself is built)")
+
+
 def binding_command(out: str) -> list:
     import torch
     from torch.utils import cpp_extension
 
     inc = [*cpp_extension.include_paths(), os.path.join(os.path.dirname(os.path.dirname(hipcc())), "include"),
            sysconfig.get_paths()["include"]]
-    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+    return [cxx(), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
             "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             *[f for p in inc for f in ("-isystem", p)], os.path.join(CSRC, "binding.cpp"), "-o", out,
@@ -51,7 +61,7 @@ def binding_command(out: str) -> list:
             "-L" + HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
 
 
-def build(verbose: bool = False) -> str:
+def build_library(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     cc = hipcc()
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
@@ -83,11 +93,24 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
     os.replace(tmp, LIB)
+    return LIB
+
+
+def build_binding() -> str:
     tmp = BINDING + ".tmp"
     r = subprocess.run(binding_command(tmp), stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
     if r.returncode != 0:
-        raise RuntimeError("binding compile failed:\n" + r.stdout.decode(errors="replace"))
+        raise RuntimeError(f"binding compile failed ({LIB} is built):\n" + r.stdout.decode(errors="replace"))
     os.replace(tmp, BINDING)
+    return BINDING
+
+
+def build(verbose: bool = False) -> str:
+    build_library(verbose)
+    if importlib.util.find_spec("torch") is None:
+        print("torch is not installed: the C library alone is built, without the Python module", file=sys.stderr)
+    else:
+        build_binding()
     return LIB
 
 
