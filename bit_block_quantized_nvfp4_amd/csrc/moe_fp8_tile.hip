@@ -182,10 +182,9 @@ __device__ __forceinline__ u32x4 buf_of(const void* p, uint32_t bytes) {
 // Memory to LDS, 16 (4) bytes a lane: lane l's bytes at voff + soff land at
 // lds + 16 l (4 l).  No register is written.  In asm because the compiler
 // would wait for every such load before the next LDS read of any buffer; the
-// kernel's own waits below order them.  m0 is reserved: the compiler keeps
-// nothing in it, and nothing else here uses it; a memory instruction may read it
-// one state after it was written.  ONCE: the bytes are not
-// read again (non-temporal).
+// kernel's own waits below order them.  m0 is theirs while a block lasts, and
+// named as overwritten; a memory instruction may read it one state after it was
+// written.  ONCE: the bytes are not read again (non-temporal).
 // A wave-uniform offset for these, in a scalar register that a memory
 // instruction may read: one that a vector instruction wrote needs 5 states.
 __device__ __forceinline__ uint32_t dma_offset(uint32_t v) {
@@ -198,16 +197,16 @@ __device__ __forceinline__ void dma_b128(u32x4 buf, uint32_t voff, uint32_t soff
   if (ONCE)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds" ::"s"(lds),
                  "v"(voff), "s"(buf), "s"(soff)
-                 : "memory");
+                 : "m0", "memory");
   else
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds),
                  "v"(voff), "s"(buf), "s"(soff)
-                 : "memory");
+                 : "m0", "memory");
 }
 __device__ __forceinline__ void dma_b32(u32x4 buf, uint32_t voff, uint32_t soff, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds),
                "v"(voff), "s"(buf), "s"(soff)
-               : "memory");
+               : "m0", "memory");
 }
 // All but the wave's last N memory operations are done, and all its LDS reads;
 // then the block's waves meet.
