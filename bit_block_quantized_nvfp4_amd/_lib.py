@@ -25,12 +25,6 @@ MOE_OP_EXPERT_FFN = 2
 MOE_OP_EXPERT_FFN_COMBINE = 3
 MOE_OP_LAYER = 4
 MOE_NOALLOC_WS_BYTES = 32 << 20
-MOE_DT_BF16 = 0
-MOE_DT_F16 = 1
-MOE_DT_F32 = 2
-MOE_GATE_NONE = 0
-MOE_GATE_TOKEN = 1
-MOE_GATE_ELEMENT = 2
 
 
 class MoeNvfp4Weights(ctypes.Structure):
