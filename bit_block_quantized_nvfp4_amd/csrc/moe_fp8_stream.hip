@@ -281,12 +281,12 @@ hipError_t launch_fp8_stream_experts(const moe_fp8_weights& W, const uint16_t* x
   // K.  The call in a row in a graph, H = 2048, I = 512, top 10 of 512 and a
   // shared one, us (gate_up waves, down row tiles x waves; * the one taken):
   //   T (groups)   8, 2x2  4, 2x2  8, 4x2  4, 4x2  4, 4x1
-  //   1 (11)        15.0*   15.9    15.7    17.0    17.5
-  //   2 (21)        22.4    21.2*   21.9    21.7    22.4
-  //   4 (41)        33.9    32.4*   35.8    34.6    33.4
-  //   6 (61)        43.3    40.9    44.0    41.4    40.5*
-  //   8 (81)        51.0    52.5    57.8    51.9    47.7*
-  //   12 (121)      83.0    67.3    72.8    65.5    64.4*
+  //   1 (11)        15.0*   16.5    15.9    17.1    18.4
+  //   2 (21)        21.5    21.1*   21.8    21.5    22.5
+  //   4 (41)        33.6    32.6*   34.8    34.5    33.1
+  //   6 (61)        48.0    44.2    48.2    44.1    43.5*
+  //   8 (81)        53.7    49.7    54.9    50.8    47.7*
+  //   12 (121)      77.4    70.6    77.5    70.5    66.2*
   if (G > 16)
     MOE_LAUNCH("fp8_stream_gate_up", s, (k_fp8_stream<MOE_DT_BF16, kStreamGateUp, 2, 4, 4>),
                dim3((unsigned)G * a.tiles), dim3(256), 0, s, a);

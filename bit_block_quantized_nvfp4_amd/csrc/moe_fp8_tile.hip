@@ -801,23 +801,28 @@ static int tiles_per_block(size_t S, int G, int nt) {
   return n;
 }
 
-// Batches up to this many tokens stream the experts' weights (16 rows of a group
-// are one pass).  Streams against tiles, us: H = 2048, I = 512, top 10 of 512, T =
-// 9 52 and 68, 11 62 and 72, 13 66 and 78, 16 87 and 80; H = 4096, I = 1024, top 2
-// of 8, T = 9 31 and 41, 13 30 and 47, 16 39 and 42; H = 1024, I = 256, top 10 of
-// 512, T = 9 20 and 27, 13 23 and 31, 16 27 and 33.
-constexpr int kFp8StreamT = 13;
+// Few tokens stream the experts' weights (16 rows of a group are one pass): the
+// layer's own switch, and a few more where the matrices are small and a group's
+// start counts.  Streams against tiles, us, the same routing (bf16, a shared
+// expert): H = 2048, I = 512, top 10 of 512, T = 8 49 and 66, 10 58 and 70, 12 67
+// and 73, 13 79 and 80, 16 87 and 84; H = 1024, I = 256, T = 8 20 and 25, 12 23 and
+// 28; H = 2048, I = 1408, top 6 of 64, T = 8 83 and 88, 12 73 and 75; H = 2048, I =
+// 1024, top 8 of 256, T = 4 43 and 43, 8 77 and 72, 10 89 and 77; H = 4096, I =
+// 1536, top 8 of 128, T = 1 43 and 54, 4 126 and 115, 8 206 and 204, 12 248 and 220.
+static bool fp8_experts_stream(int T, int H, int I) {
+  return T <= kDecodeMaxT || (T <= 12 && (long)H * I <= 1L << 20);
+}
 
 size_t fp8_expert_ffn_workspace_bytes(int T, int K, int H, int I, int has_shared) {
   const size_t S = (size_t)T * K + (has_shared ? T : 0);
-  if (T <= kFp8StreamT) return up256(S * I * sizeof(float));
+  if (fp8_experts_stream(T, H, I)) return up256(S * I * sizeof(float));
   const size_t tiles = max_tiles(S, kPMaxG);
   return up256((size_t)T * H) + up256((size_t)T * (H / kQB) * sizeof(float)) + up256(S * I) +
          up256(tiles * (I / kQB) * kPM * sizeof(float)) + 16 * (tiles + 1);
 }
 
 uint64_t fp8_expert_ffn_threads(const moe_fp8_weights& W, int T, int K) {
-  if (T <= kFp8StreamT) return 0;  // at most 13 * 32 + 1 groups
+  if (fp8_experts_stream(T, W.H, W.I)) return 0;  // at most 12 * 32 + 1 groups
   const size_t S = (size_t)T * K + (W.has_shared ? T : 0), mt = max_tiles(S, W.E + W.has_shared);
   const int ngu = W.I / 128, ndn = W.H / 128, G = W.E + W.has_shared;
   return std::max({(uint64_t)mt * (ngu / tiles_per_block(S, G, ngu)) * 512,
@@ -828,7 +833,7 @@ uint64_t fp8_expert_ffn_threads(const moe_fp8_weights& W, int T, int K) {
 hipError_t launch_fp8_expert_ffn(const moe_fp8_weights& W, const uint16_t* x, int T, int K,
                                  const int32_t* offsets, const int32_t* sorted_slot,
                                  const int32_t* groups, uint16_t* y, void* ws, hipStream_t s) {
-  if (T <= kFp8StreamT)
+  if (fp8_experts_stream(T, W.H, W.I))
     return launch_fp8_stream_experts(W, x, T, K, offsets, sorted_slot, groups, (float*)ws, y, s);
   const size_t S = (size_t)T * K + (W.has_shared ? T : 0);
   const int G = W.E + W.has_shared;

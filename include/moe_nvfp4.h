@@ -532,8 +532,9 @@ int moe_fp8_linear(const moe_fp8_matrix* M, const void* x, int T, int dtype, voi
  *
  * with xq, hq the rows quantised as above (x [T][H] bf16, h not rounded in
  * between).  offsets, sorted_slot and groups are moe_permute's; y_slots goes to
- * moe_combine.  Up to 13 tokens the active experts' weights stream once, in
- * two launches; more run as the quantisation and two grouped products.
+ * moe_combine.  Up to 8 tokens (12 where H*I <= 2^20) the active experts' weights
+ * stream once, in two launches; more run as the quantisation and two grouped
+ * products.
  *
  *   ws  at least moe_fp8_expert_ffn_workspace_bytes(T, K, H, I, has_shared)
  *
