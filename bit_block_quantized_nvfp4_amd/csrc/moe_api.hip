@@ -311,6 +311,8 @@ int moe_route_permute(const float* logits, int T, int E, int K, int has_shared, 
     return fail(MOE_EINVAL, "moe_route_permute: null pointer");
   if (!sizes_ok_common(T, E, K) || (has_shared != 0 && has_shared != 1))
     return fail(MOE_EINVAL, "moe_route_permute: need T >= 1, 1 <= K <= min(E, 32), E <= 1024, has_shared in {0,1}");
+  if (!slots_ok(T, K, has_shared))
+    return fail(MOE_EINVAL, "moe_route_permute: T*(K + has_shared) must be below 2^31 (T=%d K=%d)", T, K);
   const size_t need = moe::permute_workspace_bytes(T, E, K);
   if (need > 0 && (!ws || ws_bytes < need))
     return fail(MOE_EWORKSPACE, "moe_route_permute: workspace of %zu bytes needed, %zu given", need, ws_bytes);

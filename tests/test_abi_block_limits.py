@@ -36,6 +36,7 @@ def test_shared_positions_fit_int32(L, dt):
     _refused(L, lib.moe_combine(P, P, P, T, 1, 8, 1, P, None), b"2^31")
     _refused(L, lib.moe_combine_gated(P, P, P, P, T, 1, 8, P, None), b"2^31")
     _refused(L, lib.moe_permute(P, T, 8, 1, 1, P, P, P, P, P, None, 0, None), b"2^31")
+    _refused(L, lib.moe_route_permute(P, T, 8, 1, 1, P, P, P, P, P, P, P, None, 0, None), b"2^31")
 
 
 def test_grids_stay_below_2_32_threads(L):
