@@ -170,12 +170,14 @@ void* ptr(const Tensor* t) { return t ? t->data_ptr() : nullptr; }
 // One call of the C ABI, without the interpreter's lock: a launch may have to wait
 // (a full queue, the first call's kernel lookup), and other Python threads go on
 // meanwhile, as they do through ctypes.  The caller's frame holds the arguments.
+struct Unlocked {
+  PyThreadState* const state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
 template <typename F, typename... A>
 int call(F f, A... a) {
-  PyThreadState* const s = PyEval_SaveThread();
-  const int status = f(a...);
-  PyEval_RestoreThread(s);
-  return status;
+  const Unlocked meanwhile;
+  return f(a...);
 }
 
 void check(int status) {
