@@ -182,9 +182,11 @@ __device__ __forceinline__ u32x4 buf_of(const void* p, uint32_t bytes) {
 // Memory to LDS, 16 (4) bytes a lane: lane l's bytes at voff + soff land at
 // lds + 16 l (4 l).  No register is written.  In asm because the compiler
 // would wait for every such load before the next LDS read of any buffer; the
-// kernel's own waits below order them.  m0 is theirs while a block lasts, and
-// named as overwritten; a memory instruction may read it one state after it was
-// written.  ONCE: the bytes are not read again (non-temporal).
+// kernel's own waits below order them.  m0 is reserved in the compiler (it may
+// not be named as overwritten), which keeps nothing in it between instructions;
+// that nothing else touches it is tested on the built code.  A memory instruction
+// may read it one state after it was written.  ONCE: the bytes are not read again
+// (non-temporal).
 // A wave-uniform offset for these, in a scalar register that a memory
 // instruction may read: one that a vector instruction wrote needs 5 states.
 __device__ __forceinline__ uint32_t dma_offset(uint32_t v) {
@@ -197,16 +199,16 @@ __device__ __forceinline__ void dma_b128(u32x4 buf, uint32_t voff, uint32_t soff
   if (ONCE)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds" ::"s"(lds),
                  "v"(voff), "s"(buf), "s"(soff)
-                 : "m0", "memory");
+                 : "memory");
   else
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds),
                  "v"(voff), "s"(buf), "s"(soff)
-                 : "m0", "memory");
+                 : "memory");
 }
 __device__ __forceinline__ void dma_b32(u32x4 buf, uint32_t voff, uint32_t soff, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds),
                "v"(voff), "s"(buf), "s"(soff)
-               : "m0", "memory");
+               : "memory");
 }
 // All but the wave's last N memory operations are done, and all its LDS reads;
 // then the block's waves meet.
@@ -228,9 +230,11 @@ __device__ __forceinline__ void meet() {
 // KG > 1 (linear mode): KG groups of waves with buffers of their own take every
 // KG-th step and join their sums at the end, in the groups' order; a step costs
 // about half a microsecond of waiting whatever its size, which counts where
-// there are few tiles.
+// there are few tiles.  The grouped modes' registers are held to two waves a SIMD:
+// down has two blocks on a compute unit so, with six registers spilled once a tile
+// (the experts' call at T = 4096 531 us, with one block 585 us).
 template <int MODE, int DT, int BN, int BM, int WN, int WM, int NBUF, int KG = 1>
-__global__ __launch_bounds__(64 * WN * WM * KG, 2) void k_fp8_tile(TileArgs a) {
+__global__ __launch_bounds__(64 * WN * WM * KG, MODE == kTileLinear ? 1 : 2) void k_fp8_tile(TileArgs a) {
   constexpr int NW = WN * WM, NT = 64 * NW;    // waves and threads of a group
   constexpr int TN = BN / WN, TM = BM / WM;    // a wave's part of the tile
   constexpr int FN = TN / 32, FM = TM / 32;    // products of 32 x 32
