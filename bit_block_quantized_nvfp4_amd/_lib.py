@@ -74,6 +74,34 @@ class MoeFp8Weights(ctypes.Structure):
     ]
 
 
+class MoeDenseWeights(ctypes.Structure):
+    _fields_ = [
+        ("gu", ctypes.c_void_p),
+        ("dn", ctypes.c_void_p),
+        ("H", ctypes.c_int32),
+        ("I", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class MoeInt8Matrix(ctypes.Structure):
+    _fields_ = [
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("N", ctypes.c_int32),
+        ("K", ctypes.c_int32),
+    ]
+
+
+class MoeGradTensor(ctypes.Structure):
+    _fields_ = [
+        ("grad", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"moe_nvfp4 status {status}: {msg}")
@@ -119,6 +147,17 @@ _SIGS = {
     "moe_fp8_expert_ffn_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
     "moe_fp8_expert_ffn": (_I, [ctypes.POINTER(MoeFp8Weights), _P, _I, _I, _P, _P, _P, _P, _P,
                                 _SZ, _P]),
+    "moe_dense_ffn_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "moe_dense_ffn": (_I, [ctypes.POINTER(MoeDenseWeights), _P, _I, _P, _P, _P, _SZ, _P]),
+    "moe_dense_ffn_grad_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "moe_dense_ffn_grad": (_I, [ctypes.POINTER(MoeDenseWeights), _P, _P, _P, _I, _P, _P, _P, _P,
+                                _SZ, _P]),
+    "moe_int8_quant": (_I, [_P, _I, _I, _I, _P, _P, _P]),
+    "moe_int8_linear_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "moe_int8_linear": (_I, [ctypes.POINTER(MoeInt8Matrix), _P, _I, _I, _I, _P, _P, _SZ, _P]),
+    "moe_grad_norm_workspace_bytes": (_SZ, [_I]),
+    "moe_grad_norm": (_I, [ctypes.POINTER(MoeGradTensor), _I, _P, _P, _SZ, _P]),
+    "moe_grad_clip": (_I, [ctypes.POINTER(MoeGradTensor), _I, _P, _F, _P]),
     "moe_timing_enable": (_I, [_I]),
     "moe_timing_reset": (_I, []),
     "moe_timing_read": (_I, [ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(_I),

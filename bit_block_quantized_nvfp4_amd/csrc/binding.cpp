@@ -1,4 +1,5 @@
-// Python entry points of the token sort, block norm and e4m3 operators: tensors
+// Python entry points of the token sort, block norm, e4m3, dense block, 8-bit integer
+// and gradient norm operators: tensors
 // in, checks, outputs where none are given, one call of the C ABI on torch's
 // current stream, tensors out.  No arithmetic.  ops.py documents the arguments
 // and passes them on by position; doing the marshalling here instead of there
@@ -15,6 +16,7 @@
 #include <initializer_list>
 #include <sstream>
 #include <string>
+#include <vector>
 
 #include "../../include/moe_nvfp4.h"
 
@@ -544,6 +546,200 @@ PyObject* fp8_expert_ffn(Args a) {
   return wrap(y);
 }
 
+// The dense block's weights, rows x of its width, and their number.
+moe_dense_weights dense_weights(const Tensor& gu, const Tensor& dn, const Tensor& x, c10::Device dev, int* T) {
+  const int dt = dtype_of(gu, "gu");
+  if (dt == MOE_DT_F32) refuse("gu must be bfloat16 or float16, got torch.float32");
+  two_dims(gu, "gu");
+  two_dims(x, "x");
+  moe_dense_weights W;
+  if (gu.size(0) % 2) refuse("gu must have an even number of rows, got ", gu.size(0));
+  W.H = size32(gu.size(1), "H");
+  W.I = size32(gu.size(0) / 2, "I");
+  W.dtype = dt;
+  W.gu = need(gu, gu.scalar_type(), {2 * (int64_t)W.I, W.H}, dev, "gu");
+  W.dn = need(dn, gu.scalar_type(), {W.H, W.I}, dev, "dn");
+  *T = size32(x.size(0), "T");
+  need(x, gu.scalar_type(), {*T, W.H}, dev, "x");
+  return W;
+}
+
+PyObject* dense_ffn(Args a) {
+  const Tensor& gu = a.tensor("gu");
+  const Tensor& dn = a.tensor("dn");
+  const Tensor& x = a.tensor("x");
+  const bool keep = a.truth();
+  const Tensor* ws_given = a.maybe("ws");
+  const Tensor* given = a.maybe("out");
+  const Tensor* gu_given = a.maybe("gu_out");
+  const c10::Device dev = device_of(x, "x");
+  const OnDevice on(dev);
+  int T;
+  const moe_dense_weights W = dense_weights(gu, dn, x, dev, &T);
+  if (gu_given && !keep) refuse("gu_out is given without keep");
+  Tensor y = output(given, x.scalar_type(), {T, W.H}, dev, "out");
+  Tensor kept;
+  if (keep) kept = output(gu_given, x.scalar_type(), {T, 2 * (int64_t)W.I}, dev, "gu_out");
+  const size_t bytes = moe_dense_ffn_workspace_bytes(T, W.H, W.I);
+  Tensor ws = scratch(ws_given, bytes, dev);
+  check(call(moe_dense_ffn, &W, x.data_ptr(), T, y.data_ptr(), keep ? kept.data_ptr() : nullptr,
+             ws.data_ptr(), bytes, stream()));
+  return keep ? wrap_all({y, kept}) : wrap(y);
+}
+
+PyObject* dense_ffn_grad(Args a) {
+  const Tensor& gu = a.tensor("gu");
+  const Tensor& dn = a.tensor("dn");
+  const Tensor& dy = a.tensor("dy");
+  const Tensor& x = a.tensor("x");
+  const Tensor& kept = a.tensor("gu kept");
+  const Tensor* ws_given = a.maybe("ws");
+  const Tensor* dx_given = a.maybe("dx");
+  const Tensor* dgu_given = a.maybe("dw_gu");
+  const Tensor* ddn_given = a.maybe("dw_dn");
+  const c10::Device dev = device_of(x, "x");
+  const OnDevice on(dev);
+  int T;
+  const moe_dense_weights W = dense_weights(gu, dn, x, dev, &T);
+  const ScalarType type = x.scalar_type();
+  need(dy, type, {T, W.H}, dev, "dy");
+  need(kept, type, {T, 2 * (int64_t)W.I}, dev, "gu kept");
+  Tensor dx = output(dx_given, type, {T, W.H}, dev, "dx");
+  Tensor dgu = output(dgu_given, type, {2 * (int64_t)W.I, W.H}, dev, "dw_gu");
+  Tensor ddn = output(ddn_given, type, {W.H, W.I}, dev, "dw_dn");
+  const size_t bytes = moe_dense_ffn_grad_workspace_bytes(T, W.H, W.I);
+  Tensor ws = scratch(ws_given, bytes, dev);
+  check(call(moe_dense_ffn_grad, &W, dy.data_ptr(), x.data_ptr(), kept.data_ptr(), T, dx.data_ptr(),
+             dgu.data_ptr(), ddn.data_ptr(), ws.data_ptr(), bytes, stream()));
+  return wrap_all({dx, dgu, ddn});
+}
+
+PyObject* int8_quant(Args a) {
+  const Tensor& x = a.tensor("x");
+  const Tensor* codes_given = a.maybe("codes");
+  const Tensor* scales_given = a.maybe("scales");
+  const c10::Device dev = device_of(x, "x");
+  const OnDevice on(dev);
+  const int dt = dtype_of(x, "x");
+  two_dims(x, "x");
+  const int T = size32(x.size(0), "T"), K = size32(x.size(1), "K");
+  need(x, x.scalar_type(), {T, K}, dev, "x");
+  Tensor codes = output(codes_given, at::kChar, {T, K}, dev, "codes");
+  Tensor scales = output(scales_given, at::kFloat, {T}, dev, "scales");
+  check(call(moe_int8_quant, x.data_ptr(), T, K, dt, (int8_t*)codes.data_ptr(), scales.data_ptr<float>(),
+             stream()));
+  return wrap_all({codes, scales});
+}
+
+PyObject* int8_linear(Args a) {
+  const Tensor& codes = a.tensor("codes");
+  const Tensor& scales = a.tensor("scales");
+  const Tensor& x = a.tensor("x");
+  const bool gated = a.truth();
+  const Tensor* ws_given = a.maybe("ws");
+  const Tensor* given = a.maybe("out");
+  const c10::Device dev = device_of(x, "x");
+  const OnDevice on(dev);
+  const int dt = dtype_of(x, "x");
+  two_dims(codes, "codes");
+  moe_int8_matrix M;
+  M.N = size32(codes.size(0), "N");
+  M.K = size32(codes.size(1), "K");
+  M.codes = (const int8_t*)need(codes, at::kChar, {M.N, M.K}, dev, "codes");
+  M.scales = (const float*)need(scales, at::kFloat, {M.N}, dev, "scales");
+  if (x.dim() != 2 || x.size(1) != M.K) refuse("x must be [T, ", M.K, "], got ", shape_text(x.sizes()));
+  if (gated && M.N % 2) refuse("a gated matrix has an even number of rows, got ", M.N);
+  const int T = size32(x.size(0), "T");
+  need(x, x.scalar_type(), {T, M.K}, dev, "x");
+  Tensor out = output(given, x.scalar_type(), {T, gated ? M.N / 2 : M.N}, dev, "out");
+  const size_t bytes = moe_int8_linear_workspace_bytes(T, M.N, M.K);
+  Tensor ws;
+  if (bytes) ws = scratch(ws_given, bytes, dev);
+  check(call(moe_int8_linear, &M, x.data_ptr(), T, dt, gated, out.data_ptr(),
+             bytes ? ws.data_ptr() : nullptr, bytes, stream()));
+  return wrap(out);
+}
+
+// A list or tuple of tensors, held while it lives.
+struct TensorList {
+  PyObject* seq;
+  TensorList(PyObject* o, const char* name) : seq(o) {
+    if (!PyList_Check(o) && !PyTuple_Check(o)) refuse(name, " must be a list or tuple of tensors");
+    Py_INCREF(seq);
+  }
+  TensorList(const TensorList&) = delete;
+  ~TensorList() { Py_DECREF(seq); }
+  Py_ssize_t size() const { return PySequence_Fast_GET_SIZE(seq); }
+  const Tensor& at(Py_ssize_t i, const char* name) const {
+    PyObject* o = PySequence_Fast_GET_ITEM(seq, i);
+    if (!THPVariable_Check(o)) refuse(name, "[", i, "] must be a tensor");
+    return THPVariable_Unpack(o);
+  }
+};
+
+c10::Device device_of_list(const TensorList& l, const char* name) {
+  if (l.size() < 1) refuse(name, " is empty");
+  if (l.size() > (1 << 20)) refuse(name, " has more than 2^20 tensors");
+  return device_of(l.at(0, name), name);
+}
+
+// The gradients as the library takes them: any layout without gaps, the sums and the
+// scaling go value by value.
+std::vector<moe_grad_tensor> grad_list(const TensorList& l, c10::Device dev) {
+  std::vector<moe_grad_tensor> r((size_t)l.size());
+  for (Py_ssize_t i = 0; i < l.size(); ++i) {
+    const Tensor& t = l.at(i, "grads");
+    if (t.device() != dev) refuse("grads[", i, "] must be on ", dev.str(), ", got ", t.device().str());
+    if (!t.is_non_overlapping_and_dense()) refuse("grads[", i, "] must have no gaps and no overlaps");
+    r[i].grad = t.data_ptr();
+    r[i].out = nullptr;
+    r[i].n = t.numel();
+    r[i].dtype = dtype_of(t, "grads");
+  }
+  return r;
+}
+
+PyObject* grad_norm(Args a) {
+  const TensorList grads(a.next(), "grads");
+  const Tensor* given = a.maybe("norm");
+  const Tensor* ws_given = a.maybe("ws");
+  const c10::Device dev = device_of_list(grads, "grads");
+  const OnDevice on(dev);
+  const std::vector<moe_grad_tensor> list = grad_list(grads, dev);
+  Tensor norm = output(given, at::kFloat, {1}, dev, "norm");
+  const size_t bytes = moe_grad_norm_workspace_bytes((int)list.size());
+  Tensor ws = scratch(ws_given, bytes, dev);
+  check(call(moe_grad_norm, list.data(), (int)list.size(), norm.data_ptr<float>(), ws.data_ptr(), bytes,
+             stream()));
+  return wrap(norm);
+}
+
+PyObject* grad_clip(Args a) {
+  const TensorList grads(a.next(), "grads");
+  const Tensor& norm = a.tensor("norm");
+  const float max_norm = a.number();
+  PyObject* const outs = a.next();
+  const c10::Device dev = device_of_list(grads, "grads");
+  const OnDevice on(dev);
+  std::vector<moe_grad_tensor> list = grad_list(grads, dev);
+  need(norm, at::kFloat, {1}, dev, "norm");
+  if (outs == Py_None) {
+    for (moe_grad_tensor& g : list) g.out = (void*)g.grad;
+  } else {
+    const TensorList out(outs, "out");
+    if (out.size() != grads.size()) refuse("out has ", out.size(), " tensors, grads has ", grads.size());
+    for (Py_ssize_t i = 0; i < out.size(); ++i) {
+      const Tensor &g = grads.at(i, "grads"), &o = out.at(i, "out");
+      if (o.device() != dev || o.scalar_type() != g.scalar_type() || o.sizes() != g.sizes() ||
+          (g.numel() > 0 && o.strides() != g.strides()))
+        refuse("out[", i, "] must be like grads[", i, "]: device, type, shape and strides");
+      list[i].out = o.data_ptr();
+    }
+  }
+  check(call(moe_grad_clip, list.data(), (int)list.size(), norm.data_ptr<float>(), max_norm, stream()));
+  Py_RETURN_NONE;
+}
+
 // C++ errors end here: none passes into the interpreter.
 template <PyObject* (*F)(Args)>
 PyObject* entry(PyObject*, PyObject* const* v, Py_ssize_t n) {
@@ -579,7 +775,9 @@ PyMethodDef methods[] = {
     ENTRY(dispatch),        ENTRY(dispatch_grad), ENTRY(combine),
     ENTRY(combine_grad),    ENTRY(route_topk_grad), ENTRY(block_norm),
     ENTRY(block_norm_grad), ENTRY(fp8_quant),     ENTRY(fp8_linear),
-    ENTRY(fp8_expert_ffn),  {"set_errors", set_errors, METH_VARARGS, nullptr},
+    ENTRY(fp8_expert_ffn),  ENTRY(dense_ffn),     ENTRY(dense_ffn_grad),
+    ENTRY(int8_quant),      ENTRY(int8_linear),   ENTRY(grad_norm),
+    ENTRY(grad_clip),       {"set_errors", set_errors, METH_VARARGS, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods,
                       nullptr,               nullptr,    nullptr, nullptr};

@@ -1,6 +1,7 @@
 // C entry points of libmoe_nvfp4: argument checks, the gfx950 gate, one-time
 // kernel resolution, dispatch to the launchers, error text, and the optional
 // per-kernel event timing.
+#include <float.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
@@ -92,6 +93,9 @@ int ensure_init() {
   moe::register_block_norm_kernels(ks);
   moe::register_fp8_stream_kernels(ks);
   moe::register_fp8_tile_kernels(ks);
+  moe::register_dense_kernels(ks);
+  moe::register_int8_kernels(ks);
+  moe::register_grad_norm_kernels(ks);
   for (const void* k : ks) {
     hipFuncAttributes attr;
     e = hipFuncGetAttributes(&attr, k);
@@ -674,6 +678,160 @@ int moe_fp8_expert_ffn(const moe_fp8_weights* W, const uint16_t* x, int T, int K
   return launched(moe::launch_fp8_expert_ffn(*W, x, T, K, offsets, sorted_slot, groups, y_slots, ws,
                                              (hipStream_t)stream),
                   "moe_fp8_expert_ffn launch");
+}
+
+static bool dense_sizes_ok(int T, int H, int I) {
+  return T >= 1 && H >= 8 && H <= 65536 && H % 8 == 0 && I >= 8 && I <= 65536 && I % 8 == 0;
+}
+
+// What both dense entry points ask of the weights and the sizes.
+static int dense_ok(const char* what, const moe_dense_weights& W, int T) {
+  if (!W.gu || !W.dn) return fail(MOE_EINVAL, "%s: null weight pointer", what);
+  if (W.dtype != MOE_DT_BF16 && W.dtype != MOE_DT_F16)
+    return fail(MOE_EUNSUPPORTED, "%s: dtype %d is not bf16 or f16", what, W.dtype);
+  if (!dense_sizes_ok(T, W.H, W.I))
+    return fail(MOE_EINVAL, "%s: need T >= 1, H and I multiples of 8 in [8, 65536] (T=%d H=%d I=%d)", what, T, W.H, W.I);
+  if (!grid_ok(moe::dense_threads(T, W.H, W.I))) return too_many_rows(what, T);
+  return MOE_OK;
+}
+
+size_t moe_dense_ffn_workspace_bytes(int T, int H, int I) {
+  return dense_sizes_ok(T, H, I) ? moe::dense_ffn_workspace_bytes(T, H, I) : 0;
+}
+
+int moe_dense_ffn(const moe_dense_weights* W, const void* x, int T, void* y, void* gu_out,
+                  void* ws, size_t ws_bytes, void* stream) {
+  if (!W || !x || !y) return fail(MOE_EINVAL, "moe_dense_ffn: null pointer");
+  int rc = dense_ok("moe_dense_ffn", *W, T);
+  if (rc != MOE_OK) return rc;
+  if (!aligned16((const char*)x, (const char*)y, (const char*)gu_out, (const char*)W->gu,
+                 (const char*)W->dn, (const char*)ws))
+    return fail(MOE_EINVAL, "moe_dense_ffn: weights, rows and workspace must be aligned to 16 bytes");
+  const size_t need = moe::dense_ffn_workspace_bytes(T, W->H, W->I);
+  if (!ws || ws_bytes < need)
+    return fail(MOE_EWORKSPACE, "moe_dense_ffn: workspace of %zu bytes needed, %zu given", need, ws_bytes);
+  rc = ensure_init();
+  if (rc != MOE_OK) return rc;
+  return launched(moe::launch_dense_ffn(*W, x, T, y, gu_out, ws, (hipStream_t)stream),
+                  "moe_dense_ffn launch");
+}
+
+size_t moe_dense_ffn_grad_workspace_bytes(int T, int H, int I) {
+  return dense_sizes_ok(T, H, I) ? moe::dense_ffn_grad_workspace_bytes(T, H, I) : 0;
+}
+
+int moe_dense_ffn_grad(const moe_dense_weights* W, const void* dy, const void* x, const void* gu,
+                       int T, void* dx, void* dw_gu, void* dw_dn, void* ws, size_t ws_bytes,
+                       void* stream) {
+  if (!W || !dy || !x || !gu || !dx || !dw_gu || !dw_dn)
+    return fail(MOE_EINVAL, "moe_dense_ffn_grad: null pointer");
+  int rc = dense_ok("moe_dense_ffn_grad", *W, T);
+  if (rc != MOE_OK) return rc;
+  if (!aligned16((const char*)dy, (const char*)x, (const char*)gu, (const char*)dx,
+                 (const char*)dw_gu, (const char*)dw_dn, (const char*)W->gu, (const char*)W->dn,
+                 (const char*)ws))
+    return fail(MOE_EINVAL, "moe_dense_ffn_grad: weights, rows and workspace must be aligned to 16 bytes");
+  const size_t need = moe::dense_ffn_grad_workspace_bytes(T, W->H, W->I);
+  if (!ws || ws_bytes < need)
+    return fail(MOE_EWORKSPACE, "moe_dense_ffn_grad: workspace of %zu bytes needed, %zu given", need, ws_bytes);
+  rc = ensure_init();
+  if (rc != MOE_OK) return rc;
+  return launched(moe::launch_dense_ffn_grad(*W, dy, x, gu, T, dx, dw_gu, dw_dn, ws, (hipStream_t)stream),
+                  "moe_dense_ffn_grad launch");
+}
+
+static bool int8_k_ok(int T, int K) { return T >= 1 && K >= 16 && K <= 65536 && K % 16 == 0; }
+static bool int8_matrix_ok(int T, int N, int K) {
+  return int8_k_ok(T, K) && N >= 8 && N <= 131072 && N % 8 == 0;
+}
+
+int moe_int8_quant(const void* x, int T, int K, int dtype, int8_t* codes, float* scales,
+                   void* stream) {
+  if (!x || !codes || !scales) return fail(MOE_EINVAL, "moe_int8_quant: null pointer");
+  if (!dtype_ok(dtype)) return fail(MOE_EUNSUPPORTED, "moe_int8_quant: unknown dtype %d", dtype);
+  if (!int8_k_ok(T, K))
+    return fail(MOE_EINVAL, "moe_int8_quant: need T >= 1 and K a multiple of 16 in [16, 65536] (T=%d K=%d)", T, K);
+  if (!grid_ok((uint64_t)T * 256)) return too_many_rows("moe_int8_quant", T);
+  if (!aligned16((const char*)x, (const char*)codes))
+    return fail(MOE_EINVAL, "moe_int8_quant: rows must be aligned to 16 bytes");
+  int rc = ensure_init();
+  if (rc != MOE_OK) return rc;
+  return launched(moe::launch_int8_quant(x, T, K, dtype, codes, scales, (hipStream_t)stream),
+                  "moe_int8_quant launch");
+}
+
+size_t moe_int8_linear_workspace_bytes(int T, int N, int K) {
+  return int8_matrix_ok(T, N, K) ? moe::int8_linear_workspace_bytes(T, N, K) : 0;
+}
+
+int moe_int8_linear(const moe_int8_matrix* M, const void* x, int T, int dtype, int gated,
+                    void* out, void* ws, size_t ws_bytes, void* stream) {
+  if (!M || !x || !out) return fail(MOE_EINVAL, "moe_int8_linear: null pointer");
+  if (!M->codes || !M->scales) return fail(MOE_EINVAL, "moe_int8_linear: null weight pointer");
+  if (!dtype_ok(dtype)) return fail(MOE_EUNSUPPORTED, "moe_int8_linear: unknown dtype %d", dtype);
+  if (gated != 0 && gated != 1) return fail(MOE_EINVAL, "moe_int8_linear: gated must be 0 or 1");
+  if (!int8_matrix_ok(T, M->N, M->K) || (gated && M->N % 16))
+    return fail(MOE_EINVAL, "moe_int8_linear: need T >= 1, K a multiple of 16 in [16, 65536] and N a multiple of 8 (gated: 16) in [8, 131072] (T=%d N=%d K=%d)", T, M->N, M->K);
+  if (!grid_ok(moe::int8_linear_threads(T, M->N))) return too_many_rows("moe_int8_linear", T);
+  if (!aligned16((const char*)x, (const char*)out, (const char*)M->codes, (const char*)ws))
+    return fail(MOE_EINVAL, "moe_int8_linear: codes, rows and workspace must be aligned to 16 bytes");
+  const size_t need = moe::int8_linear_workspace_bytes(T, M->N, M->K);
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(MOE_EWORKSPACE, "moe_int8_linear: workspace of %zu bytes needed, %zu given", need, ws_bytes);
+  int rc = ensure_init();
+  if (rc != MOE_OK) return rc;
+  return launched(moe::launch_int8_linear(*M, x, T, dtype, gated, out, ws, (hipStream_t)stream),
+                  "moe_int8_linear launch");
+}
+
+// What both gradient entry points ask of the list; outs: its outputs too.
+static int grad_list_ok(const char* what, const moe_grad_tensor* list, int count, bool outs) {
+  if (!list) return fail(MOE_EINVAL, "%s: null pointer", what);
+  if (count < 1 || count > (1 << 20))
+    return fail(MOE_EINVAL, "%s: need between 1 and 2^20 tensors, got %d", what, count);
+  for (int i = 0; i < count; ++i) {
+    const moe_grad_tensor& g = list[i];
+    if (!dtype_ok(g.dtype)) return fail(MOE_EUNSUPPORTED, "%s: tensor %d: unknown dtype %d", what, i, g.dtype);
+    if (g.n < 0 || g.n > (1LL << 38))
+      return fail(MOE_EINVAL, "%s: tensor %d: need 0 <= n <= 2^38, got %lld", what, i, (long long)g.n);
+    if (g.n == 0) continue;
+    if (!g.grad || (outs && !g.out)) return fail(MOE_EINVAL, "%s: tensor %d: null pointer", what, i);
+    const uintptr_t es = g.dtype == MOE_DT_F32 ? 4 : 2;
+    if ((uintptr_t)g.grad % es || (outs && (uintptr_t)g.out % es))
+      return fail(MOE_EINVAL, "%s: tensor %d: not aligned to its type", what, i);
+  }
+  return MOE_OK;
+}
+
+size_t moe_grad_norm_workspace_bytes(int count) {
+  return count >= 1 && count <= (1 << 20) ? moe::grad_norm_workspace_bytes(count) : 0;
+}
+
+int moe_grad_norm(const moe_grad_tensor* list, int count, float* norm, void* ws, size_t ws_bytes,
+                  void* stream) {
+  if (!norm) return fail(MOE_EINVAL, "moe_grad_norm: null pointer");
+  int rc = grad_list_ok("moe_grad_norm", list, count, false);
+  if (rc != MOE_OK) return rc;
+  const size_t need = moe::grad_norm_workspace_bytes(count);
+  if (!ws || ws_bytes < need || (uintptr_t)ws % 8)
+    return fail(MOE_EWORKSPACE, "moe_grad_norm: workspace of %zu bytes, aligned to 8, needed, %zu given", need, ws_bytes);
+  rc = ensure_init();
+  if (rc != MOE_OK) return rc;
+  return launched(moe::launch_grad_norm(list, count, norm, (double*)ws, (hipStream_t)stream),
+                  "moe_grad_norm launch");
+}
+
+int moe_grad_clip(const moe_grad_tensor* list, int count, const float* norm, float max_norm,
+                  void* stream) {
+  if (!norm) return fail(MOE_EINVAL, "moe_grad_clip: null pointer");
+  if (!(max_norm >= 0.f && max_norm <= FLT_MAX))
+    return fail(MOE_EINVAL, "moe_grad_clip: max_norm must be finite and not negative");
+  int rc = grad_list_ok("moe_grad_clip", list, count, true);
+  if (rc != MOE_OK) return rc;
+  rc = ensure_init();
+  if (rc != MOE_OK) return rc;
+  return launched(moe::launch_grad_clip(list, count, norm, max_norm, (hipStream_t)stream),
+                  "moe_grad_clip launch");
 }
 
 int moe_timing_enable(int on) {

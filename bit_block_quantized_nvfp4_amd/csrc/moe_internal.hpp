@@ -144,6 +144,8 @@ uint64_t block_norm_threads(int T, int H, int dtype);
 uint64_t fp8_quant_threads(int T, int K);
 uint64_t fp8_linear_threads(int T, int N, int K);
 uint64_t fp8_expert_ffn_threads(const moe_fp8_weights& W, int T, int K);
+uint64_t dense_threads(int T, int H, int I);
+uint64_t int8_linear_threads(int T, int N);
 
 // Token sort and its gradients (moe_sort.hip).
 void register_sort_kernels(std::vector<const void*>& k);
@@ -194,5 +196,31 @@ hipError_t launch_fp8_stream_experts(const moe_fp8_weights& W, const uint16_t* x
                                      const int32_t* offsets, const int32_t* sorted_slot,
                                      const int32_t* groups, float* h, uint16_t* y,
                                      hipStream_t s);
+
+// The dense gated feed-forward block and its gradients (moe_dense.hip).
+void register_dense_kernels(std::vector<const void*>& k);
+size_t dense_ffn_workspace_bytes(int T, int H, int I);
+size_t dense_ffn_grad_workspace_bytes(int T, int H, int I);
+hipError_t launch_dense_ffn(const moe_dense_weights& W, const void* x, int T, void* y, void* gu,
+                            void* ws, hipStream_t s);
+hipError_t launch_dense_ffn_grad(const moe_dense_weights& W, const void* dy, const void* x,
+                                 const void* gu, int T, void* dx, void* dw_gu, void* dw_dn,
+                                 void* ws, hipStream_t s);
+
+// Products in 8-bit integers (moe_int8.hip).
+void register_int8_kernels(std::vector<const void*>& k);
+hipError_t launch_int8_quant(const void* x, int T, int K, int dtype, int8_t* codes, float* scales,
+                             hipStream_t s);
+size_t int8_linear_workspace_bytes(int T, int N, int K);
+hipError_t launch_int8_linear(const moe_int8_matrix& M, const void* x, int T, int dtype, int gated,
+                              void* out, void* ws, hipStream_t s);
+
+// The norm of many gradients and their scaling (moe_grad_norm.hip).
+void register_grad_norm_kernels(std::vector<const void*>& k);
+size_t grad_norm_workspace_bytes(int count);
+hipError_t launch_grad_norm(const moe_grad_tensor* g, int count, float* norm, double* ws,
+                            hipStream_t s);
+hipError_t launch_grad_clip(const moe_grad_tensor* g, int count, const float* norm, float max_norm,
+                            hipStream_t s);
 
 }  // namespace moe

@@ -1,9 +1,10 @@
 """Python binding of the C ABI (include/moe_nvfp4.h): argument marshalling only
-(csrc/binding.cpp does it for the sort, norm and e4m3 operators).
+(csrc/binding.cpp does it for the sort, norm, e4m3, dense block, 8-bit integer and
+gradient norm operators).
 
 Every function takes and returns torch tensors on the current HIP device and
-enqueues the library's kernels on torch's current stream (moe_layer and the sort,
-norm, combine and e4m3 operators: on their tensors' device, whichever is current,
+enqueues the library's kernels on torch's current stream (moe_layer and the
+operators of csrc/binding.cpp: on their tensors' device, whichever is current,
 and its current stream).  Outputs (and, unless
 given, workspaces) are allocated with torch; all arithmetic runs in the HIP
 kernels of libmoe_nvfp4.so.
@@ -12,7 +13,7 @@ from __future__ import annotations
 
 import ctypes
 from dataclasses import dataclass
-from typing import Optional
+from typing import List, Optional, Sequence
 
 import torch
 
@@ -28,7 +29,8 @@ __all__ = [
     "moe_expert_ffn_combine", "MOE_ACT_FP8_ROUTED", "MOE_ACT_FP8_SHARED",
     "moe_dispatch", "moe_dispatch_grad", "moe_combine_grad", "moe_route_topk_grad",
     "moe_block_norm", "moe_block_norm_grad", "FP8Matrix", "FP8Weights", "moe_fp8_quant",
-    "moe_fp8_linear", "moe_fp8_expert_ffn",
+    "moe_fp8_linear", "moe_fp8_expert_ffn", "DenseWeights", "moe_dense_ffn", "moe_dense_ffn_grad",
+    "Int8Matrix", "moe_int8_quant", "moe_int8_linear", "moe_grad_norm", "moe_grad_clip",
 ]
 
 
@@ -503,6 +505,78 @@ def moe_fp8_expert_ffn(W: FP8Weights, x: torch.Tensor, K: int, offsets: torch.Te
     return _lib.binding().fp8_expert_ffn(W.gu_codes, W.gu_scales, W.dn_codes, W.dn_scales, W.E, W.H,
                                          W.I, W.has_shared, x, K, offsets, sorted_slot, groups, ws,
                                          y_slots)
+
+
+@dataclass
+class DenseWeights:
+    """The weights of a dense gated feed-forward block (moe_dense_weights)."""
+    gu: torch.Tensor  # bf16 or float16 [2I, H]: gate rows, then up rows
+    dn: torch.Tensor  # the same type, [H, I]
+
+
+def moe_dense_ffn(W: DenseWeights, x: torch.Tensor, keep: bool = False,
+                  ws: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  gu_out: Optional[torch.Tensor] = None):
+    """(silu(x Wg^T) * (x Wu^T)) Wd^T for rows x [T, H] of the weights' type: y [T, H],
+    or (y, gu) with keep, gu [T, 2I] the projections that moe_dense_ffn_grad reads."""
+    return _lib.binding().dense_ffn(W.gu, W.dn, x, keep, ws, out, gu_out)
+
+
+def moe_dense_ffn_grad(W: DenseWeights, dy: torch.Tensor, x: torch.Tensor, gu: torch.Tensor,
+                       ws: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                       dw_gu: Optional[torch.Tensor] = None,
+                       dw_dn: Optional[torch.Tensor] = None):
+    """Gradients of moe_dense_ffn from that of y, with x and the projections gu of the
+    forward call: (dx, dw_gu, dw_dn) like x, W.gu and W.dn."""
+    return _lib.binding().dense_ffn_grad(W.gu, W.dn, dy, x, gu, ws, dx, dw_gu, dw_dn)
+
+
+@dataclass
+class Int8Matrix:
+    """A weight matrix in 8-bit integers with a float32 scale per row (output channel):
+    W[n][k] = codes[n][k] * scales[n]."""
+    codes: torch.Tensor   # int8 [N, K]
+    scales: torch.Tensor  # float32 [N]
+
+    @classmethod
+    def from_float(cls, w: torch.Tensor) -> "Int8Matrix":
+        """Quantise [N, K]: each row's largest magnitude becomes 127.  Done once, when
+        weights are laid out."""
+        v = w.float()
+        s = v.abs().amax(1).clamp_min(2.0 ** -100) / 127.0
+        return cls(torch.round(v / s[:, None]).clamp(-127, 127).to(torch.int8).contiguous(), s.contiguous())
+
+
+def moe_int8_quant(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
+                   scales: Optional[torch.Tensor] = None):
+    """Rows of x (bf16, float16 or float32 [T, K]) as 8-bit integers with a float32
+    scale per row: (codes int8 [T, K], scales [T])."""
+    return _lib.binding().int8_quant(x, codes, scales)
+
+
+def moe_int8_linear(M: Int8Matrix, x: torch.Tensor, gated: bool = False,
+                    ws: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x [T, K] times the matrix's transpose, [T, N] in x's type: x is quantised as by
+    moe_int8_quant, the sums are exact.  gated: the first half of the rows is a gate,
+    the result silu(first half) * second half, [T, N/2]."""
+    return _lib.binding().int8_linear(M.codes, M.scales, x, gated, ws, out)
+
+
+def moe_grad_norm(grads: Sequence[torch.Tensor], norm: Optional[torch.Tensor] = None,
+                  ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The norm of all gradients together (float32 [1]).  grads: a list of bf16, float16
+    or float32 tensors of any shapes, types mixed, on one device."""
+    return _lib.binding().grad_norm(grads, norm, ws)
+
+
+def moe_grad_clip(grads: Sequence[torch.Tensor], norm: torch.Tensor, max_norm: float,
+                  out: Optional[Sequence[torch.Tensor]] = None) -> List[torch.Tensor]:
+    """Every gradient times min(1, max_norm / (norm + 1e-6)), in place or into the
+    tensors of out.  norm is moe_grad_norm's, or one joined over processes.  Returns
+    the scaled tensors."""
+    _lib.binding().grad_clip(grads, norm, max_norm, out)
+    return list(grads if out is None else out)
 
 
 def timing_enable(on: bool = True) -> None:

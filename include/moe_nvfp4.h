@@ -14,8 +14,11 @@
  *
  * Around and beside the layer: the token sort by itself with its gradients
  * (moe_dispatch, moe_combine_grad, ...), the norms before and after a block
- * (moe_block_norm), and products in e4m3 with a scale per block of 128
- * (moe_fp8_linear, moe_fp8_expert_ffn).
+ * (moe_block_norm), products in e4m3 with a scale per block of 128
+ * (moe_fp8_linear, moe_fp8_expert_ffn), and the dense block beside the experts:
+ * its feed-forward in 16 bits with gradients (moe_dense_ffn), the norm of many
+ * gradients and their clipping (moe_grad_norm, moe_grad_clip), and products in
+ * 8-bit integers (moe_int8_linear).
  *
  * Sources.  The operations are the ones listed as the prefill ops of a MoE
  * layer that can change the logits (router GEMM + top-k, shared expert, routed
@@ -558,6 +561,117 @@ size_t moe_fp8_expert_ffn_workspace_bytes(int T, int K, int H, int I, int has_sh
 int moe_fp8_expert_ffn(const moe_fp8_weights* W, const uint16_t* x, int T, int K,
                        const int32_t* offsets, const int32_t* sorted_slot, const int32_t* groups,
                        uint16_t* y_slots, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * A dense gated feed-forward block in 16 bits (a layer without experts, or a shared
+ * expert while it trains), laid out like one group of moe_nvfp4_weights:
+ *
+ *   gu [2I][H]  rows 0..I-1 gate, I..2I-1 up;  dn [H][I];  both of dtype (MOE_DT_BF16
+ *   or MOE_DT_F16), as all rows of these entry points
+ *
+ * moe_dense_ffn:       g = x W_gate^T, u = x W_up^T, h = silu(g) u, y = h W_down^T
+ *   x, y [T][H]; gu_out [T][2I] (or NULL): g and u of every row, for the gradients
+ * moe_dense_ffn_grad:  with s = sigmoid(g) and dh = dy W_down
+ *   dg = dh u s (1 + g (1 - s)), du = dh g s
+ *   dx = dg W_gate + du W_up, dw_gu = [dg du]^T x, dw_dn = dy^T h
+ *   dy, x, dx [T][H], gu [T][2I] as kept, dw_gu and dw_dn like the weights
+ *
+ * Sums and the activation are f32; h, dg and du are rounded to dtype as the next
+ * product's operands, every output once.  A NaN or an infinity in a row of x (of dy)
+ * reaches that row of y (of dx) alone, and every weight gradient.
+ *
+ *   ws  at least moe_dense_ffn_workspace_bytes(T, H, I), or ..._grad_...(T, H, I)
+ *
+ * Limits: T >= 1, H and I multiples of 8 in [8, 65536], pointers aligned to 16 bytes,
+ * launches of fewer than 2^32 threads: at most max(T, H, 2I) max(H, 2I) / 32.
+ * Outputs and workspace may not overlap one another or the inputs.
+ */
+typedef struct moe_dense_weights {
+  const void* gu;
+  const void* dn;
+  int32_t H;
+  int32_t I;
+  int32_t dtype;
+} moe_dense_weights;
+
+size_t moe_dense_ffn_workspace_bytes(int T, int H, int I);
+int moe_dense_ffn(const moe_dense_weights* W, const void* x, int T, void* y, void* gu_out,
+                  void* ws, size_t ws_bytes, void* stream);
+size_t moe_dense_ffn_grad_workspace_bytes(int T, int H, int I);
+int moe_dense_ffn_grad(const moe_dense_weights* W, const void* dy, const void* x, const void* gu,
+                       int T, void* dx, void* dw_gu, void* dw_dn, void* ws, size_t ws_bytes,
+                       void* stream);
+
+/*
+ * Products in 8-bit integers with a scale per token and per channel.  A weight
+ * matrix W[n][k] = codes[n][k] scales[n]; a row x is quantised as a whole: a =
+ * max(absmax, 2^-100), scale s = a / 127, code = x (127 / a) to the nearest integer,
+ * ties to even, each operation rounded to f32.
+ *
+ *   codes [N][K] int8 (any of the 256), scales [N] float32
+ *
+ * moe_int8_quant writes the codes [T][K] and scales [T] of rows x.
+ *
+ * moe_int8_linear: z[t][n] = s[t] scales[n] sum_k code_x[t][k] codes[n][k], exact
+ * integer sums, then f32; gated 0: out = z, [T][N]; gated 1: rows 0..N/2-1 are a
+ * gate, the others its up projection, out[t][n] = silu(z[t][n]) z[t][N/2 + n],
+ * [T][N/2].  One rounding to dtype.
+ *
+ *   x [T][K], out of dtype
+ *   ws  at least moe_int8_linear_workspace_bytes(T, N, K) bytes
+ *
+ * A NaN or an infinity in a row makes its scale NaN and its codes zeros, so that
+ * row's outputs are NaN and no others.  The outputs may not overlap the inputs.
+ * Limits: K a multiple of 16 in [16, 65536], N a multiple of 8 (gated: 16) in
+ * [8, 131072], T >= 1, launches of fewer than 2^32 threads: 256 a row for the
+ * quantisation, N * T / 32 for the product; pointers of codes, x and out aligned to
+ * 16 bytes.
+ */
+typedef struct moe_int8_matrix {
+  const int8_t* codes;
+  const float* scales;
+  int32_t N;
+  int32_t K;
+} moe_int8_matrix;
+
+int moe_int8_quant(const void* x, int T, int K, int dtype, int8_t* codes, float* scales,
+                   void* stream);
+size_t moe_int8_linear_workspace_bytes(int T, int N, int K);
+int moe_int8_linear(const moe_int8_matrix* M, const void* x, int T, int dtype, int gated,
+                    void* out, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The norm of many gradients together, and their scaling to a limit:
+ *
+ *   norm = sqrt(sum over all tensors and values of g^2)
+ *   c = min(1, max_norm / (norm + 1e-6)) (NaN if norm is), out = c g
+ *
+ * list: `count` tensors on the host, read before the call returns: n values of
+ * dtype (MOE_DT_*, they may differ) at `grad`, and for moe_grad_clip as many at
+ * `out`, which may be `grad` itself (scaled in place).  Tensors may be empty and need
+ * no alignment beyond their type's (both sides of one alike is faster).  norm: one
+ * float32 on the device; a norm joined over several processes serves moe_grad_clip
+ * as well.  The squares are summed in 64 bits in an order that the sizes alone
+ * determine, so the norm is infinite only if it passes float32's range itself, or
+ * a value is; moe_grad_clip works in f32 and rounds once.
+ *
+ *   ws  at least moe_grad_norm_workspace_bytes(count) bytes, aligned to 8
+ *
+ * Limits: 1 <= count <= 2^20, 0 <= n <= 2^38, max_norm finite and >= 0.  No output
+ * may overlap another tensor of the list.
+ */
+typedef struct moe_grad_tensor {
+  const void* grad;
+  void* out;
+  int64_t n;
+  int32_t dtype;
+} moe_grad_tensor;
+
+size_t moe_grad_norm_workspace_bytes(int count);
+int moe_grad_norm(const moe_grad_tensor* list, int count, float* norm, void* ws, size_t ws_bytes,
+                  void* stream);
+int moe_grad_clip(const moe_grad_tensor* list, int count, const float* norm, float max_norm,
+                  void* stream);
 
 /*
  * Per-kernel timing, for measurement only.  While enabled, every kernel the
