@@ -17,8 +17,9 @@ namespace moe {
 template <int DT>
 struct PutLinear {
   static constexpr bool kGated = false;
+  typedef NoPre Pre;
   static __device__ __forceinline__ void put(const TileArgs16& a, int m, int n, const float (&v)[8],
-                                             const float (&)[8]) {
+                                             const float (&)[8], const Pre&) {
     put8<DT>(a.out, (size_t)m * a.N + n, v);
   }
 };
@@ -27,8 +28,9 @@ struct PutLinear {
 template <int DT, bool KEEP>
 struct PutGated {
   static constexpr bool kGated = true;
+  typedef NoPre Pre;
   static __device__ __forceinline__ void put(const TileArgs16& a, int m, int n, const float (&v)[8],
-                                             const float (&u)[8]) {
+                                             const float (&u)[8], const Pre&) {
     float h[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) h[e] = silu_f32(v[e]) * u[e];
@@ -44,22 +46,30 @@ struct PutGated {
 template <int DT>
 struct PutGatedGrad {
   static constexpr bool kGated = false;
+  struct Pre {
+    u32x4 g, u;
+    __device__ __forceinline__ void get(const TileArgs16& a, int m, int n) {
+      const uint16_t* p = (const uint16_t*)a.aux + (size_t)m * 2 * a.N + n;
+      g = *(const u32x4*)p;
+      u = *(const u32x4*)(p + a.N);
+    }
+  };
   static __device__ __forceinline__ void put(const TileArgs16& a, int m, int n, const float (&v)[8],
-                                             const float (&)[8]) {
+                                             const float (&)[8], const Pre& pre) {
     const size_t at = (size_t)m * 2 * a.N + n;
     float g[8], u[8], h[8], dg[8], du[8];
-    get8<DT>(a.aux, at, g);
-    get8<DT>(a.aux, at + a.N, u);
+    Chunk<DT>::unpack(pre.g, g);
+    Chunk<DT>::unpack(pre.u, u);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      // 1 - s by itself, not as a difference
-      const float x = g[e] * 1.4426950408889634f;
-      const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-x));
-      const float rest = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x));
-      const float gs = g[e] * s;
-      h[e] = gs * u[e];
-      du[e] = v[e] * gs;
-      dg[e] = v[e] * u[e] * (s + gs * rest);
+    for (int i = 0; i < 8; ++i) {
+      // e = exp(-g), s = 1 / (1 + e), 1 - s = e s: no difference that would lose its
+      // bits (with e infinite s is 0, and so is what 1 - s is multiplied with)
+      const float e = __builtin_amdgcn_exp2f(g[i] * -1.4426950408889634f);
+      const float s = __builtin_amdgcn_rcpf(1.0f + e);
+      const float gs = g[i] * s;
+      h[i] = gs * u[i];
+      du[i] = v[i] * gs;
+      dg[i] = v[i] * u[i] * fmaf(gs, fminf(e, 0x1p100f) * s, s);
     }
     put8<DT>(a.out, at, dg);
     put8<DT>(a.out, at + a.N, du);
@@ -71,9 +81,9 @@ struct PutGatedGrad {
 constexpr int kDenseShapes = 3;
 template <int DT, bool BROWS, bool AROWS, class EP, typename F>
 static void by_tile(int shape, F&& f) {
-  if (shape == 0) f(&k_tile<DT, BROWS, AROWS, EP, 256, 256, 4, 2, 2>, 256, 256, 512);
-  if (shape == 1) f(&k_tile<DT, BROWS, AROWS, EP, 128, 128, 2, 2, 2>, 128, 128, 256);
-  if (shape == 2) f(&k_tile<DT, BROWS, AROWS, EP, 64, 64, 1, 2, 4>, 64, 64, 128);
+  if (shape == 0) f(&k_tile<DT, BROWS, AROWS, EP, 256, 256, 2, 2, 128, 2, 3>, 256, 256, 256);
+  if (shape == 1) f(&k_tile<DT, BROWS, AROWS, EP, 128, 128, 2, 2, 128, 2, 2>, 128, 128, 256);
+  if (shape == 2) f(&k_tile<DT, BROWS, AROWS, EP, 64, 64, 1, 2, 128, 4, 4>, 64, 64, 128);
 }
 
 // The shape whose rounds of 256 blocks take the least time together.

@@ -23,8 +23,9 @@ __device__ __forceinline__ float scaled(float sum, float s, float w) {
 template <int DT>
 struct PutInt8 {
   static constexpr bool kGated = false;
+  typedef NoPre Pre;
   static __device__ __forceinline__ void put(const TileArgs16& a, int m, int n, float (&v)[8],
-                                             const float (&)[8]) {
+                                             const float (&)[8], const Pre&) {
     const float s = a.sm[m];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = scaled(v[e], s, a.sn[n + e]);
@@ -35,8 +36,9 @@ struct PutInt8 {
 template <int DT>
 struct PutInt8Gated {
   static constexpr bool kGated = true;
+  typedef NoPre Pre;
   static __device__ __forceinline__ void put(const TileArgs16& a, int m, int n, float (&v)[8],
-                                             const float (&u)[8]) {
+                                             const float (&u)[8], const Pre&) {
     const float s = a.sm[m];
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -103,9 +105,9 @@ hipError_t launch_int8_quant(const void* x, int T, int K, int dtype, int8_t* cod
 constexpr int kInt8Shapes = 3;
 template <class EP, typename F>
 static void by_tile(int shape, F&& f) {
-  if (shape == 0) f(&k_tile<kElI8, false, false, EP, 256, 256, 4, 2, 2>, 256, 256, 512);
-  if (shape == 1) f(&k_tile<kElI8, false, false, EP, 128, 128, 2, 2, 2>, 128, 128, 256);
-  if (shape == 2) f(&k_tile<kElI8, false, false, EP, 64, 64, 1, 2, 4>, 64, 64, 128);
+  if (shape == 0) f(&k_tile<kElI8, false, false, EP, 256, 256, 2, 2, 128, 2, 3>, 256, 256, 256);
+  if (shape == 1) f(&k_tile<kElI8, false, false, EP, 128, 128, 2, 2, 128, 2, 2>, 128, 128, 256);
+  if (shape == 2) f(&k_tile<kElI8, false, false, EP, 64, 64, 1, 2, 128, 4, 4>, 64, 64, 128);
 }
 
 // The shape whose rounds of 256 blocks take the least time together.

@@ -6,15 +6,14 @@
 // stands in memory with k running fastest, or (16 bits) with its rows running
 // fastest: the transposed matrix, as the gradients need it.
 //
-// A block computes BN columns of BM rows in steps of 128 bytes along K (64 or 128
-// values).  Both operands go from memory to LDS without registers, 16 bytes a
-// lane, NBUF steps deep; a step's products then run on the 32x32 MFMA with sums in
-// 32 bits.  B is the MFMA's first operand, so a lane holds four consecutive outputs
-// of a row.
+// A block computes BN columns of BM rows in steps of SB = 64 or 128 bytes along K.
+// Both operands go from memory to LDS without registers, 16 bytes a lane, A's NA and
+// B's NB steps deep; a step's products then run on the 32x32 MFMA with sums in 32 bits.
+// B is the MFMA's first operand, so a lane holds four consecutive outputs of a row.
 //
-// LDS.  k fastest: a row of a step is 128 bytes, its 16-byte chunk c stands at
-// place c ^ (row / 2 % 8), so that the 16 rows that one cycle of a 16-byte read
-// serves meet all 64 banks.  Rows fastest: a k is a line of BN (BM) values, read with
+// LDS.  k fastest: a row of a step is SB bytes, its 16-byte chunk c stands at place
+// c ^ (row / (256 / SB) % (SB / 16)), so that the 16 rows that one cycle of a
+// 16-byte read serves meet all 64 banks.  Rows fastest: a k is a line of BN (BM) values, read with
 // the transposing load: 16 lanes get four k of 16 rows; its chunks are permuted so
 // that the four lines of such a load meet different banks.  The loads to LDS write
 // lanes in order, so both permutations are applied to the addresses they read.
@@ -78,7 +77,6 @@ struct TileArgs16 {
   const float* sn;
 };
 
-constexpr int kStepBytes = 128;
 constexpr uint32_t kNowhere = 0x80000000u;  // past the end of every buffer (all below 2^31 bytes)
 
 // Permutation of the 16-byte chunks of a line: rows fastest, a line of CPR chunks.
@@ -88,24 +86,25 @@ __device__ __forceinline__ int line_swz(int k) {
 }
 
 // One operand of a block: R rows of it, ROWS fastest or k fastest, brought by NT
-// threads.  GROUP (gated): every run of GROUP rows is half a run of gate rows, half
-// the up rows of the same columns, which stand `up` bytes behind.
-template <int ES, bool ROWS, int R, int NT, int GROUP>
+// threads.  GATED: the first half of the rows are gate rows, the second the up rows of
+// the same columns, which stand `up` bytes behind.
+template <int ES, bool ROWS, int R, int NT, bool GATED, int SB>
 struct Operand {
-  static constexpr int kLoads = R * 8 / NT;  // per thread and step
-  static constexpr int CPR = R / 8;          // chunks of a line (rows fastest)
-  static constexpr int KS = kStepBytes / ES; // values of K in a step
-  static_assert(R * 8 % NT == 0 && (!ROWS || ES == 2), "operand shape");
+  static constexpr int kC = SB / 16;           // chunks of a row and step
+  static constexpr int kLoads = R * kC / NT;   // per thread and step
+  static constexpr int CPR = R / 8;            // chunks of a line (rows fastest)
+  static constexpr int KS = SB / ES;           // values of K in a step
+  static_assert(R * kC % NT == 0 && NT % 128 == 0 && (!ROWS || (ES == 2 && !GATED)) && (!GATED || kLoads % 2 == 0),
+                "operand shape");
   const char* base;
   const char* up;
   uint32_t ld, kbytes, width;                // width: rows' bytes (ROWS) or bytes of the tile
   uint32_t off[kLoads];
   int chunk;
-  bool upper[kLoads];
 
   // first: the tile's first row; left: rows from there on; K values along K
   __device__ __forceinline__ void set(const void* p, uint32_t ld_, long first, int left, int K,
-                                      long up_bytes, int tid, int wv) {
+                                      long up_bytes, int tid) {
     ld = ld_;
     kbytes = (uint32_t)K * ES;
     if constexpr (ROWS) {
@@ -119,54 +118,51 @@ struct Operand {
     } else {
       base = (const char*)p + first * (long)ld;
       up = base + up_bytes;
-      constexpr int RR = GROUP ? R / 2 : R;
+      constexpr int RR = GATED ? R / 2 : R;
       width = (uint32_t)min(left, RR) * ld;
-      chunk = 16 * ((tid & 7) ^ ((tid >> 4) & 7));
+      chunk = 16 * ((tid % kC) ^ ((tid >> 4) % kC));  // row / (16 / kC) = tid / 16
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int lr = (i * NT + tid) >> 3;
-        int row = lr;
-        if constexpr (GROUP > 0) {
-          constexpr int HG = GROUP / 2;
-          row = lr / GROUP * HG + lr % HG;
-          upper[i] = (i * (NT / 8) + wv * 8) % GROUP >= HG;
-        }
-        off[i] = (uint32_t)row * ld + chunk;
+        off[i] = (uint32_t)((i * NT + tid) / kC % RR) * ld + chunk;
       }
     }
   }
-  // The loads of step s to the LDS address lds (the wave's share of it).
-  __device__ __forceinline__ void bring(int s, uint32_t lds) const {
+  // What the loads of a step share.
+  struct Step {
+    u32x4 buf, ubuf;
+    uint32_t so;
+    bool in;
+  };
+  __device__ __forceinline__ Step begin(int s) const {
+    Step t;
     if constexpr (ROWS) {
       const int k0 = s * KS, kn = min((int)(kbytes / ES) - k0, KS);
-      u32x4 buf = buf_of(base + (size_t)k0 * ld, kn > 0 ? (uint32_t)(kn - 1) * ld + width : 0u);
-      asm volatile("s_nop 4" : "+s"(buf));  // as in dma_offset
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) dma_b128(buf, off[i], 0, lds + i * NT * 16);
+      t.buf = buf_of(base + (size_t)k0 * ld, kn > 0 ? (uint32_t)(kn - 1) * ld + width : 0u);
+      asm volatile("s_nop 4" : "+s"(t.buf));  // as in dma_offset
     } else {
-      const uint32_t ko = (uint32_t)s * kStepBytes;
-      u32x4 buf = buf_of(base, width);
-      asm volatile("s_nop 4" : "+s"(buf));
-      u32x4 ubuf;
-      if constexpr (GROUP > 0) {
-        ubuf = buf_of(up, width);
-        asm volatile("s_nop 4" : "+s"(ubuf));
+      const uint32_t ko = (uint32_t)s * SB;
+      t.buf = buf_of(base, width);
+      asm volatile("s_nop 4" : "+s"(t.buf));
+      if constexpr (GATED) {
+        t.ubuf = buf_of(up, width);
+        asm volatile("s_nop 4" : "+s"(t.ubuf));
       }
-      const bool in = ko + chunk < kbytes;
-      const uint32_t so = dma_offset(min(ko, kbytes));
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        if constexpr (GROUP > 0)
-          dma_b128(upper[i] ? ubuf : buf, in ? off[i] : kNowhere, so, lds + i * NT * 16);
-        else
-          dma_b128(buf, in ? off[i] : kNowhere, so, lds + i * NT * 16);
-      }
+      t.in = ko + chunk < kbytes;
+      t.so = dma_offset(min(ko, kbytes));
     }
+    return t;
+  }
+  // Load i of a step to the LDS address lds (the wave's share of it).
+  __device__ __forceinline__ void load(const Step& t, int i, uint32_t lds) const {
+    if constexpr (ROWS)
+      dma_b128(t.buf, off[i], 0, lds + i * NT * 16);
+    else
+      dma_b128(GATED && i >= kLoads / 2 ? t.ubuf : t.buf, t.in ? off[i] : kNowhere, t.so, lds + i * NT * 16);
   }
 };
 
 // 32 rows from `row` of an operand in LDS, the ks-th 32 bytes of the step.
-template <bool ROWS, int R>
+template <bool ROWS, int R, int SB>
 __device__ __forceinline__ u32x4 operand_at(const lds_u8* p, int row, int ks, int lane) {
   if constexpr (ROWS) {
     constexpr int CPR = R / 8, LINE = R * 2;
@@ -180,27 +176,34 @@ __device__ __forceinline__ u32x4 operand_at(const lds_u8* p, int row, int ks, in
   } else {
     const int fr = lane & 31, fq = lane >> 5;
     return *(const __attribute__((address_space(3))) u32x4*)(
-        p + (row + fr) * kStepBytes + (((fq + 2 * ks) ^ ((fr >> 1) & 7)) << 4));
+        p + (row + fr) * SB + (((fq + 2 * ks) ^ (fr / (256 / SB) % (SB / 16))) << 4));
   }
 }
 
+// An epilogue that reads nothing from memory ahead.
+struct NoPre {
+  __device__ __forceinline__ void get(const TileArgs16&, int, int) {}
+};
+
 // EP: the epilogue.  EP::kGated: a wave's columns are TN / 2 gates and the TN / 2 ups of
-// the same outputs; EP::put(a, m, n, v, u): outputs n .. n + 7 of row m (both inside)
-// from the sums v (and u, the ups).
-template <int EL, bool BROWS, bool AROWS, class EP, int BN, int BM, int WN, int WM, int NBUF>
+// the same outputs; EP::put(a, m, n, v, u, pre): outputs n .. n + 7 of row m (both
+// inside) from the sums v (and u, the ups) and what EP::Pre::get(a, m, n) has read.
+template <int EL, bool BROWS, bool AROWS, class EP, int BN, int BM, int WN, int WM, int SB, int NA, int NB>
 __global__ __launch_bounds__(64 * WN * WM) void k_tile(TileArgs16 a) {
   constexpr int NW = WN * WM, NT = 64 * NW;
   constexpr int TN = BN / WN, TM = BM / WM;
   constexpr int FN = TN / 32, FM = TM / 32;
   constexpr int ES = EL == kElI8 ? 1 : 2;
-  constexpr int kBuf = (BN + BM) * kStepBytes;
+  constexpr int kA = BM * SB, kB = BN * SB, kLds = NA * kA + NB * kB;  // bytes of a step, of all
+  constexpr int KF = SB / 32;                                // products along K of a step
   constexpr bool G = EP::kGated;
   constexpr int BC = G ? BN / 2 : BN, TC = G ? TN / 2 : TN;  // outputs of a tile and of a wave
   constexpr int CH = TN / 4;                                 // 16-byte chunks of a staged row
   typedef typename Mma<EL>::Acc Acc;
-  static_assert(TN % 32 == 0 && TM % 32 == 0 && (!G || FN % 2 == 0) && NBUF >= 2, "tile shape");
-  static_assert(NW * 16 * TN * 4 <= NBUF * kBuf && (CH & (CH - 1)) == 0, "staged rows");
-  __shared__ __align__(1024) uint8_t lds[NBUF * kBuf];
+  static_assert(TN % 32 == 0 && TM % 32 == 0 && (!G || FN % 2 == 0) && NA >= 2 && NB >= NA, "tile shape");
+  constexpr int kStage = 32 * TN * 4;                        // bytes of 32 staged rows
+  static_assert(NW * 2 * kStage <= kLds && CH <= 32 && (CH & (CH - 1)) == 0, "staged rows");
+  __shared__ __align__(1024) uint8_t lds[kLds];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wv % WN, wm = wv / WN;
@@ -215,95 +218,160 @@ __global__ __launch_bounds__(64 * WN * WM) void k_tile(TileArgs16 a) {
   const int m0 = __builtin_amdgcn_readfirstlane((grp * 8 + in % gm) * BM);
   const int n0 = __builtin_amdgcn_readfirstlane((in / gm) * BC);
 
-  typedef Operand<ES, BROWS, BN, NT, G ? TN : 0> OpB;
-  typedef Operand<ES, AROWS, BM, NT, 0> OpA;
-  constexpr int D = OpB::kLoads + OpA::kLoads;
-  static_assert((NBUF - 1) * D < 64, "loads under way");
+  typedef Operand<ES, BROWS, BN, NT, G, SB> OpB;
+  typedef Operand<ES, AROWS, BM, NT, false, SB> OpA;
+  constexpr int LA = OpA::kLoads, D = LA + OpB::kLoads;
+  // loads that a wave may have under way where it waits for the next step's
+  constexpr int kAhead = (NA - 2) * D + (NB > NA ? D - LA : 0);
+  static_assert(kAhead + D < 64, "loads under way");
   OpB ob;
   OpA oa;
-  ob.set(a.b, a.ldb, n0, a.N - n0, a.K, (long)a.N * a.ldb, tid, wv);
-  oa.set(a.a, a.lda, m0, a.M - m0, a.K, 0, tid, wv);
+  ob.set(a.b, a.ldb, n0, a.N - n0, a.K, (long)a.N * a.ldb, tid);
+  oa.set(a.a, a.lda, m0, a.M - m0, a.K, 0, tid);
   lds_u8* const l0 = (lds_u8*)lds;
   const uint32_t ldsw = (uint32_t)(uintptr_t)l0 + wv * 1024;
-  const int steps = (a.K * ES + kStepBytes - 1) / kStepBytes;
+  const int steps = (a.K * ES + SB - 1) / SB;
 
-  // Steps past the last one are brought too, as zeros from outside the buffers, so
-  // that every wave has the same loads under way at every wait.
-  int d_at = 0;
-  auto bring = [&](int s) __attribute__((always_inline)) {
-    oa.bring(s, ldsw + d_at + BN * kStepBytes);
-    ob.bring(s, ldsw + d_at);
-    d_at = d_at == (NBUF - 1) * kBuf ? 0 : d_at + kBuf;
+  // Step s's turn at the buffers that step s - 1 leaves: the loads of A's step s - 1 + NA,
+  // then of B's step s - 1 + NB.  Steps past the last one are brought too, as zeros
+  // from outside the operands, so that every wave has the same loads under way at
+  // every wait.
+  int a_at = 0, b_at = 0;
+  typename OpB::Step tb;
+  typename OpA::Step ta;
+  auto begin = [&](int s) __attribute__((always_inline)) {
+    ta = oa.begin(s - 1 + NA);
+    tb = ob.begin(s - 1 + NB);
   };
+  auto load = [&](int i) __attribute__((always_inline)) {
+    if (i < LA) oa.load(ta, i, ldsw + NB * kB + a_at);
+    else ob.load(tb, i - LA, ldsw + b_at);
+    if (i == LA - 1) a_at = a_at == (NA - 1) * kA ? 0 : a_at + kA;
+    if (i == D - 1) b_at = b_at == (NB - 1) * kB ? 0 : b_at + kB;
+  };
+  constexpr int L = D / KF;  // loads that go with the first products
 #pragma unroll
-  for (int s = 0; s < NBUF - 1; ++s) bring(s);
+  for (int s = 1 - NB; s <= 0; ++s) {
+    begin(s);
+#pragma unroll
+    for (int i = s > -NA ? 0 : LA; i < (s < 0 ? D : L); ++i) load(i);
+  }
 
   Acc acc[FN][FM];
 #pragma unroll
   for (int i = 0; i < FN; ++i)
 #pragma unroll
     for (int j = 0; j < FM; ++j) acc[i][j] = Acc{};
-  int at = 0;
-  for (int s = 0; s < steps; ++s) {
-    wait_step<(NBUF - 2) * D>();
-    bring(s + NBUF - 1);
-    const lds_u8* pb = l0 + at;
-    const lds_u8* pa = pb + BN * kStepBytes;
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      u32x4 fb[FN], fa[FM];
-#pragma unroll
-      for (int i = 0; i < FN; ++i) fb[i] = operand_at<BROWS, BN>(pb, wn * TN + 32 * i, ks, lane);
-#pragma unroll
-      for (int j = 0; j < FM; ++j) fa[j] = operand_at<AROWS, BM>(pa, wm * TM + 32 * j, ks, lane);
-#pragma unroll
-      for (int i = 0; i < FN; ++i)
-#pragma unroll
-        for (int j = 0; j < FM; ++j) acc[i][j] = Mma<EL>::go(fb[i], fa[j], acc[i][j]);
+  struct Frags {
+    u32x4 b[FN], a[FM];
+  };
+  // Operand r of the ks-th 32 bytes of the step at pa and pb: b's first, all of a's, then
+  // b's others.
+  const lds_u8 *pa = l0 + NB * kB, *pb = l0;
+  auto read = [&](Frags& f, int r, int ks) __attribute__((always_inline)) {
+    if (r > 0 && r <= FM) f.a[r - 1] = operand_at<AROWS, BM, SB>(pa, wm * TM + 32 * (r - 1), ks, lane);
+    else {
+      const int i = r ? r - FM : 0;
+      // gated: a wave's columns are gates, then the ups of the same outputs
+      const int row = !G ? wn * TN + 32 * i : wn * TC + 32 * i + (i < FN / 2 ? 0 : BN / 2 - TC);
+      f.b[i] = operand_at<BROWS, BN, SB>(pb, row, ks, lane);
     }
-    at = at == (NBUF - 1) * kBuf ? 0 : at + kBuf;
+  };
+  // The products of f, and between them the reads of g, the operands of the next ones,
+  // and the part'th share of the loads of the step under way: any of these in one piece would
+  // hold up the wave with its matrix unit idle.
+  auto multiply = [&](const Frags& f, Frags& g, int ks, int part) __attribute__((always_inline)) {
+    constexpr int M = FN * FM, R = FN + FM;
+    const int from = part * D / KF, n = (part + 1) * D / KF - from;
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FM; ++j) {
+        const int m = i * FM + j;
+        acc[i][j] = Mma<EL>::go(f.b[i], f.a[j], acc[i][j]);
+        if (m < R) read(g, m, ks);
+        if (m == M - 1)
+#pragma unroll
+          for (int r = M; r < R; ++r) read(g, r, ks);
+#pragma unroll
+        for (int d = 0; d < n; ++d)
+          if ((2 * d + 1) * M / (2 * n) == m) load(from + d);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+  };
+  // A step's buffers are free once every wave has read its last operands.  The waves
+  // meet there, before the products of these; from there on the buffers are filled
+  // again.  A's, which are wanted sooner, come first.
+  wait_step<kAhead + L>();
+  Frags f[2];  // of these and of the next products, in turn
+#pragma unroll
+  for (int r = 0; r < FN + FM; ++r) read(f[0], r, 0);
+  for (int s = 0; s < steps; ++s) {
+#pragma unroll
+    for (int ks = 0; ks < KF; ++ks) {
+      const int next = ks + 1 == KF ? 0 : ks + 1;
+      if (next == 0) {
+        begin(s + 1);
+        wait_step<kAhead>();
+        pa = pa == l0 + NB * kB + (NA - 1) * kA ? l0 + NB * kB : pa + kA;
+        pb = pb == l0 + (NB - 1) * kB ? l0 : pb + kB;
+      }
+      multiply(f[ks & 1], f[1 - (ks & 1)], next, next);
+    }
   }
   wait_step<0>();  // nothing is under way to LDS, nothing is read from it any more
 
-  // The wave's sums, 16 rows at a time, through LDS of its own: a lane then has
-  // eight consecutive outputs of a row, and memory is read and written in whole
-  // pieces of rows.  Chunk c of a staged row stands at c ^ (row % chunks), for the
-  // banks.  A wave's LDS operations keep their order.
-  uint8_t* mine = lds + wv * (16 * TN * 4);
-  constexpr int LR = TC / 8, RP = 64 / LR;  // lanes of a row, rows of a pass
+  // The wave's sums, 32 rows at a time, through LDS of its own (two places in turn): a
+  // lane then has eight consecutive outputs of a row, and memory is read and written
+  // in whole pieces of rows.  Chunk c of a staged row stands at c ^ (row % chunks), for
+  // the banks.  A wave's LDS operations keep their order.  What the epilogue reads from
+  // memory is asked for 32 rows ahead.
+  constexpr int LR = TC / 8, RP = 64 / LR, P = 32 / RP;  // lanes of a row, rows of a pass, passes
   const int fr = lane & 31, fq = lane >> 5;
-  const int c8 = lane % LR, n = n0 + wn * TC + 8 * c8;
+  const int r0 = lane / LR, c8 = lane % LR, n = n0 + wn * TC + 8 * c8;
+  lds_u8* const mine = l0 + wv * (2 * kStage);
+  auto stage = [&](int j) __attribute__((always_inline)) {
 #pragma unroll
-  for (int jh = 0; jh < 2 * FM; ++jh) {
-    const int j = jh / 2;
-    if (fr / 16 == jh % 2) {
-      const int r = fr & 15;
+    for (int i = 0; i < FN; ++i)
 #pragma unroll
-      for (int i = 0; i < FN; ++i)
+      for (int g = 0; g < 4; ++g)
+        *(__attribute__((address_space(3))) f32x4*)(mine + j % 2 * kStage + fr * (TN * 4) +
+                                                    (((8 * i + 2 * g + fq) ^ (fr & (CH - 1))) << 4)) =
+            f32x4{(float)acc[i][j][4 * g], (float)acc[i][j][4 * g + 1], (float)acc[i][j][4 * g + 2],
+                  (float)acc[i][j][4 * g + 3]};
+  };
+  auto row_of = [&](int j, int q) __attribute__((always_inline)) { return m0 + wm * TM + 32 * j + q * RP + r0; };
+  typename EP::Pre pre[2][P];
+  auto fetch = [&](int j) __attribute__((always_inline)) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-          *(f32x4*)(mine + r * (TN * 4) + (((8 * i + 2 * g + fq) ^ (r & (CH - 1))) << 4)) =
-              f32x4{(float)acc[i][j][4 * g], (float)acc[i][j][4 * g + 1], (float)acc[i][j][4 * g + 2],
-                    (float)acc[i][j][4 * g + 3]};
+    for (int q = 0; q < P; ++q)
+      if (row_of(j, q) < a.M && n < a.N) pre[j % 2][q].get(a, row_of(j, q), n);
+  };
+  fetch(0);
+  stage(0);
+#pragma unroll
+  for (int j = 0; j < FM; ++j) {
+    if (j + 1 < FM) {
+      fetch(j + 1);
+      stage(j + 1);
     }
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int r0 = 0; r0 < 16; r0 += RP) {
-      const int r = r0 + lane / LR, m = m0 + wm * TM + 16 * jh + r;
+    for (int q = 0; q < P; ++q) {
+      const int r = q * RP + r0, m = row_of(j, q);
       float v[8], u[8];
       auto row8 = [&](int c, float (&f)[8]) __attribute__((always_inline)) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const f32x4 w = *(const f32x4*)(mine + r * (TN * 4) + (((c + h) ^ (r & (CH - 1))) << 4));
+          const f32x4 w = *(const __attribute__((address_space(3))) f32x4*)(
+              mine + j % 2 * kStage + r * (TN * 4) + (((c + h) ^ (r & (CH - 1))) << 4));
 #pragma unroll
           for (int e = 0; e < 4; ++e) f[4 * h + e] = w[e];
         }
       };
-      if (r < 16 && m < a.M && n < a.N) {
-        row8(2 * c8, v);
-        if (G) row8(TC / 4 + 2 * c8, u);
-        EP::put(a, m, n, v, u);
-      }
+      row8(2 * c8, v);
+      if (G) row8(TC / 4 + 2 * c8, u);
+      if (m < a.M && n < a.N) EP::put(a, m, n, v, u, pre[j % 2][q]);
     }
     __builtin_amdgcn_wave_barrier();
   }
@@ -319,10 +387,6 @@ __device__ __forceinline__ void put8(void* p, size_t at, const float (&v)[8]) {
   } else {
     *(u32x4*)((uint16_t*)p + at) = Chunk<DT>::pack(v);
   }
-}
-template <int DT>
-__device__ __forceinline__ void get8(const void* p, size_t at, float (&v)[8]) {
-  Chunk<DT>::unpack(*(const u32x4*)((const uint16_t*)p + at), v);
 }
 
 }  // namespace moe
