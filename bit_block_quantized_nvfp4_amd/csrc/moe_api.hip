@@ -94,6 +94,7 @@ int ensure_init() {
   moe::register_fp8_stream_kernels(ks);
   moe::register_fp8_tile_kernels(ks);
   moe::register_dense_kernels(ks);
+  moe::register_dense_grad_kernels(ks);
   moe::register_int8_kernels(ks);
   moe::register_grad_norm_kernels(ks);
   for (const void* k : ks) {

@@ -5,54 +5,14 @@
 //
 // and, gated, silu of the first half of the columns times the second.  The sums are
 // exact in 32-bit integers: |sum| <= 127 128 K < 2^31 for K <= 65536.
+#include "moe_int8.hpp"
+#include "moe_stream.hpp"
 #include "moe_tile.hpp"
 
 namespace moe {
 
-// z from the sum and its two scales, each product rounded to f32: not joined with the
-// rounding to f16 that follows (one instruction does both), so that every type has the
-// same z.
-__device__ __forceinline__ float scaled(float sum, float s, float w) {
-#pragma clang fp contract(off)
-  float z = sum * s;
-  z = z * w;
-  asm("" : "+v"(z));
-  return z;
-}
-
-template <int DT>
-struct PutInt8 {
-  static constexpr bool kGated = false;
-  typedef NoPre Pre;
-  static __device__ __forceinline__ void put(const TileArgs16& a, int m, int n, float (&v)[8],
-                                             const float (&)[8], const Pre&) {
-    const float s = a.sm[m];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = scaled(v[e], s, a.sn[n + e]);
-    put8<DT>(a.out, (size_t)m * a.N + n, v);
-  }
-};
-
-template <int DT>
-struct PutInt8Gated {
-  static constexpr bool kGated = true;
-  typedef NoPre Pre;
-  static __device__ __forceinline__ void put(const TileArgs16& a, int m, int n, float (&v)[8],
-                                             const float (&u)[8], const Pre&) {
-    const float s = a.sm[m];
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      v[e] = silu_f32(scaled(v[e], s, a.sn[n + e])) * scaled(u[e], s, a.sn[a.N + n + e]);
-    put8<DT>(a.out, (size_t)m * a.N + n, v);
-  }
-};
-
-// Largest magnitude so far: a NaN stays.
-__device__ __forceinline__ float amax_nan(float a, float b) { return b > a || b != b ? b : a; }
-
-// A block quantises a row: 16 values a thread at a time, twice over the row (its
-// absmax, then the codes, from the L2).  A NaN or an infinity makes the scale NaN
-// and the codes zeros, so the row's outputs are NaN, and no other row's.
+// A block quantises a row: 16 bytes a thread at a time, twice over the row (its absmax,
+// then the codes, from the L2).
 template <int DT>
 __global__ __launch_bounds__(256) void k_int8_quant(const void* __restrict__ x, int K,
                                                     uint8_t* __restrict__ codes,
@@ -73,23 +33,17 @@ __global__ __launch_bounds__(256) void k_int8_quant(const void* __restrict__ x, 
   if ((tid & 63) == 0) part[tid >> 6] = am;
   __syncthreads();
   am = amax_nan(amax_nan(part[0], part[1]), amax_nan(part[2], part[3]));
-  const bool fine = am <= 3.402823466e38f;
-  am = am < 0x1p-100f ? 0x1p-100f : am;
-  const float m = 127.0f / am;
+  float mul, scale;
+  bool fine;
+  int8_scale(am, &mul, &scale, &fine);
   uint32_t* q = (uint32_t*)(codes + (size_t)t * K);
   for (int c = tid; c < K / N; c += 256) {
     float f[N];
     Chunk<DT>::unpack(p[c], f);
 #pragma unroll
-    for (int w = 0; w < N / 4; ++w) {
-      uint32_t o = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        o |= ((uint32_t)(fine ? (int)rintf(f[4 * w + j] * m) : 0) & 0xFFu) << (8 * j);
-      q[c * (N / 4) + w] = o;
-    }
+    for (int w = 0; w < N / 4; ++w) q[c * (N / 4) + w] = int8x4(f + 4 * w, mul, fine);
   }
-  if (tid == 0) scales[t] = fine ? am / 127.0f : __uint_as_float(0x7FC00000u);
+  if (tid == 0) scales[t] = scale;
 }
 
 hipError_t launch_int8_quant(const void* x, int T, int K, int dtype, int8_t* codes, float* scales,
@@ -101,76 +55,91 @@ hipError_t launch_int8_quant(const void* x, int T, int K, int dtype, int8_t* cod
   return hipGetLastError();
 }
 
-// Tile shapes, largest first: f with the kernel, BN, BM and threads.
-constexpr int kInt8Shapes = 3;
-template <class EP, typename F>
-static void by_tile(int shape, F&& f) {
-  if (shape == 0) f(&k_tile<kElI8, false, false, EP, 256, 256, 2, 2, 128, 2, 3>, 256, 256, 256);
-  if (shape == 1) f(&k_tile<kElI8, false, false, EP, 128, 128, 2, 2, 128, 2, 2>, 128, 128, 256);
-  if (shape == 2) f(&k_tile<kElI8, false, false, EP, 64, 64, 1, 2, 128, 4, 4>, 64, 64, 128);
-}
-
-// The shape whose rounds of 256 blocks take the least time together.
-static int tile_shape(int M, int N) {
-  constexpr int size[kInt8Shapes] = {256, 128, 64};
-  constexpr int cost[kInt8Shapes] = {100, 30, 10};
-  int best = 0;
-  long least = 0;
-  for (int s = 0; s < kInt8Shapes; ++s) {
-    const long tiles = (long)((N + size[s] - 1) / size[s]) * ((M + size[s] - 1) / size[s]);
-    const long t = (tiles + 255) / 256 * cost[s];
-    if (least == 0 || t < least) least = t, best = s;
+// Up to 16 rows stream the weights.  Where the rows are few values they are quantised in
+// the same launch, which every block repeats; else in one of their own.  The shapes: f
+// with the kernel, outputs and threads of a block.
+static bool int8_streams(int T) { return T <= kStreamRows; }
+static bool int8_joins(int T, int K) { return int8_streams(T) && (long)T * K <= 16384; }
+template <int XDT, class EP, typename F>
+static void by_stream(int K, F&& f) {
+  if constexpr (EP::kGated) {
+    f(&k_stream<kElI8, XDT, EP, 2, 8, 2>, 16, 512);
+  } else {
+    if (K >= 8192) f(&k_stream<kElI8, XDT, EP, 1, 16, 4>, 16, 1024);
+    else f(&k_stream<kElI8, XDT, EP, 1, 16, 2>, 16, 1024);
   }
-  return best;
 }
 
 void register_int8_kernels(std::vector<const void*>& k) {
-  auto add = [&](auto kernel, int, int, int) { k.push_back((const void*)kernel); };
   for (int dt = MOE_DT_BF16; dt <= MOE_DT_F32; ++dt)
     by_dtype(dt, [&](auto D) {
       constexpr int DT = decltype(D)::value;
       k.push_back((const void*)&k_int8_quant<DT>);
-      for (int s = 0; s < kInt8Shapes; ++s) {
-        by_tile<PutInt8<DT>>(s, add);
-        by_tile<PutInt8Gated<DT>>(s, add);
+      auto add_stream = [&](auto kernel, int, int) { k.push_back((const void*)kernel); };
+      for (int K : {16, 65536}) {
+        by_stream<DT, PutInt8<DT>>(K, add_stream);
+        by_stream<kXOperand, PutInt8<DT>>(K, add_stream);
       }
+      by_stream<DT, PutInt8Gated<DT>>(16, add_stream);
+      by_stream<kXOperand, PutInt8Gated<DT>>(16, add_stream);
+      for (int i = 0; i < kTileShapes16; ++i)
+        by_shape(i, [&](auto shape) {
+          k.push_back((const void*)&k_tile<kElI8, false, false, PutInt8<DT>, decltype(shape)>);
+          k.push_back((const void*)&k_tile<kElI8, false, false, PutInt8Gated<DT>, decltype(shape)>);
+        });
     });
 }
 
 static size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 uint64_t int8_linear_threads(int T, int N) {
-  return std::max<uint64_t>((uint64_t)((T + 63) / 64) * ((N + 63) / 64) * 128, (uint64_t)T * 256);
+  return std::max(tile_threads(T, N), (uint64_t)T * 256);
 }
 
 size_t int8_linear_workspace_bytes(int T, int N, int K) {
+  if (int8_joins(T, K)) return 0;
   return up256((size_t)T * K) + up256((size_t)T * sizeof(float));
 }
 
 hipError_t launch_int8_linear(const moe_int8_matrix& W, const void* x, int T, int dtype, int gated,
                               void* out, void* ws, hipStream_t s) {
-  int8_t* q = (int8_t*)ws;
-  float* sx = (float*)((char*)ws + up256((size_t)T * W.K));
-  hipError_t e = launch_int8_quant(x, T, W.K, dtype, q, sx, s);
-  if (e != hipSuccess) return e;
   TileArgs16 a{};
-  a.a = q;
+  a.a = x;
   a.b = W.codes;
   a.lda = a.ldb = (uint32_t)W.K;
   a.M = T;
   a.N = gated ? W.N / 2 : W.N;
   a.K = W.K;
   a.out = out;
-  a.sm = sx;
   a.sn = W.scales;
+  if (!int8_joins(T, W.K)) {
+    int8_t* q = (int8_t*)ws;
+    float* sx = (float*)((char*)ws + up256((size_t)T * W.K));
+    hipError_t e = launch_int8_quant(x, T, W.K, dtype, q, sx, s);
+    if (e != hipSuccess) return e;
+    a.a = q;
+    a.sm = sx;
+  }
   by_dtype(dtype, [&](auto D) {
     constexpr int DT = decltype(D)::value;
-    auto go = [&](auto kernel, int bn, int bm, int threads) {
-      a.nt = (W.N + bn - 1) / bn;
-      MOE_LAUNCH("int8_tile", s, kernel, dim3((unsigned)a.nt * (unsigned)((T + bm - 1) / bm)), dim3(threads), 0, s, a);
+    auto stream = [&](auto kernel, int outs, int threads) {
+      MOE_LAUNCH("int8_stream", s, kernel, dim3((unsigned)((a.N + outs - 1) / outs)), dim3(threads), 0, s, a);
     };
-    if (gated) by_tile<PutInt8Gated<DT>>(tile_shape(T, W.N), go);
-    else by_tile<PutInt8<DT>>(tile_shape(T, W.N), go);
+    auto go = [&](auto ep) {
+      typedef decltype(ep) EP;
+      if (int8_joins(T, W.K)) by_stream<DT, EP>(W.K, stream);
+      else if (int8_streams(T)) by_stream<kXOperand, EP>(W.K, stream);
+      else {
+        const int best = tile_shape(T, W.N, steps_of(W.K, 1));
+        by_shape(best, [&](auto shape) {
+          a.nt = (W.N + shape.BN - 1) / shape.BN;
+          MOE_LAUNCH("int8_tile", s, (k_tile<kElI8, false, false, EP, decltype(shape)>),
+                     dim3((unsigned)tiles_of(best, T, W.N)), dim3(shape.kThreads), 0, s, a);
+        });
+      }
+    };
+    if (gated) go(PutInt8Gated<DT>{});
+    else go(PutInt8<DT>{});
   });
   return hipGetLastError();
 }

@@ -197,8 +197,10 @@ hipError_t launch_fp8_stream_experts(const moe_fp8_weights& W, const uint16_t* x
                                      const int32_t* groups, float* h, uint16_t* y,
                                      hipStream_t s);
 
-// The dense gated feed-forward block and its gradients (moe_dense.hip).
+// The dense gated feed-forward block (moe_dense.hip) and its gradients
+// (moe_dense_grad.hip).
 void register_dense_kernels(std::vector<const void*>& k);
+void register_dense_grad_kernels(std::vector<const void*>& k);
 size_t dense_ffn_workspace_bytes(int T, int H, int I);
 size_t dense_ffn_grad_workspace_bytes(int T, int H, int I);
 hipError_t launch_dense_ffn(const moe_dense_weights& W, const void* x, int T, void* y, void* gu,

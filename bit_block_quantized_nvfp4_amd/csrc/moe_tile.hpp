@@ -46,6 +46,7 @@ constexpr int kElI8 = 16;  // beside MOE_DT_BF16 and MOE_DT_F16
 template <int EL>
 struct Mma {
   typedef f32x16 Acc;
+  typedef f32x4 Four;
   static __device__ __forceinline__ Acc go(u32x4 a, u32x4 b, Acc c) {
     if constexpr (EL == MOE_DT_BF16)
       return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
@@ -58,6 +59,7 @@ struct Mma {
 template <>
 struct Mma<kElI8> {
   typedef i32x16 Acc;
+  typedef i32x4 Four;
   static __device__ __forceinline__ Acc go(u32x4 a, u32x4 b, Acc c) {
     return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a),
                                                  __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
@@ -94,7 +96,7 @@ struct Operand {
   static constexpr int kLoads = R * kC / NT;   // per thread and step
   static constexpr int CPR = R / 8;            // chunks of a line (rows fastest)
   static constexpr int KS = SB / ES;           // values of K in a step
-  static_assert(R * kC % NT == 0 && NT % 128 == 0 && (!ROWS || (ES == 2 && !GATED)) && (!GATED || kLoads % 2 == 0),
+  static_assert(R * kC % NT == 0 && (NT % 128 == 0 || (NT == 64 && SB == 128)) && (!ROWS || (ES == 2 && !GATED)) && (!GATED || kLoads % 2 == 0),
                 "operand shape");
   const char* base;
   const char* up;
@@ -120,18 +122,19 @@ struct Operand {
       up = base + up_bytes;
       constexpr int RR = GATED ? R / 2 : R;
       width = (uint32_t)min(left, RR) * ld;
-      chunk = 16 * ((tid % kC) ^ ((tid >> 4) % kC));  // row / (16 / kC) = tid / 16
+      chunk = 16 * ((tid % kC) ^ ((tid >> 4) % kC));  // of load 0: row / (16 / kC) = tid / 16
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        off[i] = (uint32_t)((i * NT + tid) / kC % RR) * ld + chunk;
+        off[i] = (uint32_t)((i * NT + tid) / kC % RR) * ld + chunk_of(i);
       }
     }
   }
+  // The byte of its row's step that load i begins at.
+  __device__ __forceinline__ int chunk_of(int i) const { return NT == 64 ? chunk ^ (i % 2 * 64) : chunk; }
   // What the loads of a step share.
   struct Step {
     u32x4 buf, ubuf;
-    uint32_t so;
-    bool in;
+    uint32_t so, ko;
   };
   __device__ __forceinline__ Step begin(int s) const {
     Step t;
@@ -140,15 +143,14 @@ struct Operand {
       t.buf = buf_of(base + (size_t)k0 * ld, kn > 0 ? (uint32_t)(kn - 1) * ld + width : 0u);
       asm volatile("s_nop 4" : "+s"(t.buf));  // as in dma_offset
     } else {
-      const uint32_t ko = (uint32_t)s * SB;
+      t.ko = (uint32_t)s * SB;
       t.buf = buf_of(base, width);
       asm volatile("s_nop 4" : "+s"(t.buf));
       if constexpr (GATED) {
         t.ubuf = buf_of(up, width);
         asm volatile("s_nop 4" : "+s"(t.ubuf));
       }
-      t.in = ko + chunk < kbytes;
-      t.so = dma_offset(min(ko, kbytes));
+      t.so = dma_offset(min(t.ko, kbytes));
     }
     return t;
   }
@@ -157,7 +159,8 @@ struct Operand {
     if constexpr (ROWS)
       dma_b128(t.buf, off[i], 0, lds + i * NT * 16);
     else
-      dma_b128(GATED && i >= kLoads / 2 ? t.ubuf : t.buf, t.in ? off[i] : kNowhere, t.so, lds + i * NT * 16);
+      dma_b128(GATED && i >= kLoads / 2 ? t.ubuf : t.buf, t.ko + chunk_of(i) < kbytes ? off[i] : kNowhere, t.so,
+               lds + i * NT * 16);
   }
 };
 
@@ -188,30 +191,43 @@ struct NoPre {
 // EP: the epilogue.  EP::kGated: a wave's columns are TN / 2 gates and the TN / 2 ups of
 // the same outputs; EP::put(a, m, n, v, u, pre): outputs n .. n + 7 of row m (both
 // inside) from the sums v (and u, the ups) and what EP::Pre::get(a, m, n) has read.
-template <int EL, bool BROWS, bool AROWS, class EP, int BN, int BM, int WN, int WM, int SB, int NA, int NB>
-__global__ __launch_bounds__(64 * WN * WM) void k_tile(TileArgs16 a) {
-  constexpr int NW = WN * WM, NT = 64 * NW;
+// KG groups of waves with buffers of their own take every KG-th step and join their sums
+// at the end, in the groups' order: where there are few tiles, a step costs its
+// waiting whatever its size.
+template <int BN_, int BM_, int WN_, int WM_, int SB_, int NA_, int NB_, int KG_ = 1>
+struct TileShape {
+  static constexpr int BN = BN_, BM = BM_, WN = WN_, WM = WM_, SB = SB_, NA = NA_, NB = NB_, KG = KG_;
+  static constexpr int kThreads = 64 * WN * WM * KG;
+  static constexpr int kGroupLds = (NA * BM + NB * BN) * SB, kLds = KG * kGroupLds;
+};
+
+// Block `blk` of the `blocks` of a product.
+template <int EL, bool BROWS, bool AROWS, class EP, class TS>
+__device__ __forceinline__ void tile_block(const TileArgs16& a, const int blk, const int blocks, lds_u8* const lds) {
+  constexpr int BN = TS::BN, BM = TS::BM, WN = TS::WN, WM = TS::WM, SB = TS::SB, NA = TS::NA, NB = TS::NB, KG = TS::KG;
+  constexpr int NW = WN * WM, NT = 64 * NW;                  // waves and threads of a group
   constexpr int TN = BN / WN, TM = BM / WM;
   constexpr int FN = TN / 32, FM = TM / 32;
   constexpr int ES = EL == kElI8 ? 1 : 2;
-  constexpr int kA = BM * SB, kB = BN * SB, kLds = NA * kA + NB * kB;  // bytes of a step, of all
+  constexpr int kA = BM * SB, kB = BN * SB, kLds = TS::kGroupLds;  // bytes of a step, of a group
   constexpr int KF = SB / 32;                                // products along K of a step
   constexpr bool G = EP::kGated;
   constexpr int BC = G ? BN / 2 : BN, TC = G ? TN / 2 : TN;  // outputs of a tile and of a wave
   constexpr int CH = TN / 4;                                 // 16-byte chunks of a staged row
   typedef typename Mma<EL>::Acc Acc;
+  typedef typename Mma<EL>::Four Four;
   static_assert(TN % 32 == 0 && TM % 32 == 0 && (!G || FN % 2 == 0) && NA >= 2 && NB >= NA, "tile shape");
   constexpr int kStage = 32 * TN * 4;                        // bytes of 32 staged rows
-  static_assert(NW * 2 * kStage <= kLds && CH <= 32 && (CH & (CH - 1)) == 0, "staged rows");
-  __shared__ __align__(1024) uint8_t lds[kLds];
-  const int tid = threadIdx.x, lane = tid & 63;
+  static_assert(NW * 2 * kStage <= KG * kLds && CH <= 32 && (CH & (CH - 1)) == 0, "staged rows");
+  const int kg = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane((int)threadIdx.x / NT);
+  const int tid = (int)threadIdx.x - kg * NT, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wv % WN, wm = wv / WN;
 
   // Blocks are dealt to the 8 XCDs in turn: each XCD gets a run of tiles, 8 row tiles
   // deep before the next column tile, so that the blocks that run together on one
   // share the lines of both operands in its L2
-  const int mt = (a.M + BM - 1) / BM, per = (int)gridDim.x / 8, blk = blockIdx.x;
+  const int mt = (a.M + BM - 1) / BM, per = blocks / 8;
   const int lin = blk < per * 8 ? (blk % 8) * per + blk / 8 : blk;
   const int deep = 8 * a.nt, grp = lin / deep, in = lin % deep;
   const int gm = min(8, mt - grp * 8);
@@ -228,9 +244,9 @@ __global__ __launch_bounds__(64 * WN * WM) void k_tile(TileArgs16 a) {
   OpA oa;
   ob.set(a.b, a.ldb, n0, a.N - n0, a.K, (long)a.N * a.ldb, tid);
   oa.set(a.a, a.lda, m0, a.M - m0, a.K, 0, tid);
-  lds_u8* const l0 = (lds_u8*)lds;
+  lds_u8* const l0 = lds + kg * kLds;
   const uint32_t ldsw = (uint32_t)(uintptr_t)l0 + wv * 1024;
-  const int steps = (a.K * ES + SB - 1) / SB;
+  const int steps = ((a.K * ES + SB - 1) / SB + KG - 1) / KG;  // of a group
 
   // Step s's turn at the buffers that step s - 1 leaves: the loads of A's step s - 1 + NA,
   // then of B's step s - 1 + NB.  Steps past the last one are brought too, as zeros
@@ -240,8 +256,8 @@ __global__ __launch_bounds__(64 * WN * WM) void k_tile(TileArgs16 a) {
   typename OpB::Step tb;
   typename OpA::Step ta;
   auto begin = [&](int s) __attribute__((always_inline)) {
-    ta = oa.begin(s - 1 + NA);
-    tb = ob.begin(s - 1 + NB);
+    ta = oa.begin((s - 1 + NA) * KG + kg);
+    tb = ob.begin((s - 1 + NB) * KG + kg);
   };
   auto load = [&](int i) __attribute__((always_inline)) {
     if (i < LA) oa.load(ta, i, ldsw + NB * kB + a_at);
@@ -320,6 +336,37 @@ __global__ __launch_bounds__(64 * WN * WM) void k_tile(TileArgs16 a) {
     }
   }
   wait_step<0>();  // nothing is under way to LDS, nothing is read from it any more
+  if constexpr (KG > 1) {
+    // lane by lane, 16 bytes at a time, behind the places of the rows below
+    lds_u8* const sums = lds + NW * 2 * kStage + tid * 16;
+    static_assert(NW * 2 * kStage + (KG - 1) * BN * BM * 4 <= KG * kLds, "the groups' sums fit");
+    auto place = [&](int g, int i, int j, int q) __attribute__((always_inline)) {
+      return (__attribute__((address_space(3))) Four*)(sums + (((g * FN + i) * FM + j) * 4 + q) * (NT * 16));
+    };
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FM; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (kg > 0)
+            *place(kg - 1, i, j, q) =
+                Four{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    meet();
+    if (kg > 0) return;
+#pragma unroll
+    for (int g = 0; g < KG - 1; ++g)
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const Four w = *place(g, i, j, q);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += w[e];
+          }
+  }
 
   // The wave's sums, 32 rows at a time, through LDS of its own (two places in turn): a
   // lane then has eight consecutive outputs of a row, and memory is read and written
@@ -335,10 +382,9 @@ __global__ __launch_bounds__(64 * WN * WM) void k_tile(TileArgs16 a) {
     for (int i = 0; i < FN; ++i)
 #pragma unroll
       for (int g = 0; g < 4; ++g)
-        *(__attribute__((address_space(3))) f32x4*)(mine + j % 2 * kStage + fr * (TN * 4) +
-                                                    (((8 * i + 2 * g + fq) ^ (fr & (CH - 1))) << 4)) =
-            f32x4{(float)acc[i][j][4 * g], (float)acc[i][j][4 * g + 1], (float)acc[i][j][4 * g + 2],
-                  (float)acc[i][j][4 * g + 3]};
+        *(__attribute__((address_space(3))) Four*)(mine + j % 2 * kStage + fr * (TN * 4) +
+                                                   (((8 * i + 2 * g + fq) ^ (fr & (CH - 1))) << 4)) =
+            Four{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
   };
   auto row_of = [&](int j, int q) __attribute__((always_inline)) { return m0 + wm * TM + 32 * j + q * RP + r0; };
   typename EP::Pre pre[2][P];
@@ -363,10 +409,10 @@ __global__ __launch_bounds__(64 * WN * WM) void k_tile(TileArgs16 a) {
       auto row8 = [&](int c, float (&f)[8]) __attribute__((always_inline)) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const f32x4 w = *(const __attribute__((address_space(3))) f32x4*)(
+          const Four w = *(const __attribute__((address_space(3))) Four*)(
               mine + j % 2 * kStage + r * (TN * 4) + (((c + h) ^ (r & (CH - 1))) << 4));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) f[4 * h + e] = w[e];
+          for (int e = 0; e < 4; ++e) f[4 * h + e] = (float)w[e];
         }
       };
       row8(2 * c8, v);
@@ -377,9 +423,81 @@ __global__ __launch_bounds__(64 * WN * WM) void k_tile(TileArgs16 a) {
   }
 }
 
-// Eight values of a row, rounded once, nearest even.
+template <int EL, bool BROWS, bool AROWS, class EP, class TS>
+__global__ __launch_bounds__(TS::kThreads) void k_tile(TileArgs16 a) {
+  __shared__ __align__(1024) uint8_t lds[TS::kLds];
+  tile_block<EL, BROWS, AROWS, EP, TS>(a, blockIdx.x, gridDim.x, (lds_u8*)lds);
+}
+
+// ---- host side: the shapes, and which of them a product takes
+
+// f with the shape as a type.
+constexpr int kTileShapes16 = 6;
+template <typename F>
+static void by_shape(int shape, F&& f) {
+  if (shape == 0) f(TileShape<256, 256, 2, 2, 128, 2, 3>{});
+  if (shape == 1) f(TileShape<128, 128, 2, 2, 128, 2, 2>{});
+  if (shape == 2) f(TileShape<128, 128, 2, 2, 128, 2, 2, 2>{});
+  if (shape == 3) f(TileShape<64, 64, 1, 2, 128, 4, 4>{});
+  if (shape == 4) f(TileShape<64, 64, 1, 2, 128, 4, 4, 2>{});
+  if (shape == 5) f(TileShape<64, 32, 1, 1, 128, 3, 3, 4>{});
+}
+
+// Tiles of a product in a shape, and steps along K (of 128 bytes).
+static inline long tiles_of(int shape, int M, int cols) {
+  long n = 0;
+  by_shape(shape, [&](auto s) {
+    n = (long)((cols + s.BN - 1) / s.BN) * ((M + s.BM - 1) / s.BM);
+  });
+  return n;
+}
+static inline long steps_of(int K, int es) { return ((long)K * es + 127) / 128; }
+
+// Time of one round of tiles on the chip, in 10 ns: `fixed` + steps * `step` with all its
+// places taken (two blocks of the smaller shapes fit on a compute unit), and with one
+// block on each.  From launches of 128 to 1024 tiles and 1 to 64 steps (bf16, in a row in
+// a graph, us; the three layouts differ by up to a tenth):
+//                        256 tiles                      1024 tiles
+//   steps            1     4    16     64         1     4    16     64
+//   256 x 256     13.7  18.0  35.8    111      40.2  58.1   132    424
+//   128 x 128      5.2   7.4  15.5   60.1      13.2  17.4  46.7    150
+//   128 x 128, 2   6.4   7.7  13.4   47.6      20.9  24.3  58.9    180
+//   64 x 64        3.6   4.6   8.3   23.1       8.0   9.2  17.3   59.0
+//   64 x 64, 2     4.2   4.8   7.2   17.0      13.2  15.1  24.2   74.6
+//   64 x 32, 4     4.6   4.8   6.4   12.6      14.5  15.1  20.8   56.1
+// (", 2": groups along K).
+struct TileCost {
+  int places, fixed, step, fixed1, step1;
+};
+static inline TileCost tile_cost(int shape) {
+  constexpr TileCost c[kTileShapes16] = {{256, 900, 155, 900, 155}, {512, 620, 110, 460, 87}, {256, 530, 64, 530, 64},
+                                         {512, 360, 41, 330, 31},   {256, 380, 22, 380, 22},  {256, 400, 14, 400, 14}};
+  return c[shape];
+}
+// The shape in which the rounds of a product's tiles take the least time together.
+static inline int tile_shape(int M, int cols, long steps) {
+  int best = 0;
+  long least = 0;
+  for (int s = 0; s < kTileShapes16; ++s) {
+    const TileCost c = tile_cost(s);
+    const long tiles = tiles_of(s, M, cols), full = tiles / c.places, rest = tiles % c.places;
+    const long whole = c.fixed + steps * c.step, one = c.fixed1 + steps * c.step1;
+    const long t = full * whole + (rest == 0 ? 0 : rest <= 256 ? one : whole);
+    if (least == 0 || t < least) least = t, best = s;
+  }
+  return best;
+}
+// Threads of a product's launch, whatever its shape, at most.
+static inline uint64_t tile_threads(int M, int cols) {
+  uint64_t t = 0;
+  for (int s = 0; s < kTileShapes16; ++s)
+    by_shape(s, [&](auto shape) { t = std::max(t, (uint64_t)tiles_of(s, M, cols) * shape.kThreads); });
+  return t;
+}
+
+// Eight or four values of a row, rounded once, nearest even.
 template <int DT>
-__device__ __forceinline__ void put8(void* p, size_t at, const float (&v)[8]) {
+__device__ __forceinline__ void put_row(void* p, size_t at, const float (&v)[8]) {
   if constexpr (DT == MOE_DT_F32) {
     f32x4* q = (f32x4*)((float*)p + at);
     q[0] = f32x4{v[0], v[1], v[2], v[3]};
@@ -387,6 +505,15 @@ __device__ __forceinline__ void put8(void* p, size_t at, const float (&v)[8]) {
   } else {
     *(u32x4*)((uint16_t*)p + at) = Chunk<DT>::pack(v);
   }
+}
+template <int DT>
+__device__ __forceinline__ void put_row(void* p, size_t at, const float (&v)[4]) {
+  if constexpr (DT == MOE_DT_F32)
+    *(f32x4*)((float*)p + at) = f32x4{v[0], v[1], v[2], v[3]};
+  else if constexpr (DT == MOE_DT_BF16)
+    *(u32x2*)((uint16_t*)p + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  else
+    *(u32x2*)((uint16_t*)p + at) = u32x2{pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3])};
 }
 
 }  // namespace moe

@@ -125,7 +125,7 @@ def test_gradients(moe, T, H, I, dtype):
 
 
 # tiles of the largest shapes, in every product: many rows, columns and both
-LARGE = [(4100, 72, 2056), (2056, 4104, 72), (520, 2048, 4104)]
+LARGE = [(4100, 72, 2056), (2056, 4104, 72), (520, 2048, 4104), (4090, 72, 2040)]
 
 
 @pytest.mark.parametrize("dtype", HALVES)
@@ -143,7 +143,8 @@ def test_large(moe, T, H, I, dtype):
 
 
 @pytest.mark.parametrize("dtype", HALVES)
-@pytest.mark.parametrize("T,H,I", [(5, 72, 24), (100, 264, 136), (700, 1032, 520), (2100, 1032, 2056)])
+@pytest.mark.parametrize("T,H,I", [(5, 72, 24), (100, 264, 136), (700, 1032, 520), (2048, 2048, 2048),
+                                   (2100, 1032, 2056), (4090, 2056, 4096)])
 def test_gradients_of_whole_numbers_are_exact(moe, T, H, I, dtype):
     """g = 32 makes silu the identity to the last bit (exp(-32) < 2^-46): with sparse signs
     and small whole numbers every operand and sum is exact, so that one lost or repeated
@@ -161,13 +162,13 @@ def test_gradients_of_whole_numbers_are_exact(moe, T, H, I, dtype):
     Wd = signs((H, I), 0.7)
     gu = torch.cat([torch.full((T, I), 32.0), torch.randint(-2, 3, (T, I), generator=gen).float()], 1).to(dtype)
     got = moe.moe_dense_ffn_grad(moe.DenseWeights(gpu(W), gpu(Wd)), gpu(dy), gpu(x), gpu(gu))
-    dh = dy.double() @ Wd.double()
-    u = gu[:, I:].double()
+    dh = gpu(dy).double() @ gpu(Wd).double()
+    u = gpu(gu[:, I:]).double()
     dgu = torch.cat([dh * u, dh * 32], 1)
-    want = (dgu @ W.double(), dgu.t() @ x.double(), dy.double().t() @ (32 * u))
+    want = (dgu @ gpu(W).double(), dgu.t() @ gpu(x).double(), gpu(dy).double().t() @ (32 * u))
     assert max(float(v.abs().max()) for v in want) < 2 ** 24
     for a, b, name in zip(got, want, ("dx", "dw_gu", "dw_dn")):
-        assert torch.equal(a.cpu(), b.float().to(dtype)), name
+        assert torch.equal(a, b.float().to(dtype)), name
 
 
 @pytest.mark.parametrize("dtype", HALVES)

@@ -20,7 +20,7 @@ def _scalars(operand):
 
 
 @pytest.mark.slow
-@pytest.mark.parametrize("source", ["moe_dense.hip", "moe_int8.hip"])
+@pytest.mark.parametrize("source", ["moe_dense.hip", "moe_dense_grad.hip", "moe_int8.hip"])
 def test_loads_to_lds(tmp_path, source):
     try:
         cc = b.hipcc()
