@@ -793,8 +793,8 @@ static int grad_list_ok(const char* what, const moe_grad_tensor* list, int count
   for (int i = 0; i < count; ++i) {
     const moe_grad_tensor& g = list[i];
     if (!dtype_ok(g.dtype)) return fail(MOE_EUNSUPPORTED, "%s: tensor %d: unknown dtype %d", what, i, g.dtype);
-    if (g.n < 0 || g.n > (1LL << 38))
-      return fail(MOE_EINVAL, "%s: tensor %d: need 0 <= n <= 2^38, got %lld", what, i, (long long)g.n);
+    if (g.n < 0 || g.n > (1LL << 37))
+      return fail(MOE_EINVAL, "%s: tensor %d: need 0 <= n <= 2^37, got %lld", what, i, (long long)g.n);
     if (g.n == 0) continue;
     if (!g.grad || (outs && !g.out)) return fail(MOE_EINVAL, "%s: tensor %d: null pointer", what, i);
     const uintptr_t es = g.dtype == MOE_DT_F32 ? 4 : 2;

@@ -657,7 +657,7 @@ int moe_int8_linear(const moe_int8_matrix* M, const void* x, int T, int dtype, i
  *
  *   ws  at least moe_grad_norm_workspace_bytes(count) bytes, aligned to 8
  *
- * Limits: 1 <= count <= 2^20, 0 <= n <= 2^38, max_norm finite and >= 0.  No output
+ * Limits: 1 <= count <= 2^20, 0 <= n <= 2^37, max_norm finite and >= 0.  No output
  * may overlap another tensor of the list.
  */
 typedef struct moe_grad_tensor {

@@ -131,7 +131,7 @@ def test_gradient_list_refusals(L, lib):
         _is(L, f(tensors(good), n=(1 << 20) + 1), E, b"between 1 and 2^20")
         _is(L, f(tensors(good, (64, 64, 10, 3))), L.MOE_EUNSUPPORTED, b"tensor 1: unknown dtype")
         _is(L, f(tensors(good, (64, 64, -1, BF))), E, b"tensor 1: need 0 <= n")
-        _is(L, f(tensors(good, (64, 64, (1 << 38) + 1, BF))), E, b"2^38")
+        _is(L, f(tensors(good, (64, 64, (1 << 37) + 1, BF))), E, b"2^37")
         _is(L, f(tensors(good, good, (0, 64, 10, BF))), E, b"tensor 2: null pointer")
         _is(L, f(tensors((65, 65, 10, BF))), E, b"not aligned")
         _is(L, f(tensors((66, 66, 10, F32))), E, b"not aligned")
