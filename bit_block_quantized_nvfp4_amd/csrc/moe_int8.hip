@@ -11,22 +11,35 @@
 
 namespace moe {
 
-// A block quantises a row: 16 bytes a thread at a time, twice over the row (its absmax,
-// then the codes, from the L2).
-template <int DT>
+// A block quantises a row.  Up to U chunks of 16 bytes a thread stay in registers between
+// the row's absmax and its codes; longer rows (U = 0) are read twice, from the L2 the
+// second time.  8192 rows of 2048: 14 us, of 8192: 45 us with every row read twice.
+template <int DT, int U>
 __global__ __launch_bounds__(256) void k_int8_quant(const void* __restrict__ x, int K,
                                                     uint8_t* __restrict__ codes,
                                                     float* __restrict__ scales) {
   constexpr int N = Chunk<DT>::N;
   __shared__ float part[4];
-  const int t = blockIdx.x, tid = threadIdx.x;
+  const int t = blockIdx.x, tid = threadIdx.x, chunks = K / N;
   const u32x4* p = (const u32x4*)((const char*)x + (size_t)t * K * (DT == MOE_DT_F32 ? 4 : 2));
   float am = 0.f;
-  for (int c = tid; c < K / N; c += 256) {
+  auto look = [&](u32x4 v) __attribute__((always_inline)) {
     float f[N];
-    Chunk<DT>::unpack(p[c], f);
+    Chunk<DT>::unpack(v, f);
 #pragma unroll
     for (int j = 0; j < N; ++j) am = amax_nan(am, fabsf(f[j]));
+  };
+  u32x4 held[U > 0 ? U : 1];
+  if constexpr (U > 0) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      held[i] = u32x4{0u, 0u, 0u, 0u};
+      if (tid + 256 * i < chunks) held[i] = p[tid + 256 * i];
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) look(held[i]);
+  } else {
+    for (int c = tid; c < chunks; c += 256) look(p[c]);
   }
 #pragma unroll
   for (int o = 1; o < 64; o *= 2) am = amax_nan(am, __shfl_xor(am, o));
@@ -37,35 +50,59 @@ __global__ __launch_bounds__(256) void k_int8_quant(const void* __restrict__ x, 
   bool fine;
   int8_scale(am, &mul, &scale, &fine);
   uint32_t* q = (uint32_t*)(codes + (size_t)t * K);
-  for (int c = tid; c < K / N; c += 256) {
+  auto put = [&](u32x4 v, int c) __attribute__((always_inline)) {
     float f[N];
-    Chunk<DT>::unpack(p[c], f);
+    Chunk<DT>::unpack(v, f);
 #pragma unroll
     for (int w = 0; w < N / 4; ++w) q[c * (N / 4) + w] = int8x4(f + 4 * w, mul, fine);
+  };
+  if constexpr (U > 0) {
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (tid + 256 * i < chunks) put(held[i], tid + 256 * i);
+  } else {
+    for (int c = tid; c < chunks; c += 256) put(p[c], c);
   }
   if (tid == 0) scales[t] = scale;
+}
+
+// f with the chunks that a thread holds for rows of K values.
+template <int DT, typename F>
+static void by_row(int K, F&& f) {
+  const int each = (K / Chunk<DT>::N + 255) / 256;
+  if (each <= 1) f(IntC<1>{});
+  else if (each <= 4) f(IntC<4>{});
+  else if (each <= 8) f(IntC<8>{});
+  else f(IntC<0>{});
 }
 
 hipError_t launch_int8_quant(const void* x, int T, int K, int dtype, int8_t* codes, float* scales,
                              hipStream_t s) {
   by_dtype(dtype, [&](auto D) {
-    MOE_LAUNCH("int8_quant", s, (k_int8_quant<decltype(D)::value>), dim3((unsigned)T), dim3(256), 0, s, x, K,
-               (uint8_t*)codes, scales);
+    constexpr int DT = decltype(D)::value;
+    by_row<DT>(K, [&](auto U) {
+      MOE_LAUNCH("int8_quant", s, (k_int8_quant<DT, decltype(U)::value>), dim3((unsigned)T), dim3(256), 0, s, x, K,
+                 (uint8_t*)codes, scales);
+    });
   });
   return hipGetLastError();
 }
 
 // Up to 16 rows stream the weights.  Where the rows are few values they are quantised in
-// the same launch, which every block repeats; else in one of their own.  The shapes: f
-// with the kernel, outputs and threads of a block.
+// the same launch, which every block repeats (2048 x 2048, us: 1 row 5.4, else 3.4 and a
+// launch of 3.5; 8 rows 9.8 and 3.7); else in one of their own.  The shapes: f with the
+// kernel, outputs and threads of a block.
 static bool int8_streams(int T) { return T <= kStreamRows; }
-static bool int8_joins(int T, int K) { return int8_streams(T) && (long)T * K <= 16384; }
+static bool int8_joins(int T, int K) { return T <= 4 && (long)T * K <= 8192; }
 template <int XDT, class EP, typename F>
-static void by_stream(int K, F&& f) {
+static void by_stream(int M, int N, int K, F&& f) {
+  const bool half = takes_half(M, N, EP::kGated);
   if constexpr (EP::kGated) {
-    f(&k_stream<kElI8, XDT, EP, 2, 8, 2>, 16, 512);
+    if (half) f(&k_stream<kElI8, XDT, EP, 2, 8, 2, true>, 8, 512);
+    else f(&k_stream<kElI8, XDT, EP, 2, 8, 2>, 16, 512);
   } else {
-    if (K >= 8192) f(&k_stream<kElI8, XDT, EP, 1, 16, 4>, 16, 1024);
+    if (half) f(&k_stream<kElI8, XDT, EP, 1, 16, 2, true>, 8, 1024);
+    else if (K >= 8192) f(&k_stream<kElI8, XDT, EP, 1, 16, 4>, 16, 1024);
     else f(&k_stream<kElI8, XDT, EP, 1, 16, 2>, 16, 1024);
   }
 }
@@ -74,14 +111,18 @@ void register_int8_kernels(std::vector<const void*>& k) {
   for (int dt = MOE_DT_BF16; dt <= MOE_DT_F32; ++dt)
     by_dtype(dt, [&](auto D) {
       constexpr int DT = decltype(D)::value;
-      k.push_back((const void*)&k_int8_quant<DT>);
+      k.push_back((const void*)&k_int8_quant<DT, 0>);
+      k.push_back((const void*)&k_int8_quant<DT, 1>);
+      k.push_back((const void*)&k_int8_quant<DT, 4>);
+      k.push_back((const void*)&k_int8_quant<DT, 8>);
       auto add_stream = [&](auto kernel, int, int) { k.push_back((const void*)kernel); };
-      for (int K : {16, 65536}) {
-        by_stream<DT, PutInt8<DT>>(K, add_stream);
-        by_stream<kXOperand, PutInt8<DT>>(K, add_stream);
-      }
-      by_stream<DT, PutInt8Gated<DT>>(16, add_stream);
-      by_stream<kXOperand, PutInt8Gated<DT>>(16, add_stream);
+      for (int M : {1, kStreamRows})
+        for (int K : {16, 65536}) {
+          by_stream<DT, PutInt8<DT>>(M, 8, K, add_stream);
+          by_stream<kXOperand, PutInt8<DT>>(M, 8, K, add_stream);
+          by_stream<DT, PutInt8Gated<DT>>(M, 8, K, add_stream);
+          by_stream<kXOperand, PutInt8Gated<DT>>(M, 8, K, add_stream);
+        }
       for (int i = 0; i < kTileShapes16; ++i)
         by_shape(i, [&](auto shape) {
           k.push_back((const void*)&k_tile<kElI8, false, false, PutInt8<DT>, decltype(shape)>);
@@ -127,8 +168,8 @@ hipError_t launch_int8_linear(const moe_int8_matrix& W, const void* x, int T, in
     };
     auto go = [&](auto ep) {
       typedef decltype(ep) EP;
-      if (int8_joins(T, W.K)) by_stream<DT, EP>(W.K, stream);
-      else if (int8_streams(T)) by_stream<kXOperand, EP>(W.K, stream);
+      if (int8_joins(T, W.K)) by_stream<DT, EP>(T, a.N, W.K, stream);
+      else if (int8_streams(T)) by_stream<kXOperand, EP>(T, a.N, W.K, stream);
       else {
         const int best = tile_shape(T, W.N, steps_of(W.K, 1));
         by_shape(best, [&](auto shape) {

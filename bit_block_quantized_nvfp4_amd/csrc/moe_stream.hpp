@@ -8,6 +8,10 @@
 // pieces of each on their way while it multiplies the U before.  The KW waves of a tile
 // join through LDS in wave order.  16 rows are one MFMA operand whatever their number.
 //
+// HALF, for up to 8 rows: a tile is 8 weight rows, the operands' upper halves are the same
+// rows at the next piece, and the product's two diagonal quarters are added in the end.
+// Twice the blocks, for matrices whose tiles of 16 would leave compute units idle.
+//
 // 8-bit integers: with XDT a row type the rows are quantised on the way.  Each block then
 // reads all rows once for their largest magnitudes, which saves a launch where they are
 // few (moe_int8.hip); otherwise x holds codes and sm their scales.
@@ -19,6 +23,15 @@
 namespace moe {
 
 constexpr int kStreamRows = 16;
+// Outputs up to which up to 8 rows take HALF: tiles of 16 leave half the compute units
+// idle there, or (gated, two tiles a wave) with too few waves.  bf16, weights from memory,
+// in a row in a graph, us, tiles of 16 and HALF:
+//   plain, N x K     256 x 512        2.8   2.4                  gated, N outputs, K = 2048
+//   2048 x 512       3.3   2.8                                  512     6.4   4.5
+//   2048 x 2048      4.9   4.3                                  2048    7.7   5.8
+//   2048 x 8192     13.0   9.7                                  4096   11.2   8.4
+//   4096 x 2048      5.6   5.5  (8 rows 6.3, 6.8)
+constexpr bool takes_half(int rows, int outputs, bool gated) { return rows <= 8 && outputs <= (gated ? 4096 : 2048); }
 
 // One product of 128 bytes along K: lane l holds chunks l / 16 and l / 16 + 4 of row l % 16,
 // so that a load of a wave takes whole halves of 16 lines.  Element e of lane l of the
@@ -47,33 +60,35 @@ struct Mma16<kElI8> {
 constexpr int kXOperand = -1;  // XDT: x holds operands already
 
 // EP as in moe_tile.hpp, with four outputs of a row at a time.
-template <int EL, int XDT, class EP, int RT, int KW, int U>
+template <int EL, int XDT, class EP, int RT, int KW, int U, bool HALF = false>
 __global__ __launch_bounds__(64 * KW) void k_stream(TileArgs16 a) {
   constexpr bool G = EP::kGated;
   constexpr int ES = EL == kElI8 ? 1 : 2;
-  constexpr int OT = G ? 1 : RT;             // tiles of 16 outputs of a block
+  constexpr int OT = G ? 1 : RT;             // tiles of outputs of a block
+  constexpr int TR = HALF ? 8 : 16, PB = HALF ? 256 : 128;  // a tile's rows; bytes of a piece (HALF: two)
   typedef typename Mma16<EL>::Acc Acc;
   static_assert(!G || RT == 2, "a gate tile and an up tile");
   __shared__ f32x4 red[KW][RT][64];
   __shared__ float amax[XDT == kXOperand ? 1 : KW][kStreamRows];
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
   const int kw = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int n0 = (int)blockIdx.x * OT * 16;
+  const int n0 = (int)blockIdx.x * OT * TR;
   const uint32_t kb = (uint32_t)a.K * ES;
-  const int pieces = (int)((kb + 127) / 128);
+  const int pieces = (int)((kb + PB - 1) / PB);
 
   const char* wrow[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i)
-    wrow[i] = (const char*)a.b + (size_t)(min(n0 + (G ? 0 : 16 * i) + r, a.N - 1) + (G ? i * a.N : 0)) * kb;
-  const int xr = min(r, a.M - 1);            // rows past the last are not stored
+    wrow[i] = (const char*)a.b + (size_t)(min(n0 + (G ? 0 : TR * i) + r % TR, a.N - 1) + (G ? i * a.N : 0)) * kb;
+  const int xr = min(r % TR, a.M - 1);       // rows past the last are not stored
 
   // A lane's chunk h of piece p, zeros past the row's end (nothing is read there).
-  auto in = [&](int p, int h) __attribute__((always_inline)) {
-    return p < pieces && (uint32_t)(p * 128 + h * 64 + q * 16) < kb;
+  auto byte_of = [&](int p, int h) __attribute__((always_inline)) {
+    return (uint32_t)(p * PB + r / TR * 128 + h * 64 + q * 16);
   };
+  auto in = [&](int p, int h) __attribute__((always_inline)) { return p < pieces && byte_of(p, h) < kb; };
   auto chunk = [&](const char* row, int p, int h) __attribute__((always_inline)) {
-    return *(const u32x4*)(row + (in(p, h) ? (uint32_t)(p * 128 + h * 64 + q * 16) : 0u));
+    return *(const u32x4*)(row + (in(p, h) ? byte_of(p, h) : 0u));
   };
   struct Piece {
     u32x4 w[RT][2];
@@ -117,7 +132,7 @@ __global__ __launch_bounds__(64 * KW) void k_stream(TileArgs16 a) {
   // 16 bytes of x's operand
   auto operand = [&](int p, int h) __attribute__((always_inline)) {
     u32x4 o = {0u, 0u, 0u, 0u};
-    const uint32_t at = in(p, h) ? (uint32_t)(p * 128 + h * 64 + q * 16) : 0u;
+    const uint32_t at = in(p, h) ? byte_of(p, h) : 0u;
     if constexpr (XDT == kXOperand) {
       o = *(const u32x4*)((const char*)a.a + (size_t)xr * kb + at);
     } else {
@@ -166,13 +181,21 @@ __global__ __launch_bounds__(64 * KW) void k_stream(TileArgs16 a) {
   for (int i = 0; i < RT; ++i)
 #pragma unroll
     for (int w = 1; w < KW; ++w) acc[i] += __builtin_bit_cast(Acc, red[w][i][lane]);
+  if constexpr (HALF) {
+    // rows 4 q .. of columns r < 8, and rows 8 + 4 q .. of columns 8 + r
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][e] += __shfl(acc[i][e], (lane + 40) & 63);
+    if (q >= 2) return;
+  }
   if (r >= a.M) return;
   typename EP::Pre pre;
   if constexpr (XDT == kXOperand) pre.get(a, r, n0);
   else pre.s = sx;
 #pragma unroll
   for (int i = 0; i < OT; ++i) {
-    const int n = n0 + 16 * i + 4 * q;
+    const int n = n0 + TR * i + 4 * q;
     if (n >= a.N) continue;
     float v[4], u[4];
 #pragma unroll
