@@ -6,6 +6,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 #include <string>
@@ -686,13 +687,14 @@ static bool dense_sizes_ok(int T, int H, int I) {
 }
 
 // What both dense entry points ask of the weights and the sizes.
-static int dense_ok(const char* what, const moe_dense_weights& W, int T) {
+static int dense_ok(const char* what, const moe_dense_weights& W, int T,
+                    uint64_t (*threads)(int, int, int)) {
   if (!W.gu || !W.dn) return fail(MOE_EINVAL, "%s: null weight pointer", what);
   if (W.dtype != MOE_DT_BF16 && W.dtype != MOE_DT_F16)
     return fail(MOE_EUNSUPPORTED, "%s: dtype %d is not bf16 or f16", what, W.dtype);
   if (!dense_sizes_ok(T, W.H, W.I))
     return fail(MOE_EINVAL, "%s: need T >= 1, H and I multiples of 8 in [8, 65536] (T=%d H=%d I=%d)", what, T, W.H, W.I);
-  if (!grid_ok(moe::dense_threads(T, W.H, W.I))) return too_many_rows(what, T);
+  if (!grid_ok(threads(T, W.H, W.I))) return too_many_rows(what, T);
   return MOE_OK;
 }
 
@@ -703,7 +705,7 @@ size_t moe_dense_ffn_workspace_bytes(int T, int H, int I) {
 int moe_dense_ffn(const moe_dense_weights* W, const void* x, int T, void* y, void* gu_out,
                   void* ws, size_t ws_bytes, void* stream) {
   if (!W || !x || !y) return fail(MOE_EINVAL, "moe_dense_ffn: null pointer");
-  int rc = dense_ok("moe_dense_ffn", *W, T);
+  int rc = dense_ok("moe_dense_ffn", *W, T, moe::dense_ffn_threads);
   if (rc != MOE_OK) return rc;
   if (!aligned16((const char*)x, (const char*)y, (const char*)gu_out, (const char*)W->gu,
                  (const char*)W->dn, (const char*)ws))
@@ -726,7 +728,7 @@ int moe_dense_ffn_grad(const moe_dense_weights* W, const void* dy, const void* x
                        void* stream) {
   if (!W || !dy || !x || !gu || !dx || !dw_gu || !dw_dn)
     return fail(MOE_EINVAL, "moe_dense_ffn_grad: null pointer");
-  int rc = dense_ok("moe_dense_ffn_grad", *W, T);
+  int rc = dense_ok("moe_dense_ffn_grad", *W, T, moe::dense_ffn_grad_threads);
   if (rc != MOE_OK) return rc;
   if (!aligned16((const char*)dy, (const char*)x, (const char*)gu, (const char*)dx,
                  (const char*)dw_gu, (const char*)dw_dn, (const char*)W->gu, (const char*)W->dn,
@@ -773,7 +775,7 @@ int moe_int8_linear(const moe_int8_matrix* M, const void* x, int T, int dtype, i
   if (gated != 0 && gated != 1) return fail(MOE_EINVAL, "moe_int8_linear: gated must be 0 or 1");
   if (!int8_matrix_ok(T, M->N, M->K) || (gated && M->N % 16))
     return fail(MOE_EINVAL, "moe_int8_linear: need T >= 1, K a multiple of 16 in [16, 65536] and N a multiple of 8 (gated: 16) in [8, 131072] (T=%d N=%d K=%d)", T, M->N, M->K);
-  if (!grid_ok(moe::int8_linear_threads(T, M->N))) return too_many_rows("moe_int8_linear", T);
+  if (!grid_ok(moe::int8_linear_threads(T, M->N, M->K))) return too_many_rows("moe_int8_linear", T);
   if (!aligned16((const char*)x, (const char*)out, (const char*)M->codes, (const char*)ws))
     return fail(MOE_EINVAL, "moe_int8_linear: codes, rows and workspace must be aligned to 16 bytes");
   const size_t need = moe::int8_linear_workspace_bytes(T, M->N, M->K);
@@ -804,6 +806,27 @@ static int grad_list_ok(const char* what, const moe_grad_tensor* list, int count
   return MOE_OK;
 }
 
+// Two outputs of a list may not share memory (a tensor named twice): the launches would
+// scale it in an order of their own.
+static int grad_outs_ok(const moe_grad_tensor* list, int count) {
+  struct Range {
+    uintptr_t from, to;
+  };
+  std::vector<Range> r;
+  r.reserve((size_t)count);
+  bool sorted = true;
+  for (int i = 0; i < count; ++i) {
+    if (list[i].n == 0) continue;
+    const uintptr_t p = (uintptr_t)list[i].out;
+    r.push_back(Range{p, p + (uintptr_t)list[i].n * (list[i].dtype == MOE_DT_F32 ? 4 : 2)});
+    sorted = sorted && (r.size() == 1 || r[r.size() - 2].from <= p);
+  }
+  if (!sorted) std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.from < b.from; });
+  for (size_t i = 1; i < r.size(); ++i)
+    if (r[i].from < r[i - 1].to) return fail(MOE_EINVAL, "moe_grad_clip: two outputs overlap");
+  return MOE_OK;
+}
+
 size_t moe_grad_norm_workspace_bytes(int count) {
   return count >= 1 && count <= (1 << 20) ? moe::grad_norm_workspace_bytes(count) : 0;
 }
@@ -828,6 +851,7 @@ int moe_grad_clip(const moe_grad_tensor* list, int count, const float* norm, flo
   if (!(max_norm >= 0.f && max_norm <= FLT_MAX))
     return fail(MOE_EINVAL, "moe_grad_clip: max_norm must be finite and not negative");
   int rc = grad_list_ok("moe_grad_clip", list, count, true);
+  if (rc == MOE_OK) rc = grad_outs_ok(list, count);
   if (rc != MOE_OK) return rc;
   rc = ensure_init();
   if (rc != MOE_OK) return rc;

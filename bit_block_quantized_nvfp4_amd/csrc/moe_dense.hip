@@ -84,9 +84,9 @@ void register_dense_kernels(std::vector<const void*>& k) {
 }
 
 
-uint64_t dense_threads(int T, int H, int I) {
-  const uint64_t fwd = std::max({tile_threads(T, 2 * I), tile_threads(T, H)});
-  return std::max(fwd, tile_threads(T, H) + tile_threads(2 * I, H) + tile_threads(H, I));
+uint64_t dense_ffn_threads(int T, int H, int I) {
+  if (T <= kStreamRows) return 0;  // at most 65536 / 8 blocks
+  return std::max(tile_threads(T, 2 * I, steps_of(H, 2)), tile_threads(T, H, steps_of(I, 2)));
 }
 
 size_t dense_ffn_workspace_bytes(int T, int H, int I) { return up256((size_t)T * I * 2); }

@@ -99,6 +99,27 @@ void register_dense_grad_kernels(std::vector<const void*>& k) {
     });
 }
 
+// The sizes of the three products.
+static GradArgs grads_of(int T, int H, int I) {
+  GradArgs g{};
+  g.dx.M = T, g.dx.N = H, g.dx.K = 2 * I;
+  g.dgu.M = 2 * I, g.dgu.N = H, g.dgu.K = T;
+  g.ddn.M = H, g.ddn.N = I, g.ddn.K = T;
+  return g;
+}
+
+uint64_t dense_ffn_grad_threads(int T, int H, int I) {
+  const GradArgs g = grads_of(T, H, I);
+  const int best = grads_shape(g);
+  uint64_t t = tile_threads(T, I, steps_of(H, 2));
+  by_shape(best, [&](auto shape) {
+    uint64_t tiles = 0;
+    for (const TileArgs16* a : {&g.dx, &g.dgu, &g.ddn}) tiles += (uint64_t)tiles_of(best, a->M, a->N);
+    t = std::max(t, tiles * shape.kThreads);
+  });
+  return t;
+}
+
 size_t dense_ffn_grad_workspace_bytes(int T, int H, int I) {
   return up256((size_t)T * 2 * I * 2) + up256((size_t)T * I * 2);
 }
@@ -125,30 +146,21 @@ hipError_t launch_dense_ffn_grad(const moe_dense_weights& W, const void* dy, con
     a.out2 = h;
     e = product<DT, true, PutGatedGrad<DT>>("dense_down_grad", a, s);
     if (e != hipSuccess) return;
-    GradArgs g{};
+    GradArgs g = grads_of(T, W.H, W.I);
     g.dx.a = dgu;  // dx = dgu Wgu
     g.dx.lda = 2 * ib;
     g.dx.b = W.gu;
     g.dx.ldb = hb;
-    g.dx.M = T;
-    g.dx.N = W.H;
-    g.dx.K = 2 * W.I;
     g.dx.out = dx;
     g.dgu.a = dgu;  // dWgu = dgu^T x
     g.dgu.lda = 2 * ib;
     g.dgu.b = x;
     g.dgu.ldb = hb;
-    g.dgu.M = 2 * W.I;
-    g.dgu.N = W.H;
-    g.dgu.K = T;
     g.dgu.out = dw_gu;
     g.ddn.a = dy;  // dWd = dy^T h
     g.ddn.lda = hb;
     g.ddn.b = h;
     g.ddn.ldb = ib;
-    g.ddn.M = W.H;
-    g.ddn.N = W.I;
-    g.ddn.K = T;
     g.ddn.out = dw_dn;
     const int best = grads_shape(g);
     by_shape(best, [&](auto shape) {

@@ -133,8 +133,9 @@ void register_int8_kernels(std::vector<const void*>& k) {
 
 static size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-uint64_t int8_linear_threads(int T, int N) {
-  return std::max(tile_threads(T, N), (uint64_t)T * 256);
+uint64_t int8_linear_threads(int T, int N, int K) {
+  if (int8_streams(T)) return 0;  // at most 131072 / 8 blocks
+  return std::max(tile_threads(T, N, steps_of(K, 1)), (uint64_t)T * 256);
 }
 
 size_t int8_linear_workspace_bytes(int T, int N, int K) {

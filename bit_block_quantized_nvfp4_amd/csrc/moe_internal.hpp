@@ -144,8 +144,9 @@ uint64_t block_norm_threads(int T, int H, int dtype);
 uint64_t fp8_quant_threads(int T, int K);
 uint64_t fp8_linear_threads(int T, int N, int K);
 uint64_t fp8_expert_ffn_threads(const moe_fp8_weights& W, int T, int K);
-uint64_t dense_threads(int T, int H, int I);
-uint64_t int8_linear_threads(int T, int N);
+uint64_t dense_ffn_threads(int T, int H, int I);
+uint64_t dense_ffn_grad_threads(int T, int H, int I);
+uint64_t int8_linear_threads(int T, int N, int K);
 
 // Token sort and its gradients (moe_sort.hip).
 void register_sort_kernels(std::vector<const void*>& k);

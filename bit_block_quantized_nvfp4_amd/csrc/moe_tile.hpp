@@ -487,11 +487,11 @@ static inline int tile_shape(int M, int cols, long steps) {
   }
   return best;
 }
-// Threads of a product's launch, whatever its shape, at most.
-static inline uint64_t tile_threads(int M, int cols) {
+// Threads of a product's launch.
+static inline uint64_t tile_threads(int M, int cols, long steps) {
+  const int best = tile_shape(M, cols, steps);
   uint64_t t = 0;
-  for (int s = 0; s < kTileShapes16; ++s)
-    by_shape(s, [&](auto shape) { t = std::max(t, (uint64_t)tiles_of(s, M, cols) * shape.kThreads); });
+  by_shape(best, [&](auto shape) { t = (uint64_t)tiles_of(best, M, cols) * shape.kThreads; });
   return t;
 }
 

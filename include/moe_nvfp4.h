@@ -583,7 +583,8 @@ int moe_fp8_expert_ffn(const moe_fp8_weights* W, const uint16_t* x, int T, int K
  *   ws  at least moe_dense_ffn_workspace_bytes(T, H, I), or ..._grad_...(T, H, I)
  *
  * Limits: T >= 1, H and I multiples of 8 in [8, 65536], pointers aligned to 16 bytes,
- * launches of fewer than 2^32 threads: at most max(T, H, 2I) max(H, 2I) / 32.
+ * launches of fewer than 2^32 threads: products that large take one per 256 outputs
+ * (T 2I forward; T H + 3 H I behind dh), those of narrow matrices up to one per 8.
  * Outputs and workspace may not overlap one another or the inputs.
  */
 typedef struct moe_dense_weights {
@@ -624,8 +625,8 @@ int moe_dense_ffn_grad(const moe_dense_weights* W, const void* dy, const void* x
  * row's outputs are NaN and no others.  The outputs may not overlap the inputs.
  * Limits: K a multiple of 16 in [16, 65536], N a multiple of 8 (gated: 16) in
  * [8, 131072], T >= 1, launches of fewer than 2^32 threads: 256 a row for the
- * quantisation, N * T / 32 for the product; pointers of codes, x and out aligned to
- * 16 bytes.
+ * quantisation, one per 256 outputs for a product that large (of a narrow matrix up to
+ * one per 8); pointers of codes, x and out aligned to 16 bytes.
  */
 typedef struct moe_int8_matrix {
   const int8_t* codes;
@@ -658,7 +659,7 @@ int moe_int8_linear(const moe_int8_matrix* M, const void* x, int T, int dtype, i
  *   ws  at least moe_grad_norm_workspace_bytes(count) bytes, aligned to 8
  *
  * Limits: 1 <= count <= 2^20, 0 <= n <= 2^37, max_norm finite and >= 0.  No output
- * may overlap another tensor of the list.
+ * may overlap another tensor of the list (two outputs that do are refused).
  */
 typedef struct moe_grad_tensor {
   const void* grad;

@@ -62,7 +62,7 @@ def test_dense_refusals(L, lib):
         _is(L, c(ws=ODD), E, b"aligned")
         _is(L, c(ws=None), L.MOE_EWORKSPACE, b"workspace")
         _is(L, c(nb=63), L.MOE_EWORKSPACE, b"workspace")
-        _is(L, c(T=1 << 30, H=64, I=64), E, b"2^32 threads")
+        _is(L, c(T=1 << 30, H=65536, I=65536), E, b"2^32 threads")
     _is(L, f(y=None), E, b"null")
     _is(L, f(y=ODD), E, b"aligned")
     _is(L, f(k=ODD), E, b"aligned")
@@ -141,6 +141,8 @@ def test_gradient_list_refusals(L, lib):
     _is(L, clip(tensors((64, 65, 10, BF))), E, b"not aligned")
     for top in (-1.0, float("inf"), float("nan")):
         _is(L, clip(tensors(good), top=top), E, b"max_norm")
+    _is(L, clip(tensors(good, good)), E, b"overlap")
+    _is(L, clip(tensors((64, 100, 4, F32), (64, 64, 10, BF), (64, 84, 9, BF))), E, b"overlap")
     norm = calls["norm"]
     _is(L, norm(tensors(good), ws=None), L.MOE_EWORKSPACE, b"workspace")
     _is(L, norm(tensors(good), nb=wsb(1) - 1), L.MOE_EWORKSPACE, b"workspace")
@@ -179,3 +181,19 @@ def test_int8_matrix_layout_on_the_host():
     assert M.codes.dtype == torch.int8 and torch.equal(M.codes.long(), codes) and torch.equal(M.scales, scale)
     zero = moe.Int8Matrix.from_float(torch.zeros(8, 16))
     assert not zero.codes.any() and torch.isfinite(zero.scales).all()
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are none; without a device nothing is launched")
+def test_calls_within_the_limits_are_accepted(L, lib):
+    """They get past every check, to the device that is missing here."""
+    big = 1 << 60
+    w = L.MoeDenseWeights(64, 64, 64, 64, BF)
+    m = L.MoeInt8Matrix(64, 64, 131072, 65536)
+    side = (L.MoeGradTensor * 4)(*[L.MoeGradTensor(*t) for t in ((64, 64, 10, BF), (64, 84, 0, BF), (128, 84, 9, BF), (64, 102, 1, F16))])
+    calls = [lambda: lib.moe_dense_ffn(ctypes.byref(w), P, 1 << 27, P, P, P, big, None),
+             lambda: lib.moe_dense_ffn_grad(ctypes.byref(w), P, P, P, 1 << 27, P, P, P, P, big, None),
+             lambda: lib.moe_int8_linear(ctypes.byref(m), P, 1 << 22, BF, 1, P, P, big, None),
+             lambda: lib.moe_int8_quant(P, (1 << 24) - 1, 64, F32, P, P, None),
+             lambda: lib.moe_grad_clip(side, 4, P, 0.0, None), lambda: lib.moe_grad_norm(side, 4, P, P, big, None)]
+    for f in calls:
+        assert f() in (L.MOE_EHIP, L.MOE_EUNSUPPORTED), lib.moe_last_error()
