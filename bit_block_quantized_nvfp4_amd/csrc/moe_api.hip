@@ -683,7 +683,8 @@ int moe_fp8_expert_ffn(const moe_fp8_weights* W, const uint16_t* x, int T, int K
 }
 
 static bool dense_sizes_ok(int T, int H, int I) {
-  return T >= 1 && H >= 8 && H <= 65536 && H % 8 == 0 && I >= 8 && I <= 65536 && I % 8 == 0;
+  return T >= 1 && T <= (1 << 30) && H >= 8 && H <= 65536 && H % 8 == 0 && I >= 8 && I <= 65536 &&
+         I % 8 == 0;
 }
 
 // What both dense entry points ask of the weights and the sizes.
@@ -693,7 +694,7 @@ static int dense_ok(const char* what, const moe_dense_weights& W, int T,
   if (W.dtype != MOE_DT_BF16 && W.dtype != MOE_DT_F16)
     return fail(MOE_EUNSUPPORTED, "%s: dtype %d is not bf16 or f16", what, W.dtype);
   if (!dense_sizes_ok(T, W.H, W.I))
-    return fail(MOE_EINVAL, "%s: need T >= 1, H and I multiples of 8 in [8, 65536] (T=%d H=%d I=%d)", what, T, W.H, W.I);
+    return fail(MOE_EINVAL, "%s: need 1 <= T <= 2^30, H and I multiples of 8 in [8, 65536] (T=%d H=%d I=%d)", what, T, W.H, W.I);
   if (!grid_ok(threads(T, W.H, W.I))) return too_many_rows(what, T);
   return MOE_OK;
 }
@@ -806,24 +807,39 @@ static int grad_list_ok(const char* what, const moe_grad_tensor* list, int count
   return MOE_OK;
 }
 
-// Two outputs of a list may not share memory (a tensor named twice): the launches would
-// scale it in an order of their own.
+// Two outputs of a list may not share memory (a tensor named twice), nor an output and a
+// gradient but its own in place: the launches would read and scale them in an order of
+// their own.
 static int grad_outs_ok(const moe_grad_tensor* list, int count) {
   struct Range {
     uintptr_t from, to;
+    int of;
+  };
+  const auto range = [&](const void* p, int i) {
+    const uintptr_t at = (uintptr_t)p;
+    return Range{at, at + (uintptr_t)list[i].n * (list[i].dtype == MOE_DT_F32 ? 4 : 2), i};
   };
   std::vector<Range> r;
   r.reserve((size_t)count);
-  bool sorted = true;
+  bool sorted = true, in_place = true;
   for (int i = 0; i < count; ++i) {
     if (list[i].n == 0) continue;
-    const uintptr_t p = (uintptr_t)list[i].out;
-    r.push_back(Range{p, p + (uintptr_t)list[i].n * (list[i].dtype == MOE_DT_F32 ? 4 : 2)});
-    sorted = sorted && (r.size() == 1 || r[r.size() - 2].from <= p);
+    r.push_back(range(list[i].out, i));
+    sorted = sorted && (r.size() == 1 || r[r.size() - 2].from <= r.back().from);
+    in_place = in_place && list[i].grad == list[i].out;
   }
   if (!sorted) std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.from < b.from; });
   for (size_t i = 1; i < r.size(); ++i)
     if (r[i].from < r[i - 1].to) return fail(MOE_EINVAL, "moe_grad_clip: two outputs overlap");
+  for (int i = 0; i < count && !in_place; ++i) {
+    if (list[i].n == 0) continue;
+    const Range g = range(list[i].grad, i);
+    // the first output that ends behind the gradient's begin, and those after it
+    for (auto o = std::partition_point(r.begin(), r.end(), [&](const Range& o) { return o.to <= g.from; });
+         o != r.end() && o->from < g.to; ++o)
+      if (o->of != i || o->from != g.from)
+        return fail(MOE_EINVAL, "moe_grad_clip: an output overlaps a gradient that is not its own");
+  }
   return MOE_OK;
 }
 

@@ -6,15 +6,15 @@
 // stands in memory with k running fastest, or (16 bits) with its rows running
 // fastest: the transposed matrix, as the gradients need it.
 //
-// A block computes BN columns of BM rows in steps of SB = 64 or 128 bytes along K.
+// A block computes BN columns of BM rows in steps of 128 bytes along K.
 // Both operands go from memory to LDS without registers, 16 bytes a lane, A's NA and
 // B's NB steps deep; a step's products then run on the 32x32 MFMA with sums in 32 bits.
 // B is the MFMA's first operand, so a lane holds four consecutive outputs of a row.
 //
-// LDS.  k fastest: a row of a step is SB bytes, its 16-byte chunk c stands at place
-// c ^ (row / (256 / SB) % (SB / 16)), so that the 16 rows that one cycle of a
-// 16-byte read serves meet all 64 banks.  Rows fastest: a k is a line of BN (BM) values, read with
-// the transposing load: 16 lanes get four k of 16 rows; its chunks are permuted so
+// LDS.  k fastest: a row of a step is 128 bytes, its 16-byte chunk c stands at place
+// c ^ (row / 2 % 8), so that the 16 rows that one cycle of a 16-byte read serves meet
+// all 64 banks.  Rows fastest: a k is a line of BN (BM) values, read with the
+// transposing load: 16 lanes get four k of 16 rows; its chunks are permuted so
 // that the four lines of such a load meet different banks.  The loads to LDS write
 // lanes in order, so both permutations are applied to the addresses they read.
 //
@@ -79,6 +79,7 @@ struct TileArgs16 {
   const float* sn;
 };
 
+constexpr int SB = 128;  // bytes of a step along K, of each row
 constexpr uint32_t kNowhere = 0x80000000u;  // past the end of every buffer (all below 2^31 bytes)
 
 // Permutation of the 16-byte chunks of a line: rows fastest, a line of CPR chunks.
@@ -90,13 +91,13 @@ __device__ __forceinline__ int line_swz(int k) {
 // One operand of a block: R rows of it, ROWS fastest or k fastest, brought by NT
 // threads.  GATED: the first half of the rows are gate rows, the second the up rows of
 // the same columns, which stand `up` bytes behind.
-template <int ES, bool ROWS, int R, int NT, bool GATED, int SB>
+template <int ES, bool ROWS, int R, int NT, bool GATED>
 struct Operand {
   static constexpr int kC = SB / 16;           // chunks of a row and step
   static constexpr int kLoads = R * kC / NT;   // per thread and step
   static constexpr int CPR = R / 8;            // chunks of a line (rows fastest)
   static constexpr int KS = SB / ES;           // values of K in a step
-  static_assert(R * kC % NT == 0 && (NT % 128 == 0 || (NT == 64 && SB == 128)) && (!ROWS || (ES == 2 && !GATED)) && (!GATED || kLoads % 2 == 0),
+  static_assert(R * kC % NT == 0 && NT % 64 == 0 && (!ROWS || (ES == 2 && !GATED)) && (!GATED || kLoads % 2 == 0),
                 "operand shape");
   const char* base;
   const char* up;
@@ -165,7 +166,7 @@ struct Operand {
 };
 
 // 32 rows from `row` of an operand in LDS, the ks-th 32 bytes of the step.
-template <bool ROWS, int R, int SB>
+template <bool ROWS, int R>
 __device__ __forceinline__ u32x4 operand_at(const lds_u8* p, int row, int ks, int lane) {
   if constexpr (ROWS) {
     constexpr int CPR = R / 8, LINE = R * 2;
@@ -179,7 +180,7 @@ __device__ __forceinline__ u32x4 operand_at(const lds_u8* p, int row, int ks, in
   } else {
     const int fr = lane & 31, fq = lane >> 5;
     return *(const __attribute__((address_space(3))) u32x4*)(
-        p + (row + fr) * SB + (((fq + 2 * ks) ^ (fr / (256 / SB) % (SB / 16))) << 4));
+        p + (row + fr) * SB + (((fq + 2 * ks) ^ (fr / 2 % 8)) << 4));
   }
 }
 
@@ -194,9 +195,9 @@ struct NoPre {
 // KG groups of waves with buffers of their own take every KG-th step and join their sums
 // at the end, in the groups' order: where there are few tiles, a step costs its
 // waiting whatever its size.
-template <int BN_, int BM_, int WN_, int WM_, int SB_, int NA_, int NB_, int KG_ = 1>
+template <int BN_, int BM_, int WN_, int WM_, int NA_, int NB_, int KG_ = 1>
 struct TileShape {
-  static constexpr int BN = BN_, BM = BM_, WN = WN_, WM = WM_, SB = SB_, NA = NA_, NB = NB_, KG = KG_;
+  static constexpr int BN = BN_, BM = BM_, WN = WN_, WM = WM_, NA = NA_, NB = NB_, KG = KG_;
   static constexpr int kThreads = 64 * WN * WM * KG;
   static constexpr int kGroupLds = (NA * BM + NB * BN) * SB, kLds = KG * kGroupLds;
 };
@@ -204,7 +205,7 @@ struct TileShape {
 // Block `blk` of the `blocks` of a product.
 template <int EL, bool BROWS, bool AROWS, class EP, class TS>
 __device__ __forceinline__ void tile_block(const TileArgs16& a, const int blk, const int blocks, lds_u8* const lds) {
-  constexpr int BN = TS::BN, BM = TS::BM, WN = TS::WN, WM = TS::WM, SB = TS::SB, NA = TS::NA, NB = TS::NB, KG = TS::KG;
+  constexpr int BN = TS::BN, BM = TS::BM, WN = TS::WN, WM = TS::WM, NA = TS::NA, NB = TS::NB, KG = TS::KG;
   constexpr int NW = WN * WM, NT = 64 * NW;                  // waves and threads of a group
   constexpr int TN = BN / WN, TM = BM / WM;
   constexpr int FN = TN / 32, FM = TM / 32;
@@ -234,8 +235,8 @@ __device__ __forceinline__ void tile_block(const TileArgs16& a, const int blk, c
   const int m0 = __builtin_amdgcn_readfirstlane((grp * 8 + in % gm) * BM);
   const int n0 = __builtin_amdgcn_readfirstlane((in / gm) * BC);
 
-  typedef Operand<ES, BROWS, BN, NT, G, SB> OpB;
-  typedef Operand<ES, AROWS, BM, NT, false, SB> OpA;
+  typedef Operand<ES, BROWS, BN, NT, G> OpB;
+  typedef Operand<ES, AROWS, BM, NT, false> OpA;
   constexpr int LA = OpA::kLoads, D = LA + OpB::kLoads;
   // loads that a wave may have under way where it waits for the next step's
   constexpr int kAhead = (NA - 2) * D + (NB > NA ? D - LA : 0);
@@ -285,12 +286,12 @@ __device__ __forceinline__ void tile_block(const TileArgs16& a, const int blk, c
   // b's others.
   const lds_u8 *pa = l0 + NB * kB, *pb = l0;
   auto read = [&](Frags& f, int r, int ks) __attribute__((always_inline)) {
-    if (r > 0 && r <= FM) f.a[r - 1] = operand_at<AROWS, BM, SB>(pa, wm * TM + 32 * (r - 1), ks, lane);
+    if (r > 0 && r <= FM) f.a[r - 1] = operand_at<AROWS, BM>(pa, wm * TM + 32 * (r - 1), ks, lane);
     else {
       const int i = r ? r - FM : 0;
       // gated: a wave's columns are gates, then the ups of the same outputs
       const int row = !G ? wn * TN + 32 * i : wn * TC + 32 * i + (i < FN / 2 ? 0 : BN / 2 - TC);
-      f.b[i] = operand_at<BROWS, BN, SB>(pb, row, ks, lane);
+      f.b[i] = operand_at<BROWS, BN>(pb, row, ks, lane);
     }
   };
   // The products of f, and between them the reads of g, the operands of the next ones,
@@ -435,15 +436,15 @@ __global__ __launch_bounds__(TS::kThreads) void k_tile(TileArgs16 a) {
 constexpr int kTileShapes16 = 6;
 template <typename F>
 static void by_shape(int shape, F&& f) {
-  if (shape == 0) f(TileShape<256, 256, 2, 2, 128, 2, 3>{});
-  if (shape == 1) f(TileShape<128, 128, 2, 2, 128, 2, 2>{});
-  if (shape == 2) f(TileShape<128, 128, 2, 2, 128, 2, 2, 2>{});
-  if (shape == 3) f(TileShape<64, 64, 1, 2, 128, 4, 4>{});
-  if (shape == 4) f(TileShape<64, 64, 1, 2, 128, 4, 4, 2>{});
-  if (shape == 5) f(TileShape<64, 32, 1, 1, 128, 3, 3, 4>{});
+  if (shape == 0) f(TileShape<256, 256, 2, 2, 2, 3>{});
+  if (shape == 1) f(TileShape<128, 128, 2, 2, 2, 2>{});
+  if (shape == 2) f(TileShape<128, 128, 2, 2, 2, 2, 2>{});
+  if (shape == 3) f(TileShape<64, 64, 1, 2, 4, 4>{});
+  if (shape == 4) f(TileShape<64, 64, 1, 2, 4, 4, 2>{});
+  if (shape == 5) f(TileShape<64, 32, 1, 1, 3, 3, 4>{});
 }
 
-// Tiles of a product in a shape, and steps along K (of 128 bytes).
+// Tiles of a product in a shape, and steps along K.
 static inline long tiles_of(int shape, int M, int cols) {
   long n = 0;
   by_shape(shape, [&](auto s) {
@@ -451,7 +452,7 @@ static inline long tiles_of(int shape, int M, int cols) {
   });
   return n;
 }
-static inline long steps_of(int K, int es) { return ((long)K * es + 127) / 128; }
+static inline long steps_of(int K, int es) { return ((long)K * es + SB - 1) / SB; }
 
 // Time of one round of tiles on the chip, in 10 ns: `fixed` + steps * `step` with all its
 // places taken (two blocks of the smaller shapes fit on a compute unit), and with one

@@ -582,7 +582,7 @@ int moe_fp8_expert_ffn(const moe_fp8_weights* W, const uint16_t* x, int T, int K
  *
  *   ws  at least moe_dense_ffn_workspace_bytes(T, H, I), or ..._grad_...(T, H, I)
  *
- * Limits: T >= 1, H and I multiples of 8 in [8, 65536], pointers aligned to 16 bytes,
+ * Limits: 1 <= T <= 2^30, H and I multiples of 8 in [8, 65536], pointers aligned to 16 bytes,
  * launches of fewer than 2^32 threads: products that large take one per 256 outputs
  * (T 2I forward; T H + 3 H I behind dh), those of narrow matrices up to one per 8.
  * Outputs and workspace may not overlap one another or the inputs.
@@ -659,7 +659,7 @@ int moe_int8_linear(const moe_int8_matrix* M, const void* x, int T, int dtype, i
  *   ws  at least moe_grad_norm_workspace_bytes(count) bytes, aligned to 8
  *
  * Limits: 1 <= count <= 2^20, 0 <= n <= 2^37, max_norm finite and >= 0.  No output
- * may overlap another tensor of the list (two outputs that do are refused).
+ * may overlap another tensor of the list (refused).
  */
 typedef struct moe_grad_tensor {
   const void* grad;

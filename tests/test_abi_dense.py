@@ -52,7 +52,7 @@ def test_dense_refusals(L, lib):
         _is(L, c(gu=0), E, b"weight pointer")
         _is(L, c(dn=0), E, b"weight pointer")
         _is(L, c(dt=F32), L.MOE_EUNSUPPORTED, b"dtype")
-        _is(L, c(T=0), E, b"T >= 1")
+        _is(L, c(T=0), E, b"1 <= T")
         _is(L, c(H=12), E, b"multiples of 8")
         _is(L, c(I=4), E, b"multiples of 8")
         _is(L, c(H=65544), E, b"65536")
@@ -63,6 +63,8 @@ def test_dense_refusals(L, lib):
         _is(L, c(ws=None), L.MOE_EWORKSPACE, b"workspace")
         _is(L, c(nb=63), L.MOE_EWORKSPACE, b"workspace")
         _is(L, c(T=1 << 30, H=65536, I=65536), E, b"2^32 threads")
+    for c in (f, g):
+        _is(L, c(T=(1 << 30) + 1, H=8, I=8), E, b"2^30")
     _is(L, f(y=None), E, b"null")
     _is(L, f(y=ODD), E, b"aligned")
     _is(L, f(k=ODD), E, b"aligned")
@@ -143,6 +145,9 @@ def test_gradient_list_refusals(L, lib):
         _is(L, clip(tensors(good), top=top), E, b"max_norm")
     _is(L, clip(tensors(good, good)), E, b"overlap")
     _is(L, clip(tensors((64, 100, 4, F32), (64, 64, 10, BF), (64, 84, 9, BF))), E, b"overlap")
+    for other in ((64, 1000, 10, BF), (60, 1000, 4, BF), (83 & ~1, 1000, 2, BF)):
+        _is(L, clip(tensors((2000, 64, 10, BF), other)), E, b"not its own")
+    _is(L, clip(tensors((64, 66, 10, BF))), E, b"not its own")
     norm = calls["norm"]
     _is(L, norm(tensors(good), ws=None), L.MOE_EWORKSPACE, b"workspace")
     _is(L, norm(tensors(good), nb=wsb(1) - 1), L.MOE_EWORKSPACE, b"workspace")
@@ -189,11 +194,13 @@ def test_calls_within_the_limits_are_accepted(L, lib):
     big = 1 << 60
     w = L.MoeDenseWeights(64, 64, 64, 64, BF)
     m = L.MoeInt8Matrix(64, 64, 131072, 65536)
-    side = (L.MoeGradTensor * 4)(*[L.MoeGradTensor(*t) for t in ((64, 64, 10, BF), (64, 84, 0, BF), (128, 84, 9, BF), (64, 102, 1, F16))])
+    side = (L.MoeGradTensor * 4)(*[L.MoeGradTensor(*t) for t in ((64, 64, 10, BF), (64, 84, 0, BF), (128, 84, 9, BF), (600, 102, 1, F16))])
+    apart = (L.MoeGradTensor * 3)(*[L.MoeGradTensor(*t) for t in ((64, 1084, 10, BF), (84, 1000, 10, BF), (64, 2000, 10, BF))])
     calls = [lambda: lib.moe_dense_ffn(ctypes.byref(w), P, 1 << 27, P, P, P, big, None),
              lambda: lib.moe_dense_ffn_grad(ctypes.byref(w), P, P, P, 1 << 27, P, P, P, P, big, None),
              lambda: lib.moe_int8_linear(ctypes.byref(m), P, 1 << 22, BF, 1, P, P, big, None),
              lambda: lib.moe_int8_quant(P, (1 << 24) - 1, 64, F32, P, P, None),
-             lambda: lib.moe_grad_clip(side, 4, P, 0.0, None), lambda: lib.moe_grad_norm(side, 4, P, P, big, None)]
+             lambda: lib.moe_grad_clip(side, 4, P, 0.0, None), lambda: lib.moe_grad_clip(apart, 3, P, 0.0, None),
+             lambda: lib.moe_grad_norm(side, 4, P, P, big, None)]
     for f in calls:
         assert f() in (L.MOE_EHIP, L.MOE_EUNSUPPORTED), lib.moe_last_error()
