@@ -433,15 +433,17 @@ __global__ __launch_bounds__(TS::kThreads) void k_tile(TileArgs16 a) {
 // ---- host side: the shapes, and which of them a product takes
 
 // f with the shape as a type.
-constexpr int kTileShapes16 = 6;
+constexpr int kTileShapes16 = 8;
 template <typename F>
 static void by_shape(int shape, F&& f) {
   if (shape == 0) f(TileShape<256, 256, 2, 2, 2, 3>{});
-  if (shape == 1) f(TileShape<128, 128, 2, 2, 2, 2>{});
-  if (shape == 2) f(TileShape<128, 128, 2, 2, 2, 2, 2>{});
-  if (shape == 3) f(TileShape<64, 64, 1, 2, 4, 4>{});
-  if (shape == 4) f(TileShape<64, 64, 1, 2, 4, 4, 2>{});
-  if (shape == 5) f(TileShape<64, 32, 1, 1, 3, 3, 4>{});
+  if (shape == 1) f(TileShape<256, 128, 2, 2, 2, 3>{});
+  if (shape == 2) f(TileShape<128, 128, 2, 2, 4, 4>{});
+  if (shape == 3) f(TileShape<128, 128, 2, 2, 2, 2>{});
+  if (shape == 4) f(TileShape<128, 64, 2, 2, 3, 3, 2>{});
+  if (shape == 5) f(TileShape<64, 64, 1, 2, 4, 4>{});
+  if (shape == 6) f(TileShape<64, 64, 1, 2, 4, 4, 2>{});
+  if (shape == 7) f(TileShape<64, 32, 1, 1, 3, 3, 4>{});
 }
 
 // Tiles of a product in a shape, and steps along K.
@@ -454,25 +456,31 @@ static inline long tiles_of(int shape, int M, int cols) {
 }
 static inline long steps_of(int K, int es) { return ((long)K * es + SB - 1) / SB; }
 
-// Time of one round of tiles on the chip, in 10 ns: `fixed` + steps * `step` with all its
-// places taken (two blocks of the smaller shapes fit on a compute unit), and with one
-// block on each.  From launches of 128 to 1024 tiles and 1 to 64 steps (bf16, in a row in
-// a graph, us; the three layouts differ by up to a tenth):
+// Time of a round of tiles on the chip, in 10 ns, beyond the launch's 2.5 us: `fixed1` +
+// steps * `step1` with one block on each compute unit, the first of them; `fixed` + steps *
+// `step` every further one, or with two blocks on each where `places` is 512.  From
+// launches of 256 and 1024 tiles, 1 to 64 steps (bf16, in a row in a graph, us; the three
+// layouts differ by up to a tenth, 8-bit integers by the writes of as many more outputs
+// per byte):
 //                        256 tiles                      1024 tiles
 //   steps            1     4    16     64         1     4    16     64
-//   256 x 256     13.7  18.0  35.8    111      40.2  58.1   132    424
-//   128 x 128      5.2   7.4  15.5   60.1      13.2  17.4  46.7    150
-//   128 x 128, 2   6.4   7.7  13.4   47.6      20.9  24.3  58.9    180
-//   64 x 64        3.6   4.6   8.3   23.1       8.0   9.2  17.3   59.0
-//   64 x 64, 2     4.2   4.8   7.2   17.0      13.2  15.1  24.2   74.6
-//   64 x 32, 4     4.6   4.8   6.4   12.6      14.5  15.1  20.8   56.1
-// (", 2": groups along K).
+//   256 x 256     13.6  17.8  35.8    113      39.7  60.0   135    421
+//   256 x 128      8.6  10.8  20.5   65.4      25.0  31.3  86.0    251
+//   128 x 128, a   5.7   7.2  13.0   43.5      17.5  21.6  51.1    160
+//   128 x 128, b   5.4   7.8  15.7   60.6      12.9  17.1  46.3    151
+//   128 x 64, 2    4.7   5.6   8.7   27.0      15.5  17.3  37.1    110
+//   64 x 64        3.7   4.7   8.5   23.4       7.6   9.2  17.1   60.4
+//   64 x 64, 2     4.2   4.8   7.2   16.6      13.4  15.4  23.7   77.7
+//   64 x 32, 4     4.6   4.7   6.2   12.3      14.5  14.9  20.6   55.7
+// (a: buffers of four steps, one block on a compute unit; b: two steps, two blocks, which
+// pays where steps are few; ", 2": groups along K).
 struct TileCost {
-  int places, fixed, step, fixed1, step1;
+  int places, fixed1, step1, fixed, step;
 };
 static inline TileCost tile_cost(int shape) {
-  constexpr TileCost c[kTileShapes16] = {{256, 900, 155, 900, 155}, {512, 620, 110, 460, 87}, {256, 530, 64, 530, 64},
-                                         {512, 360, 41, 330, 31},   {256, 380, 22, 380, 22},  {256, 400, 14, 400, 14}};
+  constexpr TileCost c[kTileShapes16] = {{256, 870, 157, 830, 151}, {256, 460, 91, 400, 93}, {256, 240, 58, 300, 57},
+                                         {512, 170, 88, 285, 112},  {256, 165, 36, 240, 40}, {512, 90, 32, 130, 43},
+                                         {256, 150, 20, 220, 28},   {256, 175, 13, 260, 18}};
   return c[shape];
 }
 // The shape in which the rounds of a product's tiles take the least time together.
@@ -481,9 +489,9 @@ static inline int tile_shape(int M, int cols, long steps) {
   long least = 0;
   for (int s = 0; s < kTileShapes16; ++s) {
     const TileCost c = tile_cost(s);
-    const long tiles = tiles_of(s, M, cols), full = tiles / c.places, rest = tiles % c.places;
-    const long whole = c.fixed + steps * c.step, one = c.fixed1 + steps * c.step1;
-    const long t = full * whole + (rest == 0 ? 0 : rest <= 256 ? one : whole);
+    const long tiles = tiles_of(s, M, cols), rounds = (tiles + c.places - 1) / c.places, rest = tiles % c.places;
+    const long one = c.places == 256 || (rest > 0 && rest <= 256) ? 1 : 0;
+    const long t = (rounds - one) * (c.fixed + steps * c.step) + one * (c.fixed1 + steps * c.step1);
     if (least == 0 || t < least) least = t, best = s;
   }
   return best;

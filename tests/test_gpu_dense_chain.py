@@ -147,7 +147,8 @@ def test_two_streams_at_once(moe, T):
 # sizes that take each tile shape and stream the operators' own tests leave out
 @pytest.mark.parametrize("dtype", HALVES)
 @pytest.mark.parametrize("T,H,I", [(1030, 264, 1032), (1030, 2056, 72), (1030, 520, 520), (3, 72, 4104), (12, 4104, 72),
-                                   (9, 264, 8200)])
+                                   (9, 264, 8200), (1030, 136, 1032), (260, 264, 2056), (1030, 4104, 520),
+                                   (4100, 520, 72), (520, 4104, 264), (260, 2056, 72), (64, 65536, 64)])
 def test_other_tiles_of_the_block(moe, T, H, I, dtype):
     flush(f"dense tiles T={T} H={H} I={I} {dtype}")
     gen = torch.Generator().manual_seed(I)
@@ -161,7 +162,8 @@ def test_other_tiles_of_the_block(moe, T, H, I, dtype):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("gated", [False, True])
-@pytest.mark.parametrize("T,N,K", [(4100, 2064, 48), (1030, 2064, 528), (1030, 528, 1040), (6, 2064, 8208), (12, 2064, 16400),
+@pytest.mark.parametrize("T,N,K", [(4100, 2064, 48), (1030, 2064, 528), (1030, 528, 1040), (1030, 2064, 272), (4100, 1040, 1040),
+                                   (1030, 1040, 528), (2100, 4112, 2064), (6, 2064, 8208), (12, 2064, 16400),
                                    (2, 8208, 144), (7, 8208, 272), (5, 272, 144)])
 def test_other_tiles_of_the_products_in_8_bits(moe, T, N, K, gated, dtype):
     flush(f"int8 tiles T={T} N={N} K={K} gated={gated} {dtype}")
