@@ -66,21 +66,24 @@ __global__ __launch_bounds__(TS::kThreads) void k_dense_grads(GradArgs g) {
                                                   first ? g.dgu_blocks : g.ddn_blocks, (lds_u8*)lds);
   }
 }
-// Their shape: the rounds of all tiles, each as long as its own steps.
+// Their shape: the longest product's tiles, alone on their compute units if those that are as
+// long leave room for that, or the rounds of all tiles, each as long as its own steps.
 static int grads_shape(const GradArgs& g) {
   int best = 0;
   long least = 0;
   for (int s = 0; s < kTileShapes16; ++s) {
     const TileCost c = tile_cost(s);
-    long tiles = 0, work = 0, longest = 0, longest1 = 0;
+    long tiles = 0, work = 0, t = 0;
     for (const TileArgs16* a : {&g.dx, &g.dgu, &g.ddn}) {
       const long n = tiles_of(s, a->M, a->N), steps = steps_of(a->K, 2);
+      long as_long = 0;
+      for (const TileArgs16* b : {&g.dx, &g.dgu, &g.ddn})
+        if (b->K >= a->K) as_long += tiles_of(s, b->M, b->N);
       tiles += n;
       work += n * (c.fixed + steps * c.step);
-      longest = std::max(longest, c.fixed + steps * c.step);
-      longest1 = std::max(longest1, c.fixed1 + steps * c.step1);
+      t = std::max(t, as_long <= 256 ? c.fixed1 + steps * c.step1 : c.fixed + steps * c.step);
     }
-    const long t = tiles <= 256 ? longest1 : tiles <= c.places ? longest : std::max(longest, work / c.places);
+    if (tiles > c.places) t = std::max(t, work / c.places);
     if (least == 0 || t < least) least = t, best = s;
   }
   return best;
