@@ -22,9 +22,8 @@ static hipError_t product(const char* name, TileArgs16 a, hipStream_t s) {
   const int cols = EP::kGated ? 2 * a.N : a.N, best = tile_shape(a.M, cols, steps_of(a.K, 2));
   by_shape(best, [&](auto shape) {
     a.nt = (cols + shape.BN - 1) / shape.BN;
-    const long tiles = tiles_of(best, a.M, cols);
-    MOE_LAUNCH(name, s, (k_tile<DT, BROWS, false, EP, decltype(shape)>), dim3(blocks_of<EP>(shape, tiles)),
-               dim3(shape.kThreads), 0, s, a, (int)tiles);
+    MOE_LAUNCH(name, s, (k_tile<DT, BROWS, false, EP, decltype(shape)>), dim3((unsigned)tiles_of(best, a.M, cols)),
+               dim3(shape.kThreads), 0, s, a);
   });
   return hipGetLastError();
 }

@@ -175,9 +175,8 @@ hipError_t launch_int8_linear(const moe_int8_matrix& W, const void* x, int T, in
         const int best = tile_shape(T, W.N, steps_of(W.K, 1));
         by_shape(best, [&](auto shape) {
           a.nt = (W.N + shape.BN - 1) / shape.BN;
-          const long tiles = tiles_of(best, T, W.N);
           MOE_LAUNCH("int8_tile", s, (k_tile<kElI8, false, false, EP, decltype(shape)>),
-                     dim3(blocks_of<EP>(shape, tiles)), dim3(shape.kThreads), 0, s, a, (int)tiles);
+                     dim3((unsigned)tiles_of(best, T, W.N)), dim3(shape.kThreads), 0, s, a);
         });
       }
     };

@@ -202,11 +202,9 @@ struct TileShape {
   static constexpr int kGroupLds = (NA * BM + NB * BN) * SB, kLds = KG * kGroupLds;
 };
 
-// Block `blk` of the `tiles` of a product.  STAY > 0: and every STAY-th tile after it.  The
-// next tile's first steps are then on their way while this one's epilogue runs, which
-// stages through the buffers that they leave.
-template <int EL, bool BROWS, bool AROWS, class EP, class TS, int STAY = 0>
-__device__ __forceinline__ void tile_block(const TileArgs16& a, int blk, const int tiles, lds_u8* const lds) {
+// Block `blk` of the `blocks` of a product.
+template <int EL, bool BROWS, bool AROWS, class EP, class TS>
+__device__ __forceinline__ void tile_block(const TileArgs16& a, const int blk, const int blocks, lds_u8* const lds) {
   constexpr int BN = TS::BN, BM = TS::BM, WN = TS::WN, WM = TS::WM, NA = TS::NA, NB = TS::NB, KG = TS::KG;
   constexpr int NW = WN * WM, NT = 64 * NW;                  // waves and threads of a group
   constexpr int TN = BN / WN, TM = BM / WM;
@@ -221,11 +219,7 @@ __device__ __forceinline__ void tile_block(const TileArgs16& a, int blk, const i
   typedef typename Mma<EL>::Four Four;
   static_assert(TN % 32 == 0 && TM % 32 == 0 && (!G || FN % 2 == 0) && NA >= 2 && NB >= NA, "tile shape");
   constexpr int kStage = 32 * TN * 4;                        // bytes of 32 staged rows
-  // places of staged rows of a wave, and where they begin
-  constexpr int kPlaces = STAY ? 1 : 2, kStageAt = STAY ? (NB - 1) * kB : 0;
-  static_assert(kStageAt + NW * kPlaces * kStage <= (STAY ? NB * kB + kA : KG * kLds) && CH <= 32 && (CH & (CH - 1)) == 0,
-                "staged rows");
-  static_assert(STAY % 8 == 0 && (!STAY || (KG == 1 && NA == 2)), "a block's next tile");
+  static_assert(NW * 2 * kStage <= KG * kLds && CH <= 32 && (CH & (CH - 1)) == 0, "staged rows");
   const int kg = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane((int)threadIdx.x / NT);
   const int tid = (int)threadIdx.x - kg * NT, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -234,15 +228,12 @@ __device__ __forceinline__ void tile_block(const TileArgs16& a, int blk, const i
   // Blocks are dealt to the 8 XCDs in turn: each XCD gets a run of tiles, 8 row tiles
   // deep before the next column tile, so that the blocks that run together on one
   // share the lines of both operands in its L2
-  int m0, n0;
-  auto place = [&](int b) __attribute__((always_inline)) {
-    const int mt = (a.M + BM - 1) / BM, per = tiles / 8;
-    const int lin = b < per * 8 ? (b % 8) * per + b / 8 : b;
-    const int deep = 8 * a.nt, grp = lin / deep, in = lin % deep;
-    const int gm = min(8, mt - grp * 8);
-    m0 = __builtin_amdgcn_readfirstlane((grp * 8 + in % gm) * BM);
-    n0 = __builtin_amdgcn_readfirstlane((in / gm) * BC);
-  };
+  const int mt = (a.M + BM - 1) / BM, per = blocks / 8;
+  const int lin = blk < per * 8 ? (blk % 8) * per + blk / 8 : blk;
+  const int deep = 8 * a.nt, grp = lin / deep, in = lin % deep;
+  const int gm = min(8, mt - grp * 8);
+  const int m0 = __builtin_amdgcn_readfirstlane((grp * 8 + in % gm) * BM);
+  const int n0 = __builtin_amdgcn_readfirstlane((in / gm) * BC);
 
   typedef Operand<ES, BROWS, BN, NT, G> OpB;
   typedef Operand<ES, AROWS, BM, NT, false> OpA;
@@ -252,6 +243,8 @@ __device__ __forceinline__ void tile_block(const TileArgs16& a, int blk, const i
   static_assert(kAhead + D < 64, "loads under way");
   OpB ob;
   OpA oa;
+  ob.set(a.b, a.ldb, n0, a.N - n0, a.K, (long)a.N * a.ldb, tid);
+  oa.set(a.a, a.lda, m0, a.M - m0, a.K, 0, tid);
   lds_u8* const l0 = lds + kg * kLds;
   const uint32_t ldsw = (uint32_t)(uintptr_t)l0 + wv * 1024;
   const int steps = ((a.K * ES + SB - 1) / SB + KG - 1) / KG;  // of a group
@@ -274,28 +267,12 @@ __device__ __forceinline__ void tile_block(const TileArgs16& a, int blk, const i
     if (i == D - 1) b_at = b_at == (NB - 1) * kB ? 0 : b_at + kB;
   };
   constexpr int L = D / KF;  // loads that go with the first products
-  // The first steps of tile b, all but those of step 0's turn, from the last buffer of A's.
-  const lds_u8 *pa, *pb;
-  auto first = [&](int b) __attribute__((always_inline)) {
-    place(b);
-    ob.set(a.b, a.ldb, n0, a.N - n0, a.K, (long)a.N * a.ldb, tid);
-    oa.set(a.a, a.lda, m0, a.M - m0, a.K, 0, tid);
-    a_at = (NA - 1) * kA;
-    b_at = 0;
-    pa = l0 + NB * kB + a_at;
-    pb = l0;
 #pragma unroll
-    for (int s = 1 - NB; s < 0; ++s) {
-      begin(s);
+  for (int s = 1 - NB; s <= 0; ++s) {
+    begin(s);
 #pragma unroll
-      for (int i = s > -NA ? 0 : LA; i < D; ++i) load(i);
-    }
-  };
-  first(blk);
-  for (;;) {
-  begin(0);
-#pragma unroll
-  for (int i = 0; i < L; ++i) load(i);
+    for (int i = s > -NA ? 0 : LA; i < (s < 0 ? D : L); ++i) load(i);
+  }
 
   Acc acc[FN][FM];
 #pragma unroll
@@ -307,6 +284,7 @@ __device__ __forceinline__ void tile_block(const TileArgs16& a, int blk, const i
   };
   // Operand r of the ks-th 32 bytes of the step at pa and pb: b's first, all of a's, then
   // b's others.
+  const lds_u8 *pa = l0 + NB * kB, *pb = l0;
   auto read = [&](Frags& f, int r, int ks) __attribute__((always_inline)) {
     if (r > 0 && r <= FM) f.a[r - 1] = operand_at<AROWS, BM>(pa, wm * TM + 32 * (r - 1), ks, lane);
     else {
@@ -398,19 +376,18 @@ __device__ __forceinline__ void tile_block(const TileArgs16& a, int blk, const i
   // memory is asked for 32 rows ahead.
   constexpr int LR = TC / 8, RP = 64 / LR, P = 32 / RP;  // lanes of a row, rows of a pass, passes
   const int fr = lane & 31, fq = lane >> 5;
-  const int r0 = lane / LR, c8 = lane % LR, n = n0 + wn * TC + 8 * c8, mrow = m0 + wm * TM + r0;
-  lds_u8* const mine = l0 + kStageAt + wv * (kPlaces * kStage);
-  if (STAY && blk + STAY < tiles) first(blk + STAY);
+  const int r0 = lane / LR, c8 = lane % LR, n = n0 + wn * TC + 8 * c8;
+  lds_u8* const mine = l0 + wv * (2 * kStage);
   auto stage = [&](int j) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < FN; ++i)
 #pragma unroll
       for (int g = 0; g < 4; ++g)
-        *(__attribute__((address_space(3))) Four*)(mine + j % kPlaces * kStage + fr * (TN * 4) +
+        *(__attribute__((address_space(3))) Four*)(mine + j % 2 * kStage + fr * (TN * 4) +
                                                    (((8 * i + 2 * g + fq) ^ (fr & (CH - 1))) << 4)) =
             Four{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
   };
-  auto row_of = [&](int j, int q) __attribute__((always_inline)) { return mrow + 32 * j + q * RP; };
+  auto row_of = [&](int j, int q) __attribute__((always_inline)) { return m0 + wm * TM + 32 * j + q * RP + r0; };
   typename EP::Pre pre[2][P];
   auto fetch = [&](int j) __attribute__((always_inline)) {
 #pragma unroll
@@ -423,7 +400,7 @@ __device__ __forceinline__ void tile_block(const TileArgs16& a, int blk, const i
   for (int j = 0; j < FM; ++j) {
     if (j + 1 < FM) {
       fetch(j + 1);
-      if (kPlaces > 1) stage(j + 1);
+      stage(j + 1);
     }
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -434,7 +411,7 @@ __device__ __forceinline__ void tile_block(const TileArgs16& a, int blk, const i
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const Four w = *(const __attribute__((address_space(3))) Four*)(
-              mine + j % kPlaces * kStage + r * (TN * 4) + (((c + h) ^ (r & (CH - 1))) << 4));
+              mine + j % 2 * kStage + r * (TN * 4) + (((c + h) ^ (r & (CH - 1))) << 4));
 #pragma unroll
           for (int e = 0; e < 4; ++e) f[4 * h + e] = (float)w[e];
         }
@@ -444,23 +421,13 @@ __device__ __forceinline__ void tile_block(const TileArgs16& a, int blk, const i
       if (m < a.M && n < a.N) EP::put(a, m, n, v, u, pre[j % 2][q]);
     }
     __builtin_amdgcn_wave_barrier();
-    if (kPlaces == 1 && j + 1 < FM) stage(j + 1);
-  }
-  blk += STAY;
-  if (!STAY || blk >= tiles) return;
-  meet();  // every wave has read its staged rows
   }
 }
 
-// Blocks of the largest tiles stay for further ones, but where the epilogue's own loads leave
-// no registers for the next tile's addresses.
-template <class EP, class TS>
-constexpr int kStay = TS::BN == 256 && TS::BM == 256 && sizeof(typename EP::Pre) <= 4 ? 256 : 0;
-
 template <int EL, bool BROWS, bool AROWS, class EP, class TS>
-__global__ __launch_bounds__(TS::kThreads) void k_tile(TileArgs16 a, int tiles) {
+__global__ __launch_bounds__(TS::kThreads) void k_tile(TileArgs16 a) {
   __shared__ __align__(1024) uint8_t lds[TS::kLds];
-  tile_block<EL, BROWS, AROWS, EP, TS, kStay<EP, TS>>(a, blockIdx.x, tiles, (lds_u8*)lds);
+  tile_block<EL, BROWS, AROWS, EP, TS>(a, blockIdx.x, gridDim.x, (lds_u8*)lds);
 }
 
 // ---- host side: the shapes, and which of them a product takes
@@ -529,12 +496,7 @@ static inline int tile_shape(int M, int cols, long steps) {
   }
   return best;
 }
-// Blocks of the launch of a product's tiles.
-template <class EP, class TS>
-static unsigned blocks_of(TS, long tiles) {
-  return (unsigned)(kStay<EP, TS> ? std::min<long>(tiles, kStay<EP, TS>) : tiles);
-}
-// Threads of a product's launch, or those that it would have with a block for each tile.
+// Threads of a product's launch.
 static inline uint64_t tile_threads(int M, int cols, long steps) {
   const int best = tile_shape(M, cols, steps);
   uint64_t t = 0;
