@@ -755,7 +755,7 @@ int moe_int8_quant(const void* x, int T, int K, int dtype, int8_t* codes, float*
   if (!dtype_ok(dtype)) return fail(MOE_EUNSUPPORTED, "moe_int8_quant: unknown dtype %d", dtype);
   if (!int8_k_ok(T, K))
     return fail(MOE_EINVAL, "moe_int8_quant: need T >= 1 and K a multiple of 16 in [16, 65536] (T=%d K=%d)", T, K);
-  if (!grid_ok((uint64_t)T * 256)) return too_many_rows("moe_int8_quant", T);
+  if (!grid_ok(moe::int8_quant_threads(T, K, dtype))) return too_many_rows("moe_int8_quant", T);
   if (!aligned16((const char*)x, (const char*)codes))
     return fail(MOE_EINVAL, "moe_int8_quant: rows must be aligned to 16 bytes");
   int rc = ensure_init();
@@ -776,7 +776,7 @@ int moe_int8_linear(const moe_int8_matrix* M, const void* x, int T, int dtype, i
   if (gated != 0 && gated != 1) return fail(MOE_EINVAL, "moe_int8_linear: gated must be 0 or 1");
   if (!int8_matrix_ok(T, M->N, M->K) || (gated && M->N % 16))
     return fail(MOE_EINVAL, "moe_int8_linear: need T >= 1, K a multiple of 16 in [16, 65536] and N a multiple of 8 (gated: 16) in [8, 131072] (T=%d N=%d K=%d)", T, M->N, M->K);
-  if (!grid_ok(moe::int8_linear_threads(T, M->N, M->K))) return too_many_rows("moe_int8_linear", T);
+  if (!grid_ok(moe::int8_linear_threads(T, M->N, M->K, dtype))) return too_many_rows("moe_int8_linear", T);
   if (!aligned16((const char*)x, (const char*)out, (const char*)M->codes, (const char*)ws))
     return fail(MOE_EINVAL, "moe_int8_linear: codes, rows and workspace must be aligned to 16 bytes");
   const size_t need = moe::int8_linear_workspace_bytes(T, M->N, M->K);

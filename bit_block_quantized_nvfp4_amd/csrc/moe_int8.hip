@@ -11,15 +11,18 @@
 
 namespace moe {
 
-// A block quantises a row.  Up to U chunks of 16 bytes a thread stay in registers between
-// the row's absmax and its codes; longer rows (U = 0) are read twice, from the L2 the
-// second time.  8192 rows of 2048: 14 us, of 8192: 45 us with every row read twice.
-template <int DT, int U>
-__global__ __launch_bounds__(256) void k_int8_quant(const void* __restrict__ x, int K,
-                                                    uint8_t* __restrict__ codes,
-                                                    float* __restrict__ scales) {
-  constexpr int N = Chunk<DT>::N;
-  __shared__ float part[4];
+// A block of W waves quantises a row, whose chunks of 16 bytes, up to U a thread, stay in
+// registers between its absmax and its codes; longer rows (U = 0) are read twice, from the
+// L2 the second time.  Bound by memory, few rows by the launch (in a row in a graph, us): 333
+// rows of 2064 f16 3.9, 8192 of 2048 bf16 13.5, of 8192 40.9, of 16384 90.8 (4.4 TB/s), 4 of 65536
+// 9.0; 4 waves reading twice take 144.6 and 21.6 for the last two, a wave to a row 6.4 and
+// 15.8 for the first two (the codes' arithmetic wants more waves).
+template <int DT, int U, int W>
+__global__ __launch_bounds__(64 * W) void k_int8_quant(const void* __restrict__ x, int K,
+                                                       uint8_t* __restrict__ codes,
+                                                       float* __restrict__ scales) {
+  constexpr int N = Chunk<DT>::N, L = 64 * W;
+  __shared__ float part[W];
   const int t = blockIdx.x, tid = threadIdx.x, chunks = K / N;
   const u32x4* p = (const u32x4*)((const char*)x + (size_t)t * K * (DT == MOE_DT_F32 ? 4 : 2));
   float am = 0.f;
@@ -34,18 +37,19 @@ __global__ __launch_bounds__(256) void k_int8_quant(const void* __restrict__ x, 
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       held[i] = u32x4{0u, 0u, 0u, 0u};
-      if (tid + 256 * i < chunks) held[i] = p[tid + 256 * i];
+      if (tid + L * i < chunks) held[i] = p[tid + L * i];
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) look(held[i]);
   } else {
-    for (int c = tid; c < chunks; c += 256) look(p[c]);
+    for (int c = tid; c < chunks; c += L) look(p[c]);
   }
 #pragma unroll
   for (int o = 1; o < 64; o *= 2) am = amax_nan(am, __shfl_xor(am, o));
   if ((tid & 63) == 0) part[tid >> 6] = am;
   __syncthreads();
-  am = amax_nan(amax_nan(part[0], part[1]), amax_nan(part[2], part[3]));
+#pragma unroll
+  for (int w = 0; w < W; ++w) am = amax_nan(am, part[w]);
   float mul, scale;
   bool fine;
   int8_scale(am, &mul, &scale, &fine);
@@ -59,30 +63,31 @@ __global__ __launch_bounds__(256) void k_int8_quant(const void* __restrict__ x, 
   if constexpr (U > 0) {
 #pragma unroll
     for (int i = 0; i < U; ++i)
-      if (tid + 256 * i < chunks) put(held[i], tid + 256 * i);
+      if (tid + L * i < chunks) put(held[i], tid + L * i);
   } else {
-    for (int c = tid; c < chunks; c += 256) put(p[c], c);
+    for (int c = tid; c < chunks; c += L) put(p[c], c);
   }
   if (tid == 0) scales[t] = scale;
 }
 
-// f with the chunks that a thread holds for rows of K values.
+// f with the chunks that a thread holds and the waves of a block for rows of K values.
 template <int DT, typename F>
 static void by_row(int K, F&& f) {
-  const int each = (K / Chunk<DT>::N + 255) / 256;
-  if (each <= 1) f(IntC<1>{});
-  else if (each <= 4) f(IntC<4>{});
-  else if (each <= 8) f(IntC<8>{});
-  else f(IntC<0>{});
+  const int waves = (K / Chunk<DT>::N + 63) / 64;  // loads of a wave
+  if (waves <= 4) f(IntC<1>{}, IntC<4>{});
+  else if (waves <= 16) f(IntC<4>{}, IntC<4>{});
+  else if (waves <= 64) f(IntC<4>{}, IntC<16>{});
+  else f(IntC<0>{}, IntC<16>{});
 }
 
 hipError_t launch_int8_quant(const void* x, int T, int K, int dtype, int8_t* codes, float* scales,
                              hipStream_t s) {
   by_dtype(dtype, [&](auto D) {
     constexpr int DT = decltype(D)::value;
-    by_row<DT>(K, [&](auto U) {
-      MOE_LAUNCH("int8_quant", s, (k_int8_quant<DT, decltype(U)::value>), dim3((unsigned)T), dim3(256), 0, s, x, K,
-                 (uint8_t*)codes, scales);
+    by_row<DT>(K, [&](auto U, auto W) {
+      constexpr int kWaves = decltype(W)::value;
+      MOE_LAUNCH("int8_quant", s, (k_int8_quant<DT, decltype(U)::value, kWaves>), dim3((unsigned)T),
+                 dim3(64 * kWaves), 0, s, x, K, (uint8_t*)codes, scales);
     });
   });
   return hipGetLastError();
@@ -111,10 +116,10 @@ void register_int8_kernels(std::vector<const void*>& k) {
   for (int dt = MOE_DT_BF16; dt <= MOE_DT_F32; ++dt)
     by_dtype(dt, [&](auto D) {
       constexpr int DT = decltype(D)::value;
-      k.push_back((const void*)&k_int8_quant<DT, 0>);
-      k.push_back((const void*)&k_int8_quant<DT, 1>);
-      k.push_back((const void*)&k_int8_quant<DT, 4>);
-      k.push_back((const void*)&k_int8_quant<DT, 8>);
+      for (int K : {16, 4096, 16384, 65536})
+        by_row<DT>(K, [&](auto U, auto W) {
+          k.push_back((const void*)&k_int8_quant<DT, decltype(U)::value, decltype(W)::value>);
+        });
       auto add_stream = [&](auto kernel, int, int) { k.push_back((const void*)kernel); };
       for (int M : {1, kStreamRows})
         for (int K : {16, 65536}) {
@@ -133,9 +138,16 @@ void register_int8_kernels(std::vector<const void*>& k) {
 
 static size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-uint64_t int8_linear_threads(int T, int N, int K) {
+uint64_t int8_quant_threads(int T, int K, int dtype) {
+  uint64_t n = 0;
+  by_dtype(dtype, [&](auto D) {
+    by_row<decltype(D)::value>(K, [&](auto, auto W) { n = (uint64_t)T * 64 * decltype(W)::value; });
+  });
+  return n;
+}
+uint64_t int8_linear_threads(int T, int N, int K, int dtype) {
   if (int8_streams(T)) return 0;  // at most 131072 / 8 blocks
-  return std::max(tile_threads(T, N, steps_of(K, 1)), (uint64_t)T * 256);
+  return std::max(tile_threads(T, N, steps_of(K, 1)), int8_quant_threads(T, K, dtype));
 }
 
 size_t int8_linear_workspace_bytes(int T, int N, int K) {

@@ -146,7 +146,8 @@ uint64_t fp8_linear_threads(int T, int N, int K);
 uint64_t fp8_expert_ffn_threads(const moe_fp8_weights& W, int T, int K);
 uint64_t dense_ffn_threads(int T, int H, int I);
 uint64_t dense_ffn_grad_threads(int T, int H, int I);
-uint64_t int8_linear_threads(int T, int N, int K);
+uint64_t int8_quant_threads(int T, int K, int dtype);
+uint64_t int8_linear_threads(int T, int N, int K, int dtype);
 
 // Token sort and its gradients (moe_sort.hip).
 void register_sort_kernels(std::vector<const void*>& k);

@@ -625,8 +625,9 @@ int moe_dense_ffn_grad(const moe_dense_weights* W, const void* dy, const void* x
  * row's outputs are NaN and no others.  The outputs may not overlap the inputs.
  * Limits: K a multiple of 16 in [16, 65536], N a multiple of 8 (gated: 16) in
  * [8, 131072], T >= 1, launches of fewer than 2^32 threads: 256 a row for the
- * quantisation, one per 256 outputs for a product that large (of a narrow matrix up to
- * one per 8); pointers of codes, x and out aligned to 16 bytes.
+ * quantisation (1024 past 8192 16-bit or 4096 f32 values), one per 256 outputs for a
+ * product that large (of a narrow matrix up to one per 8); pointers of codes, x and
+ * out aligned to 16 bytes.
  */
 typedef struct moe_int8_matrix {
   const int8_t* codes;

@@ -85,6 +85,7 @@ def test_int8_refusals(L, lib):
     _is(L, q(ODD, 4, 64, BF, P, P, None), E, b"aligned")
     _is(L, q(P, 4, 64, BF, ODD, P, None), E, b"aligned")
     _is(L, q(P, 1 << 24, 64, BF, P, P, None), E, b"2^32 threads")
+    _is(L, q(P, 1 << 22, 8208, BF, P, P, None), E, b"2^32 threads")
     wsb = lib.moe_int8_linear_workspace_bytes
     assert wsb(100, 16, 72) == 0 and wsb(100, 12, 64) == 0 and wsb(0, 16, 64) == 0 and wsb(100, 131080, 64) == 0
     assert wsb(100, 16, 64) >= 100 * 64 + 400
@@ -198,7 +199,7 @@ def test_calls_within_the_limits_are_accepted(L, lib):
     apart = (L.MoeGradTensor * 3)(*[L.MoeGradTensor(*t) for t in ((64, 1084, 10, BF), (84, 1000, 10, BF), (64, 2000, 10, BF))])
     calls = [lambda: lib.moe_dense_ffn(ctypes.byref(w), P, 1 << 27, P, P, P, big, None),
              lambda: lib.moe_dense_ffn_grad(ctypes.byref(w), P, P, P, 1 << 27, P, P, P, P, big, None),
-             lambda: lib.moe_int8_linear(ctypes.byref(m), P, 1 << 22, BF, 1, P, P, big, None),
+             lambda: lib.moe_int8_linear(ctypes.byref(m), P, (1 << 22) - 1, BF, 1, P, P, big, None),
              lambda: lib.moe_int8_quant(P, (1 << 24) - 1, 64, F32, P, P, None),
              lambda: lib.moe_grad_clip(side, 4, P, 0.0, None), lambda: lib.moe_grad_clip(apart, 3, P, 0.0, None),
              lambda: lib.moe_grad_norm(side, 4, P, P, big, None)]
