@@ -7,6 +7,10 @@
 // holds gate and up rows side by side.  h is the next product's operand and rounded to the
 // rows' type for that, as every operand of a 16-bit product is; all sums and the
 // activation are in f32.
+//
+// 8192 rows, H = 2048, I = 8192, bf16: 506 us (with the projections kept, whose 403 MB the
+// epilogue writes) and 219 us; 333 rows, 2056, 1032, f16: 11 and 7.4 us, by latency; 1 row, 2048,
+// 8192: 12.6 and 8.0 us, the weights from memory at 5.3 and 4.2 TB/s.
 #include "moe_dense.hpp"
 #include "moe_stream.hpp"
 
@@ -82,7 +86,6 @@ void register_dense_kernels(std::vector<const void*>& k) {
         });
     });
 }
-
 
 uint64_t dense_ffn_threads(int T, int H, int I) {
   if (T <= kStreamRows) return 0;  // at most 65536 / 8 blocks

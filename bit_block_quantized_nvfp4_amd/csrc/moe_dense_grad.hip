@@ -7,6 +7,10 @@
 // it: the activation's gradient is that product's epilogue, which reads the kept
 // projections and makes h again.  h, dg and du are operands of the next products and
 // rounded to the rows' type for that; all sums and the activation's gradient are in f32.
+//
+// 8192 rows, H = 2048, I = 8192, bf16: dh 370 to 387 us, of which its epilogue takes about 150 to
+// move 670 MB, the other three 1040 to 1056 us (1.30 PFLOP/s, the matrix unit at the clock
+// that the power allows); 133 rows, 1032, 520, f16: 8 and 10 us, by latency.
 #include "moe_dense.hpp"
 
 namespace moe {
@@ -48,7 +52,7 @@ struct PutGatedGrad {
 
 // The three products that follow from dgu and h, in one launch: dx (A's rows run along K,
 // B's across), then the weights' gradients (both across).  Small ones would not fill the
-// chip one after the other (T = 133, H = 1032, I = 520: 11.9 us together, 18.2 apart).
+// chip one after the other (T = 133, H = 1032, I = 520: 10 us together, 18 apart).
 struct GradArgs {
   TileArgs16 dx, dgu, ddn;
   int dx_blocks, dgu_blocks, ddn_blocks;

