@@ -36,13 +36,14 @@ struct PutGatedGrad {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       // e = exp(-g), s = 1 / (1 + e), 1 - s = e s: no difference that would lose its
-      // bits (with e infinite s is 0, and so is what 1 - s is multiplied with)
+      // bits.  Finite up to g = -88.7; beyond, s is 0 and e held finite, so that e s is 0
+      // and no NaN, and so are all three factors (below 2^-119 there)
       const float e = __builtin_amdgcn_exp2f(g[i] * -1.4426950408889634f);
       const float s = __builtin_amdgcn_rcpf(1.0f + e);
       const float gs = g[i] * s;
       h[i] = gs * u[i];
       du[i] = v[i] * gs;
-      dg[i] = v[i] * u[i] * fmaf(gs, fminf(e, 0x1p100f) * s, s);
+      dg[i] = v[i] * u[i] * fmaf(gs, fminf(e, 0x1.fffffep127f) * s, s);
     }
     put_row<DT>(a.out, at, dg);
     put_row<DT>(a.out, at + a.N, du);

@@ -576,9 +576,11 @@ int moe_fp8_expert_ffn(const moe_fp8_weights* W, const uint16_t* x, int T, int K
  *   dx = dg W_gate + du W_up, dw_gu = [dg du]^T x, dw_dn = dy^T h
  *   dy, x, dx [T][H], gu [T][2I] as kept, dw_gu and dw_dn like the weights
  *
- * Sums and the activation are f32; h, dg and du are rounded to dtype as the next
- * product's operands, every output once.  A NaN or an infinity in a row of x (of dy)
- * reaches that row of y (of dx) alone, and every weight gradient.
+ * Sums and the activation are f32 (silu and its slopes may be zero where they are
+ * below 2^-119, from g = -87.3 down); h, dg and du are rounded to dtype as the next
+ * product's operands (one past f16's range becomes infinite), every output once.  A
+ * NaN or an infinity in a row of x (of dy) reaches that row of y (of dx) alone, and
+ * every weight gradient.
  *
  *   ws  at least moe_dense_ffn_workspace_bytes(T, H, I), or ..._grad_...(T, H, I)
  *
