@@ -736,6 +736,14 @@ PyObject* grad_clip(Args a) {
       list[i].out = o.data_ptr();
     }
   }
+  // every block reads the norm while others write
+  const uintptr_t at = (uintptr_t)norm.data_ptr();
+  for (size_t i = 0; i < list.size(); ++i) {
+    const uintptr_t from = (uintptr_t)list[i].out;
+    const uintptr_t to = from + (uintptr_t)list[i].n * (list[i].dtype == MOE_DT_F32 ? 4 : 2);
+    if (from < to && from < at + sizeof(float) && at < to)
+      refuse(outs == Py_None ? "grads[" : "out[", i, "] holds the norm, which the call reads while it writes");
+  }
   check(call(moe_grad_clip, list.data(), (int)list.size(), norm.data_ptr<float>(), max_norm, stream()));
   Py_RETURN_NONE;
 }

@@ -659,10 +659,12 @@ int moe_int8_linear(const moe_int8_matrix* M, const void* x, int T, int dtype, i
  * determine, so the norm is infinite only if it passes float32's range itself, or
  * a value is; moe_grad_clip works in f32 and rounds once.
  *
- *   ws  at least moe_grad_norm_workspace_bytes(count) bytes, aligned to 8
+ *   ws  at least moe_grad_norm_workspace_bytes(count) bytes, aligned to 8, apart from
+ *       the list's tensors
  *
  * Limits: 1 <= count <= 2^20, 0 <= n <= 2^37, max_norm finite and >= 0.  No output
- * may overlap another tensor of the list (refused).
+ * may overlap another tensor of the list (refused) or the norm, which every block reads
+ * while others write (refused by the Python entry point).
  */
 typedef struct moe_grad_tensor {
   const void* grad;
