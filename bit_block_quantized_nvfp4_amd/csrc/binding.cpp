@@ -660,18 +660,20 @@ PyObject* int8_linear(Args a) {
   return wrap(out);
 }
 
-// A list or tuple of tensors, held while it lives.
+// The tensors of a list or tuple, each held while it lives: a list can lose them to other
+// Python code, on a thread that runs while a launch waits or in a dispatch mode.
 struct TensorList {
-  PyObject* seq;
-  TensorList(PyObject* o, const char* name) : seq(o) {
+  PyObject* held;
+  TensorList(PyObject* o, const char* name) {
     if (!PyList_Check(o) && !PyTuple_Check(o)) refuse(name, " must be a list or tuple of tensors");
-    Py_INCREF(seq);
+    held = PyList_Check(o) ? PyList_AsTuple(o) : Py_NewRef(o);
+    if (!held) throw Raised{};
   }
   TensorList(const TensorList&) = delete;
-  ~TensorList() { Py_DECREF(seq); }
-  Py_ssize_t size() const { return PySequence_Fast_GET_SIZE(seq); }
+  ~TensorList() { Py_DECREF(held); }
+  Py_ssize_t size() const { return PyTuple_GET_SIZE(held); }
   const Tensor& at(Py_ssize_t i, const char* name) const {
-    PyObject* o = PySequence_Fast_GET_ITEM(seq, i);
+    PyObject* o = PyTuple_GET_ITEM(held, i);
     if (!THPVariable_Check(o)) refuse(name, "[", i, "] must be a tensor");
     return THPVariable_Unpack(o);
   }
@@ -719,6 +721,7 @@ PyObject* grad_clip(Args a) {
   const Tensor& norm = a.tensor("norm");
   const float max_norm = a.number();
   PyObject* const outs = a.next();
+  const TensorList out(outs == Py_None ? grads.held : outs, "out");
   const c10::Device dev = device_of_list(grads, "grads");
   const OnDevice on(dev);
   std::vector<moe_grad_tensor> list = grad_list(grads, dev);
@@ -726,7 +729,6 @@ PyObject* grad_clip(Args a) {
   if (outs == Py_None) {
     for (moe_grad_tensor& g : list) g.out = (void*)g.grad;
   } else {
-    const TensorList out(outs, "out");
     if (out.size() != grads.size()) refuse("out has ", out.size(), " tensors, grads has ", grads.size());
     for (Py_ssize_t i = 0; i < out.size(); ++i) {
       const Tensor &g = grads.at(i, "grads"), &o = out.at(i, "out");
@@ -745,7 +747,7 @@ PyObject* grad_clip(Args a) {
       refuse(outs == Py_None ? "grads[" : "out[", i, "] holds the norm, which the call reads while it writes");
   }
   check(call(moe_grad_clip, list.data(), (int)list.size(), norm.data_ptr<float>(), max_norm, stream()));
-  Py_RETURN_NONE;
+  return PySequence_List(out.held);
 }
 
 // C++ errors end here: none passes into the interpreter.

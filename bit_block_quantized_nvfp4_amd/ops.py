@@ -575,8 +575,7 @@ def moe_grad_clip(grads: Sequence[torch.Tensor], norm: torch.Tensor, max_norm: f
     """Every gradient times min(1, max_norm / (norm + 1e-6)), in place or into the
     tensors of out.  norm is moe_grad_norm's, or one joined over processes; it may not
     stand in a tensor that is written.  Returns the scaled tensors."""
-    _lib.binding().grad_clip(grads, norm, max_norm, out)
-    return list(grads if out is None else out)
+    return _lib.binding().grad_clip(grads, norm, max_norm, out)
 
 
 def timing_enable(on: bool = True) -> None:
