@@ -86,6 +86,12 @@ struct TileArgs16 {
 };
 
 constexpr int SB = 128;  // bytes of a step along K, of each row
+// Steps along K of values of es bytes.  K is the rows' number for the weights' gradients:
+// up to 2^30, whose bytes pass an int.
+constexpr long steps_of(int K, int es) { return ((long)K * es + SB - 1) / SB; }
+static_assert(steps_of(1 << 30, 2) == 1 << 24 && steps_of((1 << 30) - 63, 2) == 1 << 24 &&
+                  steps_of((1 << 30) - 64, 2) == (1 << 24) - 1 && steps_of(8, 2) == 1 && steps_of(65536, 1) == 512,
+              "steps at the limits");
 constexpr uint32_t kNowhere = 0x80000000u;  // past the end of every buffer (all below 2^31 bytes)
 
 // Permutation of the 16-byte chunks of a line: rows fastest, a line of CPR chunks.
@@ -253,7 +259,7 @@ __device__ __forceinline__ void tile_block(const TileArgs16& a, const int blk, c
   oa.set(a.a, a.lda, m0, a.M - m0, a.K, 0, tid);
   lds_u8* const l0 = lds + kg * kLds;
   const uint32_t ldsw = (uint32_t)(uintptr_t)l0 + wv * 1024;
-  const int steps = ((a.K * ES + SB - 1) / SB + KG - 1) / KG;  // of a group
+  const int steps = (int)((steps_of(a.K, ES) + KG - 1) / KG);  // of a group
 
   // Step s's turn at the buffers that step s - 1 leaves: the loads of A's step s - 1 + NA,
   // then of B's step s - 1 + NB.  Steps past the last one are brought too, as zeros
@@ -452,7 +458,7 @@ static void by_shape(int shape, F&& f) {
   if (shape == 7) f(TileShape<64, 32, 1, 1, 3, 3, 4>{});
 }
 
-// Tiles of a product in a shape, and steps along K.
+// Tiles of a product in a shape.
 static inline long tiles_of(int shape, int M, int cols) {
   long n = 0;
   by_shape(shape, [&](auto s) {
@@ -460,7 +466,6 @@ static inline long tiles_of(int shape, int M, int cols) {
   });
   return n;
 }
-static inline long steps_of(int K, int es) { return ((long)K * es + SB - 1) / SB; }
 
 // Time of a round of tiles on the chip, in 10 ns, beyond the launch's 2.5 us: `fixed1` +
 // steps * `step1` with one block on each compute unit, the first of them; `fixed` + steps *
