@@ -1,6 +1,6 @@
 """The dense block in every shape of its tiles and streams, forward (projections kept or
-not) and backward, on whole numbers: every sum is exact, and one lost or repeated term
-shows.
+not) and backward, and its weight gradients over more rows than 2^31 elements hold: on whole
+numbers, where every sum is exact and one lost or repeated term shows.
 
 test_tile_choice.py holds that FORWARD and GRADIENTS below take all the shapes."""
 import pytest
@@ -61,3 +61,37 @@ def test_forward_of_whole_numbers_is_exact(moe, T, H, I, dtype, keep):
 def test_gradients_of_whole_numbers_are_exact(moe, T, H, I, dtype):
     flush(f"dense gradients of whole numbers T={T} H={H} I={I} {dtype}")
     base.test_gradients_of_whole_numbers_are_exact(moe, T, H, I, dtype)
+
+
+def test_weight_gradients_past_32_bits(moe):
+    """T 2I > 2^31: every row counts in dw_gu and dw_dn, and every row of dx."""
+    T, H, I, dtype, step = 140_000, 64, 8192, torch.bfloat16, 20_000
+    flush("dense gradients of whole numbers past 32 bits")
+    gen = torch.Generator(device="cuda").manual_seed(3)
+
+    def whole(lo, hi, shape):
+        return torch.randint(lo, hi + 1, shape, generator=gen, device="cuda", dtype=torch.int8).to(dtype)
+
+    x, W, Wd = whole(-1, 1, (T, H)), whole(-1, 1, (2 * I, H)), whole(-1, 1, (H, I))
+    gu = torch.empty(T, 2 * I, dtype=dtype, device="cuda")
+    gu[:, :I] = 32  # silu is the identity
+    gu[:, I:] = whole(-2, 2, (T, I))
+    dy = torch.zeros(T, H, dtype=dtype, device="cuda")  # one or two places a row: |dh| <= 2
+    at = torch.arange(T, device="cuda")
+    for sign in (1, -1):
+        dy[at, torch.randint(0, H, (T,), generator=gen, device="cuda")] = sign
+    dx, dw_gu, dw_dn = moe.moe_dense_ffn_grad(moe.DenseWeights(W, Wd), dy, x, gu)
+    want_gu = torch.zeros(2 * I, H, dtype=torch.float64, device="cuda")
+    want_dn = torch.zeros(H, I, dtype=torch.float64, device="cuda")
+    for a in range(0, T, step):
+        rows = slice(a, a + step)
+        dyr, u = dy[rows].double(), gu[rows, I:].double()
+        dh = dyr @ Wd.double()
+        dgu = torch.cat([dh * u, dh * 32], 1)
+        ref = dgu @ W.double()
+        assert float(ref.abs().max()) < 2 ** 24
+        assert torch.equal(dx[rows], ref.float().to(dtype)), f"dx from row {a}"
+        want_gu += dgu.t() @ x[rows].double()
+        want_dn += dyr.t() @ (32 * u)
+    # |terms| <= 64: no sum, finished or not, passes 64 T < 2^24
+    assert torch.equal(dw_gu, want_gu.float().to(dtype)) and torch.equal(dw_dn, want_dn.float().to(dtype))
