@@ -655,9 +655,10 @@ int moe_int8_linear(const moe_int8_matrix* M, const void* x, int T, int dtype, i
  * `out`, which may be `grad` itself (scaled in place).  Tensors may be empty and need
  * no alignment beyond their type's (both sides of one alike is faster).  norm: one
  * float32 on the device; a norm joined over several processes serves moe_grad_clip
- * as well.  The squares are summed in 64 bits in an order that the sizes alone
- * determine, so the norm is infinite only if it passes float32's range itself, or
- * a value is; moe_grad_clip works in f32 and rounds once.
+ * as well.  The squares are summed in 64 bits, so the norm is infinite only if it
+ * passes float32's range itself, or a value is; in an order that the tensors' sizes,
+ * types and addresses modulo 16 determine, so that a call repeats itself to the bit.
+ * moe_grad_clip works in f32 and rounds once.
  *
  *   ws  at least moe_grad_norm_workspace_bytes(count) bytes, aligned to 8, apart from
  *       the list's tensors
