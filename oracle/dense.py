@@ -3,9 +3,6 @@ infrastructure only).
 
   g = x Wg^T, u = x Wu^T, h = silu(g) u, y = h Wd^T
 
-`magnitudes` functions evaluate the same sums with every term's absolute value, the
-scale of their f32 error.
-
 Pins: the gradients against central differences of the forward function.
 """
 from __future__ import annotations
