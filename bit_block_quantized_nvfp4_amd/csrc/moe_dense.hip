@@ -8,9 +8,9 @@
 // rows' type for that, as every operand of a 16-bit product is; all sums and the
 // activation are in f32.
 //
-// 8192 rows, H = 2048, I = 8192, bf16: 506 us (with the projections kept, whose 403 MB the
-// epilogue writes) and 219 us; 333 rows, 2056, 1032, f16: 11 and 7.4 us, by latency; 1 row, 2048,
-// 8192: 12.6 and 8.0 us, the weights from memory at 5.3 and 4.2 TB/s.
+// 8192 rows, H = 2048, I = 8192, bf16: 471 us (with the projections kept, whose 403 MB the
+// epilogue writes) and 205 us, one after the other; 333 rows, 2056, 1032, f16: 13.3 and 7.8 us, by
+// latency; 1 row, 2048, 8192: 13.4 and 8.5 us, the weights from memory at 5.0 and 3.9 TB/s.
 #include "moe_dense.hpp"
 #include "moe_stream.hpp"
 

@@ -8,9 +8,9 @@
 // projections and makes h again.  h, dg and du are operands of the next products and
 // rounded to the rows' type for that; all sums and the activation's gradient are in f32.
 //
-// 8192 rows, H = 2048, I = 8192, bf16: dh 370 to 387 us, of which its epilogue takes about 150 to
-// move 670 MB, the other three 1040 to 1056 us (1.30 PFLOP/s, the matrix unit at the clock
-// that the power allows); 133 rows, 1032, 520, f16: 8 and 10 us, by latency.
+// 8192 rows, H = 2048, I = 8192, bf16: dh 379 us, of which its epilogue takes about 150 to move
+// 670 MB, the other three 999 us (1.38 PFLOP/s); 133 rows, 1032, 520, f16: 8.9 and 10.5 us, by
+// latency.
 #include "moe_dense.hpp"
 
 namespace moe {

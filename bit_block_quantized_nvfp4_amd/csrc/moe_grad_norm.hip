@@ -7,9 +7,9 @@
 // types: their table travels with the launch (nothing of it stands in device
 // memory, so a captured graph keeps its own), each tensor is cut into pieces,
 // and the blocks take the pieces in turn.  The scaling takes them from the last to the
-// first: what the norm read last is still in the last-level cache.  120 MB take 19.4 us for the
-// squares (6.2 TB/s), 4 to join them and 36.3 for the scaling (6.5 TB/s); a few small
-// tensors 4 and 3 us, the length of two launches.
+// first: what the norm read last is still in the last-level cache.  120 MB take 19.6 us for the
+// squares (6.1 TB/s), 4.6 to join them and 36.8 for the scaling (6.5 TB/s); a few small
+// tensors 4.3 and 3.4 us, the length of two launches.
 //
 // The squares and their sums are held in 64 bits: f32 squares would pass its range
 // from values of 1.8e19 on, and the conversion is free beside the loads.
@@ -271,7 +271,8 @@ hipError_t launch_grad_norm(const moe_grad_tensor* g, int count, float* norm, do
 
 // Outputs go past the last-level cache where they and the gradients would fill most of its
 // 256 MB: the gradients that the norm read last then stay for the scaling (norm and
-// scaling of 120 MB 78 us with ordinary stores, 65 so; of 2.4 GB 1355 and 1308 us).
+// scaling of 120 MB beside the gradients 78 us with ordinary stores, 61 so; of 2.4 GB 1355 and 1313
+// us).
 constexpr int64_t kFarBytes = (int64_t)192 << 20;
 
 hipError_t launch_grad_clip(const moe_grad_tensor* g, int count, const float* norm, float max_norm,

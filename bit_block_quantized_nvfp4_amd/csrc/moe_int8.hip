@@ -6,9 +6,10 @@
 // and, gated, silu of the first half of the columns times the second.  The sums are
 // exact in 32-bit integers: |sum| <= 127 128 K < 2^31 for K <= 65536.
 //
-// bf16 rows: 8192 x 2048 x 8192 35 us of quantisation and 123 us (2.2 POP/s); gated, 8192 x 16384 x
-// 2048, 13 and 270 to 298 us, where a tile's 16 steps are followed by as many values of silu;
-// f16 333 x 4168 x 2064 3.5 and 10.5 us, by latency; 1 row of 4096 x 4096 7.2 us in one launch.
+// bf16 rows: 8192 x 2048 x 8192 37.7 us of quantisation and 116.6 us (2.36 POP/s); gated, 8192 x
+// 16384 x 2048, 14.6 and 275 us, where a tile's 16 steps are followed by as many values of silu and
+// the columns' scales are read in every pass of the epilogue; f16 333 x 4168 x 2064 4.2 and 11.4 us,
+// by latency; 1 row of 4096 x 4096 8.2 us in one launch.
 #include "moe_int8.hpp"
 #include "moe_stream.hpp"
 #include "moe_tile.hpp"
@@ -98,8 +99,18 @@ hipError_t launch_int8_quant(const void* x, int T, int K, int dtype, int8_t* cod
 }
 
 // Up to 16 rows stream the weights.  Where the rows are few values they are quantised in
-// the same launch, which every block repeats (2048 x 2048, us: 1 row 5.4, else 3.4 and a
-// launch of 3.5; 8 rows 9.8 and 3.7); else in one of their own.  The shapes: f with the
+// the same launch, which every block repeats; else in one of their own, which costs a call
+// outside a graph one more launch.  bf16, weights from memory, in a row in a graph, us, apart
+// and joined:
+//   N x K, plain     1 row        4 rows       8 rows       N x K, gated    1 row        4 rows
+//   512 x 2048       5.8  5.4     6.1  7.5     6.3   9.8    512 x 2048      6.8  5.9     7.0  7.5
+//   2048 x 2048      5.9  5.6     6.2  7.7     6.5  10.0    2048 x 2048     7.0  6.0     7.2  7.7
+//   2048 x 4096      8.1  7.1     8.7  9.0                  8192 x 2048     9.4  8.7     9.7  10.8
+//   8192 x 2048      9.2  9.3     9.7  11.6    10.1 14.0    16384 x 2048   11.1  10.9   11.4  12.8
+//   8192 x 4096     11.7 13.3    12.4  15.9                 16384 x 4096   18.8  21.0   18.9  23.9
+//   8192 x 8192     19.9 26.8                               8192 x 8192    18.1  20.0
+// So joining wins in a graph for one row and up to about 4096 outputs (gated more), and loses
+// from two rows on, though the rule goes by the rows' values alone.  The shapes: f with the
 // kernel, outputs and threads of a block.
 static bool int8_streams(int T) { return T <= kStreamRows; }
 static bool int8_joins(int T, int K) { return T <= 4 && (long)T * K <= 8192; }

@@ -4,17 +4,20 @@
 //   z[m][n] = sum_k x[m][k] W[n][k],   out = epilogue(z),
 //
 // bound by the bytes of W.  A wave owns RT tiles of 16 weight rows (gated: a gate tile and
-// the up tile of the same outputs) and every KW-th piece of 128 bytes along K; it has U
-// pieces of each on their way while it multiplies the U before.  The KW waves of a tile
-// join through LDS in wave order.  16 rows are one MFMA operand whatever their number.
+// the up tile of the same outputs) and every KW-th piece of 128 bytes along K; it asks for U
+// pieces of each before it multiplies the U before.  It does not multiply beside them: loads
+// complete in order, and those of x's operand come behind them, so that its wait for the one
+// is a wait for the others; what hides the latency is the other waves.  The KW waves of a
+// tile join through LDS in wave order.  16 rows are one MFMA operand whatever their number.
 //
 // HALF, for up to 8 rows: a tile is 8 weight rows, the operands' upper halves are the same
 // rows at the next piece, and the product's two diagonal quarters are added in the end.
 // Twice the blocks, for matrices whose tiles of 16 would leave compute units idle.
 //
 // 8-bit integers: with XDT a row type the rows are quantised on the way.  Each block then
-// reads all rows once for their largest magnitudes, which saves a launch where they are
-// few (moe_int8.hip); otherwise x holds codes and sm their scales.
+// reads all rows once for their largest magnitudes, behind the first pieces of the weights,
+// and again for their codes, which saves a launch where they are few (moe_int8.hip);
+// otherwise x holds codes and sm their scales.
 #pragma once
 
 #include "moe_int8.hpp"
@@ -31,6 +34,13 @@ constexpr int kStreamRows = 16;
 //   2048 x 2048      4.9   4.3                                  2048    7.7   5.8
 //   2048 x 8192     13.0   9.7                                  4096   11.2   8.4
 //   4096 x 2048      5.6   5.5  (8 rows 6.3, 6.8)
+// 8-bit integers in the same way, each with a launch of about 2 us for the rows' codes:
+//   1024 x 512       4.9   4.9  (8 rows 5.3, 5.5)               1024    6.9   7.0
+//   1024 x 2048      6.5   5.9                                  2048    7.5   7.5
+//   2048 x 2048      6.6   6.0  (8 rows 7.3, 6.5)               4096    8.3   9.5
+//   2048 x 8192     11.8  10.3  (8 rows 13.1, 12.0)             4096, K = 8192  20.9  18.0
+//   4096 x 2048      7.2   7.3  (8 rows 8.0, 8.3)               8192   11.4  14.5
+// where gated HALF wins for long K alone (2048 outputs, K = 8192: 17.0 and 13.3).
 constexpr bool takes_half(int rows, int outputs, bool gated) { return rows <= 8 && outputs <= (gated ? 4096 : 2048); }
 
 // One product of 128 bytes along K: lane l holds chunks l / 16 and l / 16 + 4 of row l % 16,

@@ -22,10 +22,10 @@
 // the end of K by an offset past it, for both operands, so that nothing that
 // stands behind a row (a NaN of the next one) is multiplied.
 //
-// Large products are bound by the matrix unit at the clock that the card's power allows
-// (79 % of its cycles busy; MFMAs alone reach 1.7 PFLOP/s, 8192 x 2048 x 8192 in bf16 takes
-// 202 to 219 us, 1.25 to 1.35; in 8-bit integers 123 us, 2.2 POP/s): a wave of 128 x 128 reads
-// the fewest bytes from LDS for its products.  Small ones are bound by the latency of their
+// Large products keep the matrix unit busy 79 % of its cycles, at a clock that falls as it
+// fills (MFMAs alone reach 1.7 PFLOP/s; 8192 x 2048 x 8192 in bf16 takes 205 us, 1.34, where
+// the library's product takes 170; in 8-bit integers 117 us, 2.36 POP/s): a wave of 128 x 128
+// reads the fewest bytes from LDS for its products.  Small ones are bound by the latency of their
 // steps, 0.3 to 0.45 us each: hence the deep rings and the groups along K.
 #pragma once
 
