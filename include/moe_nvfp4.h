@@ -616,9 +616,9 @@ int moe_dense_ffn_grad(const moe_dense_weights* W, const void* dy, const void* x
  * moe_int8_quant writes the codes [T][K] and scales [T] of rows x.
  *
  * moe_int8_linear: z[t][n] = (s[t] sum_k code_x[t][k] codes[n][k]) scales[n], exact
- * integer sums, then each step rounded to f32; gated 0: out = z, [T][N]; gated 1: rows 0..N/2-1 are a
- * gate, the others its up projection, out[t][n] = silu(z[t][n]) z[t][N/2 + n],
- * [T][N/2].  One rounding to dtype.
+ * integer sums, then each step rounded to f32; gated 0: out = z, [T][N]; gated 1: rows
+ * 0..N/2-1 are a gate, the others its up projection, out[t][n] = silu(z[t][n])
+ * z[t][N/2 + n], [T][N/2].  One rounding to dtype.
  *
  *   x [T][K], out of dtype
  *   ws  at least moe_int8_linear_workspace_bytes(T, N, K) bytes
